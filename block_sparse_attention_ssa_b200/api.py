@@ -64,6 +64,27 @@ class ssa_tensor_t(ctypes.Structure):
                 ("stride_h", ctypes.c_int64), ("stride_n", ctypes.c_int64)]
 
 
+class ssa_window_dims_t(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("N", ctypes.c_int32), ("d", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("sinks", ctypes.c_int32), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+    @property
+    def torch_dtype(self) -> torch.dtype:
+        return _TORCH_DTYPES[self.dtype]
+
+
+class ssa_paged_dims_t(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("total_q", ctypes.c_int32), ("Hq", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("sinks", ctypes.c_int32), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+    @property
+    def torch_dtype(self) -> torch.dtype:
+        return _TORCH_DTYPES[self.dtype]
+
+
 _P = ctypes.POINTER
 _SIGS = {
     "ssa_version": (ctypes.c_int, []),
@@ -102,6 +123,15 @@ _SIGS = {
     "ssa_device_status": (ctypes.c_int, [_P(ctypes.c_int32), ctypes.c_int, ctypes.c_void_p]),
     "ssa_launch_count": (ctypes.c_uint64, []),
     "ssa_selftest_timeout": (ctypes.c_int, [ctypes.c_void_p]),
+    "ssa_window_workspace_bytes": (ctypes.c_size_t, [_P(ssa_window_dims_t)]),
+    "ssa_fwd_window": (ctypes.c_int, [_P(ssa_window_dims_t)] + [_P(ssa_tensor_t)] * 4 + [ctypes.c_void_p] * 2),
+    "ssa_bwd_window": (ctypes.c_int, [_P(ssa_window_dims_t)] + [_P(ssa_tensor_t)] * 4 + [ctypes.c_void_p]
+                       + [_P(ssa_tensor_t)] * 4 + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "ssa_paged_workspace_bytes": (ctypes.c_size_t, [_P(ssa_paged_dims_t)]),
+    "ssa_paged_append": (ctypes.c_int, [_P(ssa_paged_dims_t)] + [_P(ssa_tensor_t)] * 2 + [ctypes.c_void_p] * 3
+                         + [_P(ssa_tensor_t)] * 2 + [ctypes.c_void_p]),
+    "ssa_paged_attention": (ctypes.c_int, [_P(ssa_paged_dims_t)] + [_P(ssa_tensor_t)] * 3 + [ctypes.c_void_p] * 3
+                            + [_P(ssa_tensor_t), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "ssa_block_scores_noalloc": (ctypes.c_int, [_P(ssa_dims_t), _P(ssa_tensor_t), _P(ssa_tensor_t),
                                                  ctypes.c_void_p, ctypes.c_void_p]),
 }
@@ -244,6 +274,132 @@ def ssa_align_mse(dims, h_full, h_sparse, loss, ws, stream=None) -> None:
         _stream(stream)))
 
 
+# ---------------------------------------------------------------- window attention, paged cache
+# These entry points check shapes, types and devices here, where the tensors are
+# still known, and enqueue on the tensors' own device (its current stream unless
+# one is given).
+
+EVERYTHING = 2**31 - 1  # a window that hides nothing
+
+
+def make_window_dims(B: int, Hq: int, Hkv: int, N: int, d: int, window: int | None = None, sinks: int = 0,
+                     dtype: str = "bf16", scale: float | None = None) -> ssa_window_dims_t:
+    """Token t attends the last `window` tokens (None: all earlier ones) and the first `sinks` tokens."""
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    return ssa_window_dims_t(B, Hq, Hkv, N, d, EVERYTHING if window is None else window, sinks, float(scale),
+                             _DTYPES[dtype])
+
+
+def make_paged_dims(num_seqs: int, total_q: int, Hq: int, Hkv: int, d: int, page: int, num_pages: int, max_pages: int,
+                    window: int | None = None, sinks: int = 0, dtype: str = "bf16",
+                    scale: float | None = None) -> ssa_paged_dims_t:
+    """A ragged batch of num_seqs sequences with total_q new tokens over caches of num_pages pages of `page` tokens."""
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    return ssa_paged_dims_t(num_seqs, total_q, Hq, Hkv, d, page, num_pages, max_pages,
+                            EVERYTHING if window is None else window, sinks, float(scale), _DTYPES[dtype])
+
+
+def _like(name: str, x: torch.Tensor, shape: tuple, dtype: torch.dtype, device: torch.device, dense: bool = False) -> None:
+    if tuple(x.shape) != shape or x.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype} {shape}, got {x.dtype} {tuple(x.shape)}")
+    if x.device != device or device.type != "cuda":
+        raise ValueError(f"{name}: expected a tensor on one CUDA device ({device}), got {x.device}")
+    if dense and not x.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+
+
+def _bhnd(x: torch.Tensor) -> ctypes._Pointer:
+    """ssa_tensor_t of a [B, H, N, d] view; dimensions of length one get a stride that fits."""
+    sb, sh, sn, sd = x.stride()
+    if sd != 1:
+        raise ValueError("expected a contiguous last dimension")
+    d = x.shape[3]
+    return ctypes.pointer(ssa_tensor_t(x.data_ptr(), sb if x.shape[0] > 1 else d, sh if x.shape[1] > 1 else d,
+                                       sn if x.shape[2] > 1 else d))
+
+
+def _call(fn: str, device: torch.device, *args, stream=None) -> None:
+    if device.index is None or device.index == torch.cuda.current_device():
+        _check(fn, getattr(load_library(), fn)(*args, _stream(stream)))
+        return
+    with torch.cuda.device(device):
+        _check(fn, getattr(load_library(), fn)(*args, _stream(stream)))
+
+
+def _bytes(ws: torch.Tensor, device: torch.device) -> tuple[ctypes.c_void_p, int]:
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError("ws: expected a contiguous tensor on the inputs' device")
+    return ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size()
+
+
+def ssa_window_workspace_bytes(dims: ssa_window_dims_t) -> int:
+    return int(load_library().ssa_window_workspace_bytes(ctypes.byref(dims)))
+
+
+def ssa_paged_workspace_bytes(dims: ssa_paged_dims_t) -> int:
+    return int(load_library().ssa_paged_workspace_bytes(ctypes.byref(dims)))
+
+
+def ssa_fwd_window(dims, Q, K, V, h, lse, stream=None) -> None:
+    """Window attention with sinks: Q, h [B, Hq, N, d], K, V [B, Hkv, N, d], lse [B, Hq, N] fp32."""
+    dt, dev = dims.torch_dtype, Q.device
+    q, kv = (dims.B, dims.Hq, dims.N, dims.d), (dims.B, dims.Hkv, dims.N, dims.d)
+    for name, x, shape in (("Q", Q, q), ("K", K, kv), ("V", V, kv), ("h", h, q)):
+        _like(name, x, shape, dt, dev)
+    _like("lse", lse, q[:3], torch.float32, dev, dense=True)
+    _call("ssa_fwd_window", dev, ctypes.byref(dims), _bhnd(Q), _bhnd(K), _bhnd(V), _bhnd(h), _p(lse), stream=stream)
+
+
+def ssa_bwd_window(dims, Q, K, V, h, lse, g, dQ, dK, dV, ws, stream=None) -> None:
+    """Gradients of <g, h> for what ssa_fwd_window computed."""
+    dt, dev = dims.torch_dtype, Q.device
+    q, kv = (dims.B, dims.Hq, dims.N, dims.d), (dims.B, dims.Hkv, dims.N, dims.d)
+    for name, x, shape in (("Q", Q, q), ("K", K, kv), ("V", V, kv), ("h", h, q), ("g", g, q), ("dQ", dQ, q),
+                           ("dK", dK, kv), ("dV", dV, kv)):
+        _like(name, x, shape, dt, dev)
+    _like("lse", lse, q[:3], torch.float32, dev, dense=True)
+    _call("ssa_bwd_window", dev, ctypes.byref(dims), _bhnd(Q), _bhnd(K), _bhnd(V), _bhnd(h), _p(lse), _bhnd(g),
+          _bhnd(dQ), _bhnd(dK), _bhnd(dV), *_bytes(ws, dev), stream=stream)
+
+
+def _packed(name: str, x: torch.Tensor, dims, heads: int, dev) -> ctypes._Pointer:
+    """[total_q, heads, d] rows as the C ABI's packed [1, heads, total_q, d]."""
+    _like(name, x, (dims.total_q, heads, dims.d), dims.torch_dtype, dev)
+    return _bhnd(x.transpose(0, 1).unsqueeze(0))
+
+
+def _cache(name: str, x: torch.Tensor, dims, dev) -> ctypes._Pointer:
+    """A [num_pages, page, Hkv, d] cache (any strides) as the C ABI's [num_pages, Hkv, page, d]."""
+    _like(name, x, (dims.num_pages, dims.page, dims.Hkv, dims.d), dims.torch_dtype, dev)
+    return _bhnd(x.transpose(1, 2))
+
+
+def _batch(q_start, kv_len, page_table, dims, dev) -> tuple:
+    _like("q_start", q_start, (dims.num_seqs + 1,), torch.int32, dev, dense=True)
+    _like("kv_len", kv_len, (dims.num_seqs,), torch.int32, dev, dense=True)
+    _like("page_table", page_table, (dims.num_seqs, dims.max_pages), torch.int32, dev, dense=True)
+    return _p(q_start), _p(kv_len), _p(page_table)
+
+
+def ssa_paged_append(dims, k, v, q_start, kv_len, page_table, K, V, stream=None) -> None:
+    """Writes the new rows k, v [total_q, Hkv, d] into the caches K, V [num_pages, page, Hkv, d]."""
+    dev = k.device
+    _call("ssa_paged_append", dev, ctypes.byref(dims), _packed("k", k, dims, dims.Hkv, dev),
+          _packed("v", v, dims, dims.Hkv, dev), *_batch(q_start, kv_len, page_table, dims, dev),
+          _cache("K", K, dims, dev), _cache("V", V, dims, dev), stream=stream)
+
+
+def ssa_paged_attention(dims, q, K, V, q_start, kv_len, page_table, h, lse, ws, stream=None) -> None:
+    """Attention of the new rows q [total_q, Hq, d] over the caches: h [total_q, Hq, d], lse [Hq, total_q] fp32."""
+    dev = q.device
+    _like("lse", lse, (dims.Hq, dims.total_q), torch.float32, dev, dense=True)
+    _call("ssa_paged_attention", dev, ctypes.byref(dims), _packed("q", q, dims, dims.Hq, dev),
+          _cache("K", K, dims, dev), _cache("V", V, dims, dev), *_batch(q_start, kv_len, page_table, dims, dev),
+          _packed("h", h, dims, dims.Hq, dev), _p(lse), *_bytes(ws, dev), stream=stream)
+
+
 def ssa_launch_count() -> int:
     return int(load_library().ssa_launch_count())
 
@@ -301,6 +457,37 @@ def alloc_decode(dims: ssa_dims_t, device="cuda") -> dict[str, torch.Tensor]:
         "lse": torch.empty((B, Hq), dtype=torch.float32, device=device),
         "idx": torch.empty((B, Hq, k), dtype=torch.int32, device=device),
     }
+
+
+def alloc_window_forward(dims: ssa_window_dims_t, device="cuda") -> dict[str, torch.Tensor]:
+    return {
+        "h": torch.empty((dims.B, dims.Hq, dims.N, dims.d), dtype=dims.torch_dtype, device=device),
+        "lse": torch.empty((dims.B, dims.Hq, dims.N), dtype=torch.float32, device=device),
+    }
+
+
+def alloc_window_backward(dims: ssa_window_dims_t, device="cuda") -> dict[str, torch.Tensor]:
+    dt = dims.torch_dtype
+    return {
+        "dQ": torch.empty((dims.B, dims.Hq, dims.N, dims.d), dtype=dt, device=device),
+        "dK": torch.empty((dims.B, dims.Hkv, dims.N, dims.d), dtype=dt, device=device),
+        "dV": torch.empty((dims.B, dims.Hkv, dims.N, dims.d), dtype=dt, device=device),
+    }
+
+
+def alloc_window_workspace(dims: ssa_window_dims_t, device="cuda") -> torch.Tensor:
+    return torch.empty(max(ssa_window_workspace_bytes(dims), 256), dtype=torch.uint8, device=device)
+
+
+def alloc_paged(dims: ssa_paged_dims_t, device="cuda") -> dict[str, torch.Tensor]:
+    return {
+        "h": torch.empty((dims.total_q, dims.Hq, dims.d), dtype=dims.torch_dtype, device=device),
+        "lse": torch.empty((dims.Hq, dims.total_q), dtype=torch.float32, device=device),
+    }
+
+
+def alloc_paged_workspace(dims: ssa_paged_dims_t, device="cuda") -> torch.Tensor:
+    return torch.empty(max(ssa_paged_workspace_bytes(dims), 256), dtype=torch.uint8, device=device)
 
 
 def forward(dims, Q, K, V, out, ws, stream=None) -> dict[str, torch.Tensor]:

@@ -1,0 +1,156 @@
+// The paged cache's writer, and the join of attention partials.
+#include "win_common.cuh"
+
+namespace ssa {
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+// The sequence that holds packed row `row` (its first row at most `row`, the next
+// sequence's above it): -1 for rows behind the last one.
+__device__ __forceinline__ int seq_of_row(const int32_t* q_start, int seqs, int row) {
+  int lo = 0, hi = seqs;  // q_start[lo] <= row < q_start[hi] once both ends hold
+  if (row < q_start[0] || row >= q_start[seqs]) return -1;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (q_start[mid] <= row) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Append: one pass over the new rows in 16-byte pieces.  A CTA takes ROWS packed tokens
+// (all kv heads); a thread finds a token's page row once, then the CTA copies.  Bound by
+// memory (or by the launch, for single tokens): 4 row lengths of traffic a token and head.
+constexpr int AROWS = 8;
+__global__ void __launch_bounds__(256) paged_append_kernel(PagedArgs a, PagedDims D, int vecs, int es) {
+  __shared__ int64_t page_of[AROWS];
+  __shared__ int slot_of[AROWS];
+  const int row0 = blockIdx.x * AROWS;
+  if (threadIdx.x < AROWS) {
+    const int row = row0 + threadIdx.x;
+    int64_t pg = -1;
+    int slot = 0;
+    if (row < D.T) {
+      const int b = seq_of_row(a.q_start, D.seqs, row);
+      if (b >= 0) {
+        const Seq s = load_seq(a.q_start, a.kv_len, b, D.T, D.max_pages * D.page);
+        const int pos = s.len - s.n + (row - s.q0);
+        if (pos >= 0 && row - s.q0 < s.n) {
+          const int id = a.table[(int64_t)b * D.max_pages + pos / D.page];
+          if ((unsigned)id < (unsigned)D.num_pages) {
+            pg = id;
+            slot = pos % D.page;
+          }
+        }
+      }
+    }
+    page_of[threadIdx.x] = pg;
+    slot_of[threadIdx.x] = slot;
+  }
+  __syncthreads();
+  const int per_row = D.Hkv * vecs;
+  for (int e = threadIdx.x; e < AROWS * per_row; e += 256) {
+    const int r = e / per_row, h = e % per_row / vecs, c = e % vecs;
+    const int64_t pg = page_of[r];
+    if (pg < 0) continue;
+    const int64_t row = row0 + r;
+    auto piece = [&](const TensorRef& t, int64_t b, int64_t n) {
+      return const_cast<uint4*>(reinterpret_cast<const uint4*>(static_cast<const char*>(t.p) + (b * t.sb + h * t.sh + n * t.sn) * es)) + c;
+    };
+    const uint4 k = *piece(a.nk, 0, row), v = *piece(a.nv, 0, row);
+    *piece(a.k, pg, slot_of[r]) = k;
+    *piece(a.v, pg, slot_of[r]) = v;
+  }
+}
+
+// Join: CTA (c, y) looks whether the last item of attention CTA c is cut there and
+// begins there; if so it adds that item's partials in CTA order,
+//   m = max m_i, h = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i, a warp per row.
+template <typename T, int HD, int KT, int ROWS>
+__global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, Batch batch, int T_, int g, int ctas, int min_units) {
+  __shared__ Place sh;
+  __shared__ long long sh_unit[3];
+  if (threadIdx.x < 32) {
+    const long long U = batch.total<KT>();
+    const long long per = share(U, ctas, min_units);
+    const long long u0 = per * blockIdx.x, u1 = min(u0 + per, U);
+    Place at{batch.seqs, 0, 0, 0};
+    if (u0 < U) at = batch.locate<KT>(u1 - 1);
+    if (threadIdx.x == 0) {
+      sh = at;
+      sh_unit[0] = u0;
+      sh_unit[1] = u1;
+      sh_unit[2] = per;
+    }
+  }
+  __syncthreads();
+  const Place at = sh;
+  if (at.b >= batch.seqs) return;
+  const long long u0 = sh_unit[0], u1 = sh_unit[1], per = sh_unit[2];
+  const long long begin = u1 - 1 - at.off;
+  const Seq s = load_seq(batch.q_start, batch.kv_len, at.b, T_, batch.cap);
+  const int i0 = at.run * batch.TI;
+  const int units = max(1, run_tiles<KT>(s, i0, batch.TI, batch.window, batch.sinks).count);
+  if (begin < u0 || begin + units <= u1) return;  // begun before, or complete
+  const int parts = 1 + (int)((begin + units - u1 + per - 1) / per);
+  const int nrows = min(batch.TI, s.n - i0) * g;
+  const size_t psz = partial_floats(ROWS, HD);
+  const float* part = static_cast<const float*>(a.ws);
+  auto slot = [&](int i) { return part + psz * (i == 0 ? 2 * blockIdx.x + (begin == u0 ? 0 : 1) : 2 * (blockIdx.x + i)); };
+  const int lane = threadIdx.x & 31;
+  constexpr int V = HD / 32;
+  for (int r = blockIdx.y + gridDim.y * (threadIdx.x >> 5); r < nrows; r += gridDim.y * 8) {
+    float m = kNegInf;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, slot(i)[ROWS * HD + r]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float ref = m == kNegInf ? 0.f : m;
+    float l = 0.f, o[V];
+#pragma unroll
+    for (int c = 0; c < V; ++c) o[c] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+      const float* q = slot(i);
+      const float f = exp2f(q[ROWS * HD + r] - ref);
+      l = fmaf(f, q[ROWS * HD + ROWS + r], l);
+#pragma unroll
+      for (int c = 0; c < V; ++c) o[c] = fmaf(f, q[r * HD + lane * V + c], o[c]);
+    }
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    const int h = at.kvh * g + r % g, row = s.q0 + i0 + r / g;
+    T* dst = row_ptr_w<T>(a.h, 0, h, row) + lane * V;
+#pragma unroll
+    for (int c = 0; c < V; ++c) dst[c] = from_f32<T>(o[c] * inv);
+    if (lane == 0) a.lse[(int64_t)h * T_ + row] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const PagedDims& D, const PagedArgs& a, cudaStream_t st) {
+  const int es = D.dtype == SSA_BF16 ? 2 : 4;
+  paged_append_kernel<<<(D.T + AROWS - 1) / AROWS, 256, 0, st>>>(a, D, D.d * es / 16, es);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+template <int KT, int ROWS>
+cudaError_t launch_paged_join(const PagedDims& D, const PagedArgs& a, int ctas, int TI, int min_units, cudaStream_t st) {
+  const Batch batch{a.q_start, a.kv_len, D.seqs, D.T, D.max_pages * D.page, TI, D.window, D.sinks, D.Hkv};
+  const dim3 grid(ctas, 4);
+  if (D.dtype == SSA_BF16) {
+    if (D.d == 64)
+      paged_join_kernel<__nv_bfloat16, 64, KT, ROWS><<<grid, 256, 0, st>>>(a, batch, D.T, D.g, ctas, min_units);
+    else
+      paged_join_kernel<__nv_bfloat16, 128, KT, ROWS><<<grid, 256, 0, st>>>(a, batch, D.T, D.g, ctas, min_units);
+  } else if (D.d == 64) {
+    paged_join_kernel<float, 64, KT, ROWS><<<grid, 256, 0, st>>>(a, batch, D.T, D.g, ctas, min_units);
+  } else {
+    paged_join_kernel<float, 128, KT, ROWS><<<grid, 256, 0, st>>>(a, batch, D.T, D.g, ctas, min_units);
+  }
+  count_launches(1);
+  return cudaGetLastError();
+}
+template cudaError_t launch_paged_join<64, 64>(const PagedDims&, const PagedArgs&, int, int, int, cudaStream_t);
+
+}  // namespace ssa

@@ -1,0 +1,716 @@
+// Window attention with sinks and paged attention on CUDA cores.
+//
+// Mathematics: the online softmax over the visible keys (base 2, scale folded in)
+// and, backward, p = 2^(x c - lse2), dx = p (g.v - D), dQ = scale dx K,
+// dK = scale dx^T Q, dV = p^T g.  fp32 arithmetic throughout, because no tensor-core
+// input type holds fp32 values.
+//
+// Tiles: 64 queries by 64 keys, 256 threads, thread (tx, ty) owns queries 4 ty .. and
+// keys tx + 16 j: a step of four head dims is 8 16-byte shared loads (12 wavefronts) for
+// 64 multiply-adds a thread, so the FMA pipe, not shared memory, sets the pace.
+#include "win_common.cuh"
+
+namespace ssa {
+namespace {
+
+constexpr int BT = 64;
+constexpr int NT_ = 256;
+constexpr int SP = BT + 4;  // row pitch of the P tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// CTAs of one paged call, a multiple of the SMs; units are worth a CTA from two on.
+constexpr int kPagedCtas = 296;
+constexpr int kMinUnits = 2;
+
+template <int HD>
+struct Pitch {
+  static constexpr int v = HD + 4;
+};
+
+struct SimtParams {
+  TensorRef q, k, v, h;
+  float* lse;
+  int Hq, g, N, window, sinks, NT;
+  float c;
+  // paged
+  const int32_t* table;
+  Batch batch;
+  int page, num_pages, max_pages, T;
+  float* part;
+};
+
+// 64 rows of HD values into shared memory as fp32; a null row pointer gives zeros.
+template <typename T, int HD, typename F>
+__device__ __forceinline__ void load_rows(float* dst, F row) {
+  constexpr int V = Vec16<T>::kN, PER = HD / V;
+  for (int e = threadIdx.x; e < BT * PER; e += NT_) {
+    const int r = e / PER, c = (e % PER) * V;
+    float x[V];
+    const T* p = row(r);
+    if (p != nullptr) {
+      Vec16<T>::load(p + c, x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < V; i += 4)
+      *reinterpret_cast<float4*>(dst + r * Pitch<HD>::v + c + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+  }
+}
+
+// s[i][j] = A[4 ty + i] . B[tx + 16 j]
+template <int HD>
+__device__ __forceinline__ void dots(const float* A, const float* B, int tx, int ty, float (&s)[4][4]) {
+  constexpr int P = Pitch<HD>::v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < HD; k += 4) {
+    float4 a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (4 * ty + i) * P + k);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * P + k);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
+        s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
+        s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
+        s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+      }
+  }
+}
+
+// acc[i][.] += sum_u W[4 ty + i][u] X[u][.]; columns 4 tx + 64 q + 0..3.
+template <int HD>
+__device__ __forceinline__ void weighted(const float* W, const float* X, int tx, int ty, float (&acc)[4][HD / 16]) {
+#pragma unroll 2
+  for (int u = 0; u < BT; u += 4) {
+    float w[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 t = *reinterpret_cast<const float4*>(W + (4 * ty + i) * SP + u);
+      w[i][0] = t.x;
+      w[i][1] = t.y;
+      w[i][2] = t.z;
+      w[i][3] = t.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int q = 0; q < HD / 64; ++q) {
+        const float4 x = *reinterpret_cast<const float4*>(X + (u + e) * Pitch<HD>::v + 64 * q + 4 * tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[i][4 * q] = fmaf(w[i][e], x.x, acc[i][4 * q]);
+          acc[i][4 * q + 1] = fmaf(w[i][e], x.y, acc[i][4 * q + 1]);
+          acc[i][4 * q + 2] = fmaf(w[i][e], x.z, acc[i][4 * q + 2]);
+          acc[i][4 * q + 3] = fmaf(w[i][e], x.w, acc[i][4 * q + 3]);
+        }
+      }
+  }
+}
+
+template <typename T, int HD>
+__device__ __forceinline__ void store_row(T* dst, const float* acc, int tx, float mul) {
+#pragma unroll
+  for (int q = 0; q < HD / 64; ++q)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dst[64 * q + 4 * tx + i] = from_f32<T>(acc[4 * q + i] * mul);
+}
+
+template <int HD>
+constexpr size_t fwd_smem() {
+  return (size_t)(2 * BT * Pitch<HD>::v + BT * SP) * 4;
+}
+
+// ================================================================ forward
+template <typename T, int HD, bool PAGED>
+__global__ void __launch_bounds__(NT_) win_fwd_simt_kernel(SimtParams p) {
+  extern __shared__ float sm[];
+  float* sQ = sm;
+  float* sX = sQ + BT * Pitch<HD>::v;  // K, then V
+  float* sP = sX + BT * Pitch<HD>::v;
+  __shared__ Place sh_place;
+  __shared__ int sh_left;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+
+  Place at{0, 0, 0, 0};
+  int left = 1;
+  if (PAGED) {
+    if (tid < 32) {
+      const long long U = p.batch.total<BT>();
+      const long long per = share(U, (int)gridDim.x, kMinUnits);
+      const long long u0 = per * blockIdx.x;
+      const long long n = u0 < U ? min(per, U - u0) : 0;
+      if (n > 0) at = p.batch.locate<BT>(u0);
+      if (tid == 0) {
+        sh_place = at;
+        sh_left = (int)n;
+      }
+    }
+    __syncthreads();
+    at = sh_place;
+    left = sh_left;
+  }
+
+  for (int seg = 0; left > 0; ++seg) {
+    // ---- the item
+    int b, head0, q0row, kvh, nrows, p0, per_tok, i0 = 0, units, take, len, part_rows = 0;
+    Seq s{};
+    KeyTiles kt;
+    if (PAGED) {
+      b = at.b;
+      s = load_seq(p.batch.q_start, p.batch.kv_len, b, p.T, p.batch.cap);
+      i0 = at.run * p.batch.TI;
+      const int toks = min(p.batch.TI, s.n - i0);
+      kvh = at.kvh;
+      head0 = kvh * p.g;
+      per_tok = p.g;
+      nrows = toks * p.g;
+      q0row = s.q0 + i0;
+      p0 = s.len - s.n + i0;
+      len = s.len;
+      kt = run_tiles<BT>(s, i0, p.batch.TI, p.window, p.sinks);
+      units = max(1, kt.count);
+      take = min(left, units - at.off);
+      part_rows = take < units ? nrows : 0;
+    } else {
+      const int planes = (int)(gridDim.x / p.NT);
+      const int plane = (int)blockIdx.x % planes, qt = p.NT - 1 - (int)blockIdx.x / planes;
+      b = plane / p.Hq;
+      head0 = plane % p.Hq;
+      kvh = head0 / p.g;
+      per_tok = 1;
+      q0row = p0 = qt * BT;
+      nrows = min(BT, p.N - p0);
+      len = p.N;
+      kt = key_tiles<BT>(p0, p0 + nrows - 1, p.window, p.sinks);
+      units = take = kt.count;
+    }
+    auto tok_of = [&](int r) { return PAGED ? r / per_tok : r; };
+    auto head_of = [&](int r) { return PAGED ? head0 + r % per_tok : head0; };
+    load_rows<T, HD>(sQ, [&](int r) -> const T* {
+      return r < nrows ? row_ptr<T>(p.q, PAGED ? 0 : b, head_of(r), q0row + tok_of(r)) : nullptr;
+    });
+
+    float acc[4][HD / 16], m[4], l[4];
+    int pos[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = kNegInf;
+      l[i] = 0.f;
+      pos[i] = 4 * ty + i < nrows ? p0 + tok_of(4 * ty + i) : -1;
+#pragma unroll
+      for (int c = 0; c < HD / 16; ++c) acc[i][c] = 0.f;
+    }
+    const int pmax = p0 + tok_of(nrows - 1), lo_min = p0 - p.window + 1;
+
+    for (int j = at.off; j < at.off + take && j < kt.count; ++j) {
+      const int u0 = kt.tile(j) * BT;
+      // A key that no row of the item sees is not read (its memory may hold anything).
+      auto key_row = [&](const TensorRef& t, int r) -> const T* {
+        const int u = u0 + r;
+        if (u > pmax || u >= len || (u < lo_min && u >= p.sinks)) return nullptr;
+        if (!PAGED) return row_ptr<T>(t, b, kvh, u);
+        const int pg = p.table[(int64_t)b * p.max_pages + u / p.page];
+        return (unsigned)pg < (unsigned)p.num_pages ? row_ptr<T>(t, pg, kvh, u % p.page) : nullptr;
+      };
+      __syncthreads();
+      load_rows<T, HD>(sX, [&](int r) { return key_row(p.k, r); });
+      __syncthreads();
+      float x[4][4];
+      dots<HD>(sQ, sX, tx, ty, x);
+      bool held[4];
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {
+        held[jj] = true;
+        if (PAGED) {
+          const int u = u0 + tx + 16 * jj;
+          held[jj] = u < len && (unsigned)p.table[(int64_t)b * p.max_pages + u / p.page] < (unsigned)p.num_pages;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float mx = kNegInf;
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+          const int u = u0 + tx + 16 * jj;
+          const bool see = held[jj] && u <= pos[i] && (u > pos[i] - p.window || u < p.sinks);
+          x[i][jj] = see ? x[i][jj] * p.c : kNegInf;
+          mx = fmaxf(mx, x[i][jj]);
+        }
+#pragma unroll
+        for (int o = 8; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float mn = fmaxf(m[i], mx);
+        const float ref = mn == kNegInf ? 0.f : mn;
+        const float f = exp2f(m[i] - ref);
+        float sum = 0.f;
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+          const float e = exp2f(x[i][jj] - ref);
+          sum += e;
+          sP[(4 * ty + i) * SP + tx + 16 * jj] = e;
+        }
+#pragma unroll
+        for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        l[i] = l[i] * f + sum;
+        m[i] = mn;
+#pragma unroll
+        for (int c = 0; c < HD / 16; ++c) acc[i][c] *= f;
+      }
+      __syncthreads();
+      load_rows<T, HD>(sX, [&](int r) { return key_row(p.v, r); });
+      __syncthreads();
+      weighted<HD>(sP, sX, tx, ty, acc);
+    }
+
+    // ---- epilogue
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 4 * ty + i;
+      if (r >= nrows) continue;
+      if (PAGED && part_rows) {
+        float* base = p.part + (size_t)(2 * blockIdx.x + (seg ? 1 : 0)) * partial_floats(BT, HD);
+#pragma unroll
+        for (int q = 0; q < HD / 64; ++q)
+          *reinterpret_cast<float4*>(base + r * HD + 64 * q + 4 * tx) =
+              make_float4(acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]);
+        if (tx == 0) {
+          base[BT * HD + r] = m[i];
+          base[BT * HD + BT + r] = l[i];
+        }
+        continue;
+      }
+      const float inv = l[i] == 0.f ? 0.f : 1.0f / l[i];
+      store_row<T, HD>(row_ptr_w<T>(p.h, PAGED ? 0 : b, head_of(r), q0row + tok_of(r)), acc[i], tx, inv);
+      if (tx == 0) {
+        const int64_t o = PAGED ? (int64_t)head_of(r) * p.T + q0row + tok_of(r)
+                                : ((int64_t)b * p.Hq + head0) * p.N + q0row + r;
+        p.lse[o] = l[i] == 0.f ? kNegInf : (m[i] + log2f(l[i])) * kLn2;
+      }
+    }
+    if (!PAGED) break;
+    // ---- the next item
+    left -= take;
+    if (left <= 0) break;
+    at.off = 0;
+    if (++at.kvh == p.batch.Hkv) {
+      at.kvh = 0;
+      ++at.run;
+      while (at.b < p.batch.seqs) {
+        s = load_seq(p.batch.q_start, p.batch.kv_len, at.b, p.T, p.batch.cap);
+        if (at.run * p.batch.TI < s.n) break;
+        at.run = 0;
+        ++at.b;
+      }
+      if (at.b >= p.batch.seqs) break;
+    }
+    __syncthreads();  // sQ, sX and sP are read to the end
+  }
+}
+
+// ================================================================ backward
+// D_t = g_t . h_t and lse in base 2, one warp per row, rows padded to 128 tokens.
+template <typename T, int HD>
+__global__ void __launch_bounds__(256) win_bwd_pre_kernel(TensorRef h, TensorRef g, const float* lse, float* lse2,
+                                                          float* dsum, int Hq, int N, int Npad, int64_t rows) {
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  const int64_t bh = row / Npad;
+  const int t = (int)(row % Npad), b = (int)(bh / Hq), hd = (int)(bh % Hq);
+  float s = 0.f, ls = __builtin_huge_valf();  // 2^(x - inf) = 0 in the padding
+  if (t < N) {
+    constexpr int V = Vec16<T>::kN;
+    const T* hp = row_ptr<T>(h, b, hd, t);
+    const T* gp = row_ptr<T>(g, b, hd, t);
+    for (int c = lane * V; c < HD; c += 32 * V) {
+      float x[V], y[V];
+      Vec16<T>::load(hp + c, x);
+      Vec16<T>::load(gp + c, y);
+#pragma unroll
+      for (int i = 0; i < V; ++i) s = fmaf(x[i], y[i], s);
+    }
+    ls = lse[bh * N + t] * kLog2e;
+    if (ls == kNegInf) ls = __builtin_huge_valf();
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) {
+    lse2[row] = ls;
+    dsum[row] = s;
+  }
+}
+
+struct SimtBwd {
+  TensorRef q, k, v, g, dq, dk, dv;
+  const float* lse2;
+  const float* dsum;
+  float* part;
+  int Hq, Hkv, grp, N, Npad, window, sinks, NT, L, partials;
+  float c, scale;
+};
+
+template <int HD>
+constexpr size_t bwd_smem() {
+  return (size_t)(4 * BT * Pitch<HD>::v + BT * SP) * 4;
+}
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(NT_) win_bwd_dq_simt_kernel(SimtBwd p) {
+  extern __shared__ float sm[];
+  float* sQ = sm;
+  float* sG = sQ + BT * Pitch<HD>::v;
+  float* sK = sG + BT * Pitch<HD>::v;
+  float* sV = sK + BT * Pitch<HD>::v;
+  float* sS = sV + BT * Pitch<HD>::v;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int planes = (int)(gridDim.x / p.NT);
+  const int plane = (int)blockIdx.x % planes, qt = p.NT - 1 - (int)blockIdx.x / planes;
+  const int b = plane / p.Hq, h = plane % p.Hq, kvh = h / p.grp;
+  const int q0 = qt * BT, nrows = min(BT, p.N - q0);
+  const KeyTiles kt = key_tiles<BT>(q0, q0 + nrows - 1, p.window, p.sinks);
+  load_rows<T, HD>(sQ, [&](int r) -> const T* { return r < nrows ? row_ptr<T>(p.q, b, h, q0 + r) : nullptr; });
+  load_rows<T, HD>(sG, [&](int r) -> const T* { return r < nrows ? row_ptr<T>(p.g, b, h, q0 + r) : nullptr; });
+  float ls[4], ds[4], acc[4][HD / 16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t o = ((int64_t)b * p.Hq + h) * p.Npad + q0 + 4 * ty + i;
+    ls[i] = p.lse2[o];
+    ds[i] = p.dsum[o];
+#pragma unroll
+    for (int c = 0; c < HD / 16; ++c) acc[i][c] = 0.f;
+  }
+  for (int j = 0; j < kt.count; ++j) {
+    const int u0 = kt.tile(j) * BT;
+    __syncthreads();
+    load_rows<T, HD>(sK, [&](int r) -> const T* { return u0 + r < p.N ? row_ptr<T>(p.k, b, kvh, u0 + r) : nullptr; });
+    load_rows<T, HD>(sV, [&](int r) -> const T* { return u0 + r < p.N ? row_ptr<T>(p.v, b, kvh, u0 + r) : nullptr; });
+    __syncthreads();
+    float x[4][4], y[4][4];
+    dots<HD>(sQ, sK, tx, ty, x);
+    dots<HD>(sG, sV, tx, ty, y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {
+        const int u = u0 + tx + 16 * jj, t = q0 + 4 * ty + i;
+        const bool see = u <= t && (t - u < p.window || u < p.sinks);
+        sS[(4 * ty + i) * SP + tx + 16 * jj] = see ? exp2f(fmaf(x[i][jj], p.c, -ls[i])) * (y[i][jj] - ds[i]) : 0.f;
+      }
+    __syncthreads();
+    weighted<HD>(sS, sK, tx, ty, acc);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (4 * ty + i < nrows) store_row<T, HD>(row_ptr_w<T>(p.dq, b, h, q0 + 4 * ty + i), acc[i], tx, p.scale);
+}
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(NT_) win_bwd_dkv_simt_kernel(SimtBwd p) {
+  extern __shared__ float sm[];
+  float* sK = sm;
+  float* sV = sK + BT * Pitch<HD>::v;
+  float* sQ = sV + BT * Pitch<HD>::v;
+  float* sG = sQ + BT * Pitch<HD>::v;
+  float* sS = sG + BT * Pitch<HD>::v;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int planes = p.Hkv * (int)gridDim.y;
+  const int plane = (int)blockIdx.x % p.Hkv + (int)blockIdx.y * p.Hkv;
+  const Chunk ch = find_chunk<BT>((int)blockIdx.x / p.Hkv, p.NT, p.L, p.grp, p.N, p.window, p.sinks);
+  const int b = plane / p.Hkv, kvh = plane % p.Hkv;
+  const int u0 = ch.kt * BT, nq = query_tiles_of<BT>(ch.kt, p.N, p.window, p.sinks);
+  const int first = ch.idx * p.L, last = min(first + p.L, nq * p.grp);
+  load_rows<T, HD>(sK, [&](int r) -> const T* { return u0 + r < p.N ? row_ptr<T>(p.k, b, kvh, u0 + r) : nullptr; });
+  load_rows<T, HD>(sV, [&](int r) -> const T* { return u0 + r < p.N ? row_ptr<T>(p.v, b, kvh, u0 + r) : nullptr; });
+  float dk[4][HD / 16], dv[4][HD / 16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int c = 0; c < HD / 16; ++c) dk[i][c] = dv[i][c] = 0.f;
+  for (int st = first; st < last; ++st) {
+    const int h = kvh * p.grp + st / nq, q0 = (ch.kt + st % nq) * BT;
+    __syncthreads();
+    load_rows<T, HD>(sQ, [&](int r) -> const T* { return q0 + r < p.N ? row_ptr<T>(p.q, b, h, q0 + r) : nullptr; });
+    load_rows<T, HD>(sG, [&](int r) -> const T* { return q0 + r < p.N ? row_ptr<T>(p.g, b, h, q0 + r) : nullptr; });
+    float ls[4], ds[4];
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj) {
+      const int64_t o = ((int64_t)b * p.Hq + h) * p.Npad + q0 + tx + 16 * jj;
+      ls[jj] = p.lse2[o];
+      ds[jj] = p.dsum[o];
+    }
+    __syncthreads();
+    float x[4][4], y[4][4];
+    dots<HD>(sK, sQ, tx, ty, x);
+    dots<HD>(sV, sG, tx, ty, y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {
+        const int u = u0 + 4 * ty + i, t = q0 + tx + 16 * jj;
+        const bool see = u <= t && (t - u < p.window || u < p.sinks);
+        const float pv = see ? exp2f(fmaf(x[i][jj], p.c, -ls[jj])) : 0.f;
+        sS[(4 * ty + i) * SP + tx + 16 * jj] = pv;
+        y[i][jj] = see ? pv * (y[i][jj] - ds[jj]) : 0.f;
+      }
+    __syncthreads();
+    weighted<HD>(sS, sG, tx, ty, dv);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) sS[(4 * ty + i) * SP + tx + 16 * jj] = y[i][jj];
+    __syncthreads();
+    weighted<HD>(sS, sQ, tx, ty, dk);
+  }
+  (void)planes;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int u = u0 + 4 * ty + i;
+    if (u >= p.N) continue;
+    if (ch.n == 1) {
+      store_row<T, HD>(row_ptr_w<T>(p.dk, b, kvh, u), dk[i], tx, p.scale);
+      store_row<T, HD>(row_ptr_w<T>(p.dv, b, kvh, u), dv[i], tx, 1.0f);
+    } else {
+      float* base = p.part + ((size_t)plane * p.partials + ch.slot + ch.idx) * (2 * BT * HD) + (4 * ty + i) * HD;
+#pragma unroll
+      for (int q = 0; q < HD / 64; ++q) {
+        *reinterpret_cast<float4*>(base + 64 * q + 4 * tx) =
+            make_float4(dk[i][4 * q], dk[i][4 * q + 1], dk[i][4 * q + 2], dk[i][4 * q + 3]);
+        *reinterpret_cast<float4*>(base + BT * HD + 64 * q + 4 * tx) =
+            make_float4(dv[i][4 * q], dv[i][4 * q + 1], dv[i][4 * q + 2], dv[i][4 * q + 3]);
+      }
+    }
+  }
+}
+
+// Joins the chunks of one key tile in order: grid (key tiles, planes).
+template <typename T, int HD, int BTJ>
+__global__ void __launch_bounds__(256)
+    win_kvjoin_kernel(const float* part, TensorRef dk, TensorRef dv, int Hkv, int grp, int N, int NT, int L,
+                      int partials, int window, int sinks, float scale) {
+  const int kt = blockIdx.x, plane = blockIdx.y, b = plane / Hkv, kvh = plane % Hkv;
+  auto chunks_of = [&](int k) {
+    return (int)(((long long)query_tiles_of<BTJ>(k, N, window, sinks) * grp + L - 1) / L);
+  };
+  const int n = chunks_of(kt);
+  if (n == 1) return;
+  __shared__ int slot_sh;
+  if (threadIdx.x < 32) {
+    int s = 0;
+    for (int k = threadIdx.x; k < kt; k += 32) {
+      const int c = chunks_of(k);
+      s += c > 1 ? c : 0;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (threadIdx.x == 0) slot_sh = s;
+  }
+  __syncthreads();
+  const float* base = part + ((size_t)plane * partials + slot_sh) * (2 * BTJ * HD);
+  // blockIdx.z cuts the tile's rows
+  const int rows = BTJ / gridDim.z, r0 = blockIdx.z * rows;
+  for (int e = threadIdx.x; e < rows * HD / 4; e += 256) {
+    const int r = r0 + e / (HD / 4), c = (e % (HD / 4)) * 4, u = kt * BTJ + r;
+    if (u >= N) continue;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), v = a;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float* q = base + (size_t)i * (2 * BTJ * HD) + r * HD + c;
+      const float4 x = *reinterpret_cast<const float4*>(q), y = *reinterpret_cast<const float4*>(q + BTJ * HD);
+      a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+      v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+    }
+    T* ok = row_ptr_w<T>(dk, b, kvh, u) + c;
+    T* ov = row_ptr_w<T>(dv, b, kvh, u) + c;
+    ok[0] = from_f32<T>(a.x * scale);
+    ok[1] = from_f32<T>(a.y * scale);
+    ok[2] = from_f32<T>(a.z * scale);
+    ok[3] = from_f32<T>(a.w * scale);
+    ov[0] = from_f32<T>(v.x);
+    ov[1] = from_f32<T>(v.y);
+    ov[2] = from_f32<T>(v.z);
+    ov[3] = from_f32<T>(v.w);
+  }
+}
+
+template <typename K>
+cudaError_t set_smem(K kern, size_t bytes) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <typename T, int HD>
+cudaError_t fwd_t(const WinDims& D, const WinFwdArgs& a, cudaStream_t st) {
+  SimtParams p{};
+  p.q = a.q;
+  p.k = a.k;
+  p.v = a.v;
+  p.h = a.h;
+  p.lse = a.lse;
+  p.Hq = D.Hq;
+  p.g = D.g;
+  p.N = D.N;
+  p.window = D.window;
+  p.sinks = D.sinks;
+  p.NT = (D.N + BT - 1) / BT;
+  p.c = D.scale * kLog2e;
+  auto kern = win_fwd_simt_kernel<T, HD, false>;
+  cudaError_t e = set_smem(kern, fwd_smem<HD>());
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)((int64_t)p.NT * D.B * D.Hq), NT_, fwd_smem<HD>(), st>>>(p);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+template <typename T, int HD>
+cudaError_t bwd_t(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
+  cudaError_t e = launch_win_bwd_pre(D, a, st);
+  if (e != cudaSuccess) return e;
+  const WinBwdLayout L = win_bwd_layout(D);
+  const ChunkPlan cp = chunk_plan<BT>(D, kPagedCtas);
+  char* ws = static_cast<char*>(a.ws);
+  SimtBwd p{};
+  p.q = a.q;
+  p.k = a.k;
+  p.v = a.v;
+  p.g = a.g;
+  p.dq = a.dq;
+  p.dk = a.dk;
+  p.dv = a.dv;
+  p.lse2 = reinterpret_cast<const float*>(ws + L.lse2);
+  p.dsum = reinterpret_cast<const float*>(ws + L.dsum);
+  p.part = reinterpret_cast<float*>(ws + L.part);
+  p.Hq = D.Hq;
+  p.Hkv = D.Hkv;
+  p.grp = D.g;
+  p.N = D.N;
+  p.Npad = L.Npad;
+  p.window = D.window;
+  p.sinks = D.sinks;
+  p.NT = cp.NT;
+  p.L = cp.L;
+  p.partials = cp.partials;
+  p.c = D.scale * kLog2e;
+  p.scale = D.scale;
+  auto dkv = win_bwd_dkv_simt_kernel<T, HD>;
+  if ((e = set_smem(dkv, bwd_smem<HD>())) != cudaSuccess) return e;
+  dkv<<<dim3(cp.chunks * D.Hkv, D.B), NT_, bwd_smem<HD>(), st>>>(p);
+  count_launches(1);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_win_kvjoin<BT>(D, a, cp, p.part, st)) != cudaSuccess) return e;
+  auto dq = win_bwd_dq_simt_kernel<T, HD>;
+  if ((e = set_smem(dq, bwd_smem<HD>())) != cudaSuccess) return e;
+  dq<<<(unsigned)((int64_t)cp.NT * D.B * D.Hq), NT_, bwd_smem<HD>(), st>>>(p);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+template <typename T, int HD>
+cudaError_t pre_t(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
+  const WinBwdLayout L = win_bwd_layout(D);
+  char* ws = static_cast<char*>(a.ws);
+  const int64_t rows = (int64_t)D.B * D.Hq * L.Npad;
+  win_bwd_pre_kernel<T, HD><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(
+      a.h, a.g, a.lse, reinterpret_cast<float*>(ws + L.lse2), reinterpret_cast<float*>(ws + L.dsum), D.Hq, D.N, L.Npad,
+      rows);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+template <typename T, int HD, int BTJ>
+cudaError_t join_t(const WinDims& D, const WinBwdArgs& a, const ChunkPlan& p, const float* part, cudaStream_t st) {
+  win_kvjoin_kernel<T, HD, BTJ><<<dim3(p.NT, D.B * D.Hkv, 8), 256, 0, st>>>(
+      part, a.dk, a.dv, D.Hkv, D.g, D.N, p.NT, p.L, p.partials, D.window, D.sinks, D.scale);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+template <typename T, int HD>
+cudaError_t paged_t(const PagedDims& D, const PagedArgs& a, cudaStream_t st) {
+  SimtParams p{};
+  p.q = a.q;
+  p.k = a.k;
+  p.v = a.v;
+  p.h = a.h;
+  p.lse = a.lse;
+  p.Hq = D.Hq;
+  p.g = D.g;
+  p.window = D.window;
+  p.sinks = D.sinks;
+  p.c = D.scale * kLog2e;
+  p.table = a.table;
+  p.page = D.page;
+  p.num_pages = D.num_pages;
+  p.max_pages = D.max_pages;
+  p.T = D.T;
+  const int TI = BT / D.g;
+  p.batch = Batch{a.q_start, a.kv_len, D.seqs, D.T, D.max_pages * D.page, TI, D.window, D.sinks, D.Hkv};
+  p.part = static_cast<float*>(a.ws);
+  auto kern = win_fwd_simt_kernel<T, HD, true>;
+  cudaError_t e = set_smem(kern, fwd_smem<HD>());
+  if (e != cudaSuccess) return e;
+  kern<<<kPagedCtas, NT_, fwd_smem<HD>(), st>>>(p);
+  count_launches(1);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_paged_join<BT, BT>(D, a, kPagedCtas, TI, kMinUnits, st);
+}
+
+}  // namespace
+
+// One of the four (type, head dim) instances.
+#define SSA_BY_TYPE(D, F, ...)                                                             \
+  ((D).dtype == SSA_BF16 ? ((D).d == 64 ? F<__nv_bfloat16, 64>(__VA_ARGS__) : F<__nv_bfloat16, 128>(__VA_ARGS__)) \
+                         : ((D).d == 64 ? F<float, 64>(__VA_ARGS__) : F<float, 128>(__VA_ARGS__)))
+
+cudaError_t launch_win_fwd_simt(const WinDims& D, const WinFwdArgs& a, cudaStream_t st) {
+  return SSA_BY_TYPE(D, fwd_t, D, a, st);
+}
+cudaError_t launch_win_bwd_pre(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
+  return SSA_BY_TYPE(D, pre_t, D, a, st);
+}
+cudaError_t launch_win_bwd_simt(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
+  return SSA_BY_TYPE(D, bwd_t, D, a, st);
+}
+cudaError_t launch_paged_simt(const PagedDims& D, const PagedArgs& a, cudaStream_t st) {
+  return SSA_BY_TYPE(D, paged_t, D, a, st);
+}
+
+template <int BTJ>
+cudaError_t launch_win_kvjoin(const WinDims& D, const WinBwdArgs& a, const ChunkPlan& p, const float* part,
+                              cudaStream_t st) {
+  if (p.partials == 0) return cudaSuccess;
+  if (D.dtype == SSA_BF16)
+    return D.d == 64 ? join_t<__nv_bfloat16, 64, BTJ>(D, a, p, part, st) : join_t<__nv_bfloat16, 128, BTJ>(D, a, p, part, st);
+  return D.d == 64 ? join_t<float, 64, BTJ>(D, a, p, part, st) : join_t<float, 128, BTJ>(D, a, p, part, st);
+}
+template cudaError_t launch_win_kvjoin<64>(const WinDims&, const WinBwdArgs&, const ChunkPlan&, const float*, cudaStream_t);
+
+WinBwdLayout win_bwd_layout(const WinDims& D) {
+  WinBwdLayout L{};
+  L.Npad = (D.N + 127) / 128 * 128;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t rows = (size_t)D.B * D.Hq * L.Npad;
+  size_t o = 0;
+  L.lse2 = o;
+  o = up(o + rows * 4);
+  L.dsum = o;
+  o = up(o + rows * 4);
+  L.part = o;
+  const ChunkPlan p = chunk_plan<BT>(D, kPagedCtas);
+  o = up(o + (size_t)D.B * D.Hkv * p.partials * 2 * BT * D.d * 4);
+  L.bytes = o;
+  return L;
+}
+
+size_t paged_ws_bytes(const PagedDims& D) {
+  return ((size_t)2 * kPagedCtas * partial_floats(BT, D.d) * 4 + 255) / 256 * 256;
+}
+
+}  // namespace ssa

@@ -5,21 +5,11 @@
 #include <mutex>
 
 #include <cudaTypedefs.h>
-#include <nvtx3/nvToolsExt.h>
 
+#include "nvtx_range.h"
 #include "ssa_internal.cuh"
 
 namespace ssa {
-
-// One NVTX range per entry-point call, named after the call, so a profiler
-// timeline (nsys, ncu --nvtx) shows which call enqueued which kernels.
-// Header-only NVTX 3: without an attached tool the push / pop are no-ops.
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
 
 static std::atomic<uint64_t> g_launches{0};
 void count_launches(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_relaxed); }
@@ -152,6 +142,10 @@ int32_t* device_status_ptr() {
 }
 
 }  // namespace
+
+ssa_status_t require_sm100() { return check_device(); }
+int32_t* status_word() { return device_status_ptr(); }
+
 }  // namespace ssa
 
 using namespace ssa;

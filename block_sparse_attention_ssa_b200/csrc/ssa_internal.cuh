@@ -111,6 +111,11 @@ __device__ __forceinline__ unsigned long long causal_mask(int t, int u0) {
 // Host-side count of kernels enqueued by this library (ssa_launch_count).
 void count_launches(int n);
 
+// SSA_OK when the current device is an sm_100.
+ssa_status_t require_sm100();
+// The current device's status word (ssa_device_status), or null.
+int32_t* status_word();
+
 // ---------------------------------------------------------------- launchers
 // Each returns the launch status; none synchronises.
 

@@ -1,0 +1,275 @@
+// Shared by the window-attention and paged-cache kernels: validated shapes,
+// which key tiles a run of queries sees, and how a ragged batch is cut into
+// equal shares for the CTAs of one launch.
+#pragma once
+
+#include "ssa_internal.cuh"
+
+namespace ssa {
+
+// Window attention: token t sees u <= t with t - u < window or u < sinks.
+struct WinDims {
+  int B, Hq, Hkv, N, d, g, window, sinks;  // window and sinks at most N
+  float scale;
+  int dtype;
+};
+
+struct WinFwdArgs {
+  TensorRef q, k, v, h;
+  float* lse;
+};
+
+struct WinBwdArgs {
+  TensorRef q, k, v, h, g, dq, dk, dv;
+  const float* lse;
+  void* ws;
+};
+
+// Serving from a paged cache.
+struct PagedDims {
+  int seqs, T, Hq, Hkv, d, g, page, num_pages, max_pages, window, sinks;
+  float scale;
+  int dtype;
+};
+
+struct PagedArgs {
+  TensorRef q, k, v, h;  // q, h packed [1, Hq, T, d]; k, v caches [num_pages, Hkv, page, d]
+  TensorRef nk, nv;      // append: packed [1, Hkv, T, d]
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* table;
+  float* lse;
+  void* ws;
+};
+
+// ---------------------------------------------------------------- key tiles of a run of queries
+// The tiles of KT keys that queries at positions pmin..pmax see: the sink tiles
+// 0..ns-1, then tiles lo..hi of the window (sink tiles that the window reaches
+// count as window tiles).
+struct KeyTiles {
+  int ns, lo, count;
+  __host__ __device__ int tile(int j) const { return j < ns ? j : lo + (j - ns); }
+};
+
+template <int KT>
+__host__ __device__ __forceinline__ KeyTiles key_tiles(int pmin, int pmax, int window, int sinks) {
+  KeyTiles k{0, 0, 0};
+  if (pmax < 0) return k;
+  const int first = pmin - window + 1;  // no overflow: pmin > -2^30, window < 2^31
+  k.lo = first > 0 ? first / KT : 0;
+  const int s = sinks < pmax + 1 ? sinks : pmax + 1;
+  k.ns = (s + KT - 1) / KT;
+  if (k.ns > k.lo) k.ns = k.lo;
+  k.count = k.ns + pmax / KT - k.lo + 1;
+  return k;
+}
+
+// ---------------------------------------------------------------- shares of a ragged batch
+// Work items of one paged call: (sequence b, run of TI new tokens, kv head).
+// An item is as many units as its queries see key tiles (one, to write its empty
+// rows, where they see none).  Units are numbered with the kv heads innermost, then
+// the runs, then the sequences; CTA c takes units [c*per, (c+1)*per), so that one
+// long sequence is spread over every SM and many short ones share them evenly.
+// At most the first and the last item of a CTA are cut; their rows go to partials
+// that a second kernel joins in order.
+struct Seq {
+  int q0, n, len;  // first packed row, new tokens, tokens in the cache
+};
+
+__device__ __forceinline__ Seq load_seq(const int32_t* q_start, const int32_t* kv_len, int b, int T, int cap) {
+  Seq s;
+  // Two neighbours read the same clamped running maximum only through q_start
+  // itself: a decreasing pair gives an empty sequence.
+  const int a = min(max(q_start[b], 0), T), e = min(max(q_start[b + 1], 0), T);
+  s.q0 = a;
+  s.n = max(e - a, 0);
+  s.len = min(max(kv_len[b], 0), cap);
+  return s;
+}
+
+template <int KT>
+__device__ __forceinline__ KeyTiles run_tiles(const Seq& s, int i0, int TI, int window, int sinks) {
+  const int p0 = s.len - s.n + i0;
+  return key_tiles<KT>(p0, p0 + min(TI, s.n - i0) - 1, window, sinks);
+}
+
+template <int KT>
+__device__ __forceinline__ long long seq_units(const Seq& s, int TI, int window, int sinks) {
+  long long u = 0;
+  for (int i0 = 0; i0 < s.n; i0 += TI) u += max(1, run_tiles<KT>(s, i0, TI, window, sinks).count);
+  return u;
+}
+
+struct Place {
+  int b, run, kvh;  // b = seqs: past the end
+  int off;          // unit within the item
+};
+
+// Warp-wide: all 32 lanes call it with the same arguments.
+struct Batch {
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  int seqs, T, cap, TI, window, sinks, Hkv;
+
+  template <int KT>
+  __device__ long long lane_units(int b) const {
+    if (b >= seqs) return 0;
+    const Seq s = load_seq(q_start, kv_len, b, T, cap);
+    return s.n > 0 ? seq_units<KT>(s, TI, window, sinks) * Hkv : 0;
+  }
+
+  template <int KT>
+  __device__ long long total() const {
+    const int lane = threadIdx.x & 31;
+    long long u = 0;
+    for (int b = lane; b < seqs; b += 32) u += lane_units<KT>(b);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+    return u;
+  }
+
+  // The item and offset of unit `at` (0 <= at < total).
+  template <int KT>
+  __device__ Place locate(long long at) const {
+    const int lane = threadIdx.x & 31;
+    long long before = 0;
+    Place p{seqs, 0, 0, 0};
+    for (int b0 = 0; b0 < seqs; b0 += 32) {
+      const long long mine = lane_units<KT>(b0 + lane);
+      long long incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, before + incl > at);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        long long rest = at - (before + __shfl_sync(0xffffffffu, incl - mine, src));
+        p.b = b0 + src;
+        const Seq s = load_seq(q_start, kv_len, p.b, T, cap);
+        for (int i0 = 0; i0 < s.n; i0 += TI) {
+          const int u = max(1, run_tiles<KT>(s, i0, TI, window, sinks).count);
+          if (rest < (long long)u * Hkv) {
+            p.run = i0 / TI;
+            p.kvh = (int)(rest / u);
+            p.off = (int)(rest % u);
+            return p;
+          }
+          rest -= (long long)u * Hkv;
+        }
+        return p;  // not reached
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return p;
+  }
+};
+
+// Units of one CTA's share: at least kMinUnits, so that a small call uses few
+// CTAs and few partials.
+__host__ __device__ __forceinline__ long long share(long long total, int ctas, int min_units) {
+  const long long per = (total + ctas - 1) / ctas;
+  return per > min_units ? per : min_units;
+}
+
+// Partials of one cut item: `rows` accumulators of d floats (not normalised), their
+// maxima (base 2, scaled) and sums.
+__host__ __device__ __forceinline__ size_t partial_floats(int rows, int d) { return (size_t)rows * (d + 2); }
+
+// ---------------------------------------------------------------- backward chunks
+// Steps of key tile kt (tiles of BT tokens): g heads times the query tiles that see
+// it.  A tile with more than L steps is cut into chunks whose fp32 partials a second
+// kernel adds in order (sink tiles are seen by every later token).
+template <int BT>
+__host__ __device__ __forceinline__ int query_tiles_of(int kt, int N, int window, int sinks) {
+  const int NT = (N + BT - 1) / BT;
+  if (kt * BT < sinks) return NT - kt;
+  const int last = (kt * BT + BT - 1 + window - 1) / BT;  // window <= N <= 2^24
+  return (last < NT - 1 ? last : NT - 1) - kt + 1;
+}
+
+struct ChunkPlan {
+  int L, NT, chunks, partials;  // per (batch, kv head)
+};
+
+template <int BT>
+inline ChunkPlan chunk_plan(const WinDims& D, int ctas) {
+  ChunkPlan p{};
+  p.NT = (D.N + BT - 1) / BT;
+  long long steps = 0;
+  for (int kt = 0; kt < p.NT; ++kt) steps += (long long)query_tiles_of<BT>(kt, D.N, D.window, D.sinks) * D.g;
+  const long long all = steps * D.B * D.Hkv;
+  p.L = (int)((all + ctas - 1) / ctas < 8 ? 8 : (all + ctas - 1) / ctas);
+  for (int kt = 0; kt < p.NT; ++kt) {
+    const int n = (int)(((long long)query_tiles_of<BT>(kt, D.N, D.window, D.sinks) * D.g + p.L - 1) / p.L);
+    p.chunks += n;
+    if (n > 1) p.partials += n;
+  }
+  return p;
+}
+
+struct Chunk {
+  int kt, idx, n;  // chunk idx of the n of key tile kt
+  int slot;        // first partial slot of the tile within its plane (n > 1)
+};
+
+// The chunk with number ci of a plane; warp-wide.
+template <int BT>
+__device__ __forceinline__ Chunk find_chunk(int ci, int NT, int L, int g, int N, int window, int sinks) {
+  const int lane = threadIdx.x & 31;
+  int before = 0, slots = 0;
+  Chunk r{0, 0, 1, 0};
+  for (int k0 = 0; k0 < NT; k0 += 32) {
+    const int kt = k0 + lane;
+    const int n = kt < NT ? (int)(((long long)query_tiles_of<BT>(kt, N, window, sinks) * g + L - 1) / L) : 0;
+    const int sl = n > 1 ? n : 0;
+    int incl = n, incs = sl;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o), z = __shfl_up_sync(0xffffffffu, incs, o);
+      if (lane >= o) {
+        incl += y;
+        incs += z;
+      }
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, before + incl > ci);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      r.kt = k0 + src;
+      r.n = __shfl_sync(0xffffffffu, n, src);
+      r.idx = ci - before - __shfl_sync(0xffffffffu, incl - n, src);
+      r.slot = slots + __shfl_sync(0xffffffffu, incs - sl, src);
+      return r;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+    slots += __shfl_sync(0xffffffffu, incs, 31);
+  }
+  return r;
+}
+
+// ---------------------------------------------------------------- launchers
+cudaError_t launch_win_fwd_simt(const WinDims& D, const WinFwdArgs& a, cudaStream_t st);
+
+// Workspace of the backward: lse (base 2) and D_t in rows padded to 128 tokens, then partials.
+struct WinBwdLayout {
+  size_t lse2, dsum, part, bytes;
+  int Npad;
+};
+WinBwdLayout win_bwd_layout(const WinDims& D);
+// Fills lse2 (+infinity in padding rows) and dsum.
+cudaError_t launch_win_bwd_pre(const WinDims& D, const WinBwdArgs& a, cudaStream_t st);
+cudaError_t launch_win_bwd_simt(const WinDims& D, const WinBwdArgs& a, cudaStream_t st);
+// Adds the chunks' partials of key tiles of BT tokens into dK, dV.
+template <int BT>
+cudaError_t launch_win_kvjoin(const WinDims& D, const WinBwdArgs& a, const ChunkPlan& p, const float* part,
+                              cudaStream_t st);
+
+cudaError_t launch_paged_append(const PagedDims& D, const PagedArgs& a, cudaStream_t st);
+size_t paged_ws_bytes(const PagedDims& D);
+cudaError_t launch_paged_simt(const PagedDims& D, const PagedArgs& a, cudaStream_t st);
+// Joins the partials of cut items (ROWS rows of G per token of a run of TI tokens, KT keys per unit).
+template <int KT, int ROWS>
+cudaError_t launch_paged_join(const PagedDims& D, const PagedArgs& a, int ctas, int TI, int min_units, cudaStream_t st);
+
+}  // namespace ssa

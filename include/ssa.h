@@ -361,6 +361,116 @@ SSA_API ssa_status_t ssa_block_scores_noalloc(const ssa_dims_t* dims, const ssa_
                                               const ssa_tensor_t* K, float* scores,
                                               ssa_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Window attention with sinks, training and prompt form
+ * ------------------------------------------------------------------------
+ * The fixed sparse pattern beside the selected one: token t attends
+ *   A_t = {u <= t : t - u < window or u < sinks},
+ * the last `window` tokens (itself among them) and the first `sinks` tokens
+ * of the sequence.  window >= N is causal attention over everything.  Nothing
+ * is selected, so N needs no block: any N >= 0, odd ones too. */
+typedef struct {
+  int32_t B, Hq, Hkv, N, d; /* Hq % Hkv == 0, d in {64, 128}, 0 <= N <= 2^24 */
+  int32_t window;           /* >= 1 */
+  int32_t sinks;            /* >= 0 */
+  float scale;              /* finite, > 0 */
+  int32_t dtype;            /* ssa_dtype_t */
+} ssa_window_dims_t;
+
+/* Bytes of workspace that ssa_bwd_window needs (ssa_fwd_window needs none);
+ * 0 for an invalid or empty shape. */
+SSA_API size_t ssa_window_workspace_bytes(const ssa_window_dims_t* dims);
+
+/* Forward: h_t = softmax over A_t of x_tu applied to V, lse_t its natural-log
+ * normaliser, x_tu = scale * q_t . k_u.
+ *   Q, h [B, Hq, N, d], K, V [B, Hkv, N, d] strided, dims->dtype; lse
+ *     [B, Hq, N] fp32, dense.  Inputs may have zero strides (broadcast
+ *     dimensions); an output row may not be written twice, so h's strides of
+ *     dimensions longer than one are not zero (SSA_ERR_INVALID_ARG).
+ *   A NaN or an infinity in the V row of a token may reach rows of other
+ *     tokens up to 127 positions earlier (a weight of zero times it). */
+SSA_API ssa_status_t ssa_fwd_window(const ssa_window_dims_t* dims, const ssa_tensor_t* Q, const ssa_tensor_t* K,
+                                    const ssa_tensor_t* V, const ssa_tensor_t* h, float* lse,
+                                    ssa_stream_t stream);
+
+/* Backward of <g, h>: with p_tu = exp(x_tu - lse_t) and D_t = g_t . h_t,
+ *   dV_u = sum_t p_tu g_t, dx_tu = p_tu (g_t . v_u - D_t),
+ *   dQ_t = scale sum_u dx_tu k_u, dK_u = scale sum_t dx_tu q_t;
+ * dK and dV are summed over the g query heads of each kv head.  No atomics:
+ * the same inputs give the same bits.
+ *   Q, K, V, h, lse: as passed to / written by ssa_fwd_window.
+ *   g [B, Hq, N, d] dims->dtype (in, required; zero strides are fine).
+ *   dQ [B, Hq, N, d], dK, dV [B, Hkv, N, d] (out): fully overwritten.
+ *   ws: at least ssa_window_workspace_bytes(dims) bytes, 256-byte aligned. */
+SSA_API ssa_status_t ssa_bwd_window(const ssa_window_dims_t* dims, const ssa_tensor_t* Q, const ssa_tensor_t* K,
+                                    const ssa_tensor_t* V, const ssa_tensor_t* h, const float* lse,
+                                    const ssa_tensor_t* g, const ssa_tensor_t* dQ, const ssa_tensor_t* dK,
+                                    const ssa_tensor_t* dV, void* ws, size_t ws_bytes, ssa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Serving from a paged cache
+ * ------------------------------------------------------------------------
+ * A ragged batch of num_seqs sequences.  Sequence b brings
+ *   n_b = q_start[b+1] - q_start[b] >= 0
+ * new tokens, rows q_start[b] .. of the packed tensors; kv_len[b] counts its
+ * tokens in the cache, the new ones included, so that its i-th new token is at
+ * position kv_len[b] - n_b + i.  Position u of sequence b lives in row
+ * u % page of page page_table[b][u / page].  The same window and sinks as
+ * above (window >= kv_len: everything earlier, the full mode).
+ *   q_start [num_seqs + 1], kv_len [num_seqs], page_table [num_seqs,
+ *     max_pages]: int32, dense, on the device.  They are read when the kernels
+ *     run, so a captured graph replays with their current contents.
+ *   K, V caches: [num_pages, Hkv, page, d] strided (stride_b from page to
+ *     page), so that both [num_pages, page, Hkv, d] and [num_pages, Hkv, page,
+ *     d] memory will do.
+ * Values out of range on the device read and write nothing out of range:
+ * q_start is clamped to 0 .. total_q (a decreasing pair is a sequence without
+ * new tokens), kv_len to 0 .. max_pages * page, and a page id outside
+ * 0 .. num_pages - 1 holds no keys (append skips it, attention masks its
+ * positions).  Page ids that no
+ * token sees (behind the window, past kv_len) are not looked at. */
+typedef struct {
+  int32_t num_seqs;  /* >= 0 */
+  int32_t total_q;   /* rows of the packed tensors, 0 .. 2^30 */
+  int32_t Hq, Hkv, d; /* Hq % Hkv == 0, Hq / Hkv <= 64, d in {64, 128} */
+  int32_t page;      /* tokens in a page: 16, 32, 64, 128 or 256 */
+  int32_t num_pages; /* pages of each cache, >= 1 */
+  int32_t max_pages; /* columns of the page table, >= 1; max_pages * page <= 2^30 */
+  int32_t window;    /* >= 1 */
+  int32_t sinks;     /* >= 0 */
+  float scale;       /* finite, > 0 */
+  int32_t dtype;     /* ssa_dtype_t */
+} ssa_paged_dims_t;
+
+/* Bytes of workspace that ssa_paged_attention needs; 0 for an invalid or
+ * empty shape. */
+SSA_API size_t ssa_paged_workspace_bytes(const ssa_paged_dims_t* dims);
+
+/* Writes the new tokens' keys and values into their pages.
+ *   k, v: packed [1, Hkv, total_q, d] strided (in).
+ *   K, V: the caches (in/out); only the new tokens' rows are written.
+ * New tokens at negative positions and rows behind q_start[num_seqs] are
+ * skipped.  Two sequences that write the same page row race. */
+SSA_API ssa_status_t ssa_paged_append(const ssa_paged_dims_t* dims, const ssa_tensor_t* k, const ssa_tensor_t* v,
+                                      const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table,
+                                      const ssa_tensor_t* K, const ssa_tensor_t* V, ssa_stream_t stream);
+
+/* Attention of the new tokens over their sequences' pages: one token per
+ * sequence (decoding), chunks of a prompt, or both in one batch.  The cache
+ * holds the new tokens' keys and values already (ssa_paged_append).
+ *   q, h: packed [1, Hq, total_q, d] strided; lse [Hq, total_q] fp32, dense.
+ *   Rows behind q_start[num_seqs] are left as they were.  A row that sees no
+ *     key (a negative position, missing pages) gets h = 0, lse = -INFINITY.
+ *   ws: at least ssa_paged_workspace_bytes(dims) bytes, 256-byte aligned; two
+ *     calls in flight at once must not share it.
+ *   What a page holds behind kv_len or outside every row's view is never
+ *     used, NaN or not; a NaN or infinity in a V row that some new token sees
+ *     may reach rows of the same sequence's earlier new tokens. */
+SSA_API ssa_status_t ssa_paged_attention(const ssa_paged_dims_t* dims, const ssa_tensor_t* q, const ssa_tensor_t* K,
+                                         const ssa_tensor_t* V, const int32_t* q_start, const int32_t* kv_len,
+                                         const int32_t* page_table, const ssa_tensor_t* h, float* lse, void* ws,
+                                         size_t ws_bytes, ssa_stream_t stream);
+
 /* Number of kernels this library has enqueued in this process so far (all
  * devices, all threads).  Lets a caller count the launches of a region. */
 SSA_API uint64_t ssa_launch_count(void);
