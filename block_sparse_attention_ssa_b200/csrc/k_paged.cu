@@ -151,6 +151,7 @@ cudaError_t launch_paged_join(const PagedDims& D, const PagedArgs& a, int ctas, 
   count_launches(1);
   return cudaGetLastError();
 }
+template cudaError_t launch_paged_join<128, 256>(const PagedDims&, const PagedArgs&, int, int, int, cudaStream_t);
 template cudaError_t launch_paged_join<64, 64>(const PagedDims&, const PagedArgs&, int, int, int, cudaStream_t);
 
 }  // namespace ssa

@@ -55,8 +55,8 @@ ssa_status_t check_paged(const ssa_paged_dims_t* in, PagedDims* out, bool* empty
   return SSA_OK;
 }
 
-// A [B, H, N, d] tensor as in the other entry points; an output of more than one
-// (batch, head) slice may not lay them over one another.
+// A [B, H, N, d] tensor as in the other entry points.  Inputs may broadcast batches and
+// heads (stride 0); rows and an output's slices may not lie over one another.
 ssa_status_t check_tensor(const ssa_tensor_t* t, int dtype, int d, int64_t B, int64_t H, int64_t N, bool output, TensorRef* out) {
   if (t == nullptr || !aligned(t->ptr, 16)) return SSA_ERR_INVALID_ARG;
   const int64_t es = dtype == SSA_BF16 ? 2 : 4;
@@ -64,8 +64,8 @@ ssa_status_t check_tensor(const ssa_tensor_t* t, int dtype, int d, int64_t B, in
   for (int i = 0; i < 3; ++i) {
     if (st[i] < 0 || st[i] >= (1LL << 38) || (st[i] * es) % 16) return SSA_ERR_INVALID_ARG;
     if (output && n[i] > 1 && st[i] < d) return SSA_ERR_INVALID_ARG;
-    // rows that overlap in part describe no tensor; equal rows (stride 0) are a broadcast
-    if (!output && n[i] > 1 && st[i] != 0 && st[i] < d) return SSA_ERR_INVALID_ARG;
+    // rows that overlap in part describe no tensor; slices laid over one another (stride 0) are a broadcast
+    if (!output && n[i] > 1 && st[i] < d && (i == 2 || st[i] != 0)) return SSA_ERR_INVALID_ARG;
   }
   *out = TensorRef{t->ptr, t->stride_b, t->stride_h, t->stride_n};
   return SSA_OK;
@@ -75,6 +75,8 @@ ssa_status_t check_ws(const void* ws, size_t have, size_t need) {
   if (ws == nullptr || have < need) return SSA_ERR_WORKSPACE;
   return aligned(ws, kAlign) ? SSA_OK : SSA_ERR_INVALID_ARG;
 }
+
+size_t paged_bytes(const PagedDims& D) { return D.dtype == SSA_F32 ? paged_ws_bytes(D) : paged_tc_ws_bytes(D); }
 
 ssa_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? SSA_OK : SSA_ERR_CUDA; }
 
@@ -108,7 +110,11 @@ ssa_status_t ssa_fwd_window(const ssa_window_dims_t* dims, const ssa_tensor_t* Q
   if (!aligned(lse, 4)) return SSA_ERR_INVALID_ARG;
   if ((s = require_sm100()) != SSA_OK) return s;
   a.lse = lse;
-  return from_cuda(launch_win_fwd_simt(D, a, static_cast<cudaStream_t>(stream)));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (D.dtype == SSA_F32) return from_cuda(launch_win_fwd_simt(D, a, st));
+  int32_t* status = status_word();
+  if (status == nullptr) return SSA_ERR_CUDA;
+  return from_cuda(launch_win_fwd_tc(D, a, status, st));
 }
 
 ssa_status_t ssa_bwd_window(const ssa_window_dims_t* dims, const ssa_tensor_t* Q, const ssa_tensor_t* K,
@@ -142,7 +148,7 @@ size_t ssa_paged_workspace_bytes(const ssa_paged_dims_t* dims) {
   PagedDims D;
   bool empty = false;
   if (check_paged(dims, &D, &empty) != SSA_OK || empty) return 0;
-  return paged_ws_bytes(D);
+  return paged_bytes(D);
 }
 
 ssa_status_t ssa_paged_append(const ssa_paged_dims_t* dims, const ssa_tensor_t* k, const ssa_tensor_t* v,
@@ -178,20 +184,25 @@ ssa_status_t ssa_paged_attention(const ssa_paged_dims_t* dims, const ssa_tensor_
   if (s != SSA_OK) return s;
   if (empty) return SSA_OK;
   PagedArgs a{};
-  if ((s = check_tensor(q, D.dtype, D.d, 1, D.Hq, D.T, false, &a.q)) != SSA_OK) return s;
+  // a slot's heads come in one TMA box: no broadcast of them
+  if ((s = check_tensor(q, D.dtype, D.d, 1, D.Hq, D.T, true, &a.q)) != SSA_OK) return s;
   if ((s = check_tensor(K, D.dtype, D.d, D.num_pages, D.Hkv, D.page, false, &a.k)) != SSA_OK) return s;
   if ((s = check_tensor(V, D.dtype, D.d, D.num_pages, D.Hkv, D.page, false, &a.v)) != SSA_OK) return s;
   if ((s = check_tensor(h, D.dtype, D.d, 1, D.Hq, D.T, true, &a.h)) != SSA_OK) return s;
   if (!aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(page_table, 4) || !aligned(lse, 4))
     return SSA_ERR_INVALID_ARG;
-  if ((s = check_ws(ws, ws_bytes, paged_ws_bytes(D))) != SSA_OK) return s;
+  if ((s = check_ws(ws, ws_bytes, paged_bytes(D))) != SSA_OK) return s;
   if ((s = require_sm100()) != SSA_OK) return s;
   a.q_start = q_start;
   a.kv_len = kv_len;
   a.table = page_table;
   a.lse = lse;
   a.ws = ws;
-  return from_cuda(launch_paged_simt(D, a, static_cast<cudaStream_t>(stream)));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (D.dtype == SSA_F32) return from_cuda(launch_paged_simt(D, a, st));
+  int32_t* status = status_word();
+  if (status == nullptr) return SSA_ERR_CUDA;
+  return from_cuda(launch_paged_tc(D, a, status, st));
 }
 
 }  // extern "C"

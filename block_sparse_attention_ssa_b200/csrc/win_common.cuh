@@ -272,4 +272,14 @@ cudaError_t launch_paged_simt(const PagedDims& D, const PagedArgs& a, cudaStream
 template <int KT, int ROWS>
 cudaError_t launch_paged_join(const PagedDims& D, const PagedArgs& a, int ctas, int TI, int min_units, cudaStream_t st);
 
+// TMA maps over bf16 tensors of any length with broadcast batch or head dimensions.
+bool tma_map_4d(CUtensorMap* map, const void* p, int d, int64_t n1, int64_t n2, int64_t n3, int64_t s1, int64_t s2,
+                int64_t s3, int b1, int b2);
+bool win_tma_map(CUtensorMap* map, const TensorRef& t, int64_t B, int64_t H, int64_t N, int rows, int d, int* zero);
+
+// bf16 on tcgen05.
+cudaError_t launch_win_fwd_tc(const WinDims& D, const WinFwdArgs& a, int32_t* status, cudaStream_t st);
+cudaError_t launch_paged_tc(const PagedDims& D, const PagedArgs& a, int32_t* status, cudaStream_t st);
+size_t paged_tc_ws_bytes(const PagedDims& D);
+
 }  // namespace ssa

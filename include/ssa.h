@@ -384,9 +384,9 @@ SSA_API size_t ssa_window_workspace_bytes(const ssa_window_dims_t* dims);
 /* Forward: h_t = softmax over A_t of x_tu applied to V, lse_t its natural-log
  * normaliser, x_tu = scale * q_t . k_u.
  *   Q, h [B, Hq, N, d], K, V [B, Hkv, N, d] strided, dims->dtype; lse
- *     [B, Hq, N] fp32, dense.  Inputs may have zero strides (broadcast
- *     dimensions); an output row may not be written twice, so h's strides of
- *     dimensions longer than one are not zero (SSA_ERR_INVALID_ARG).
+ *     [B, Hq, N] fp32, dense.  Inputs may broadcast batches and heads (stride 0);
+ *     rows, and the slices of an output, may not lie over one another
+ *     (SSA_ERR_INVALID_ARG).
  *   A NaN or an infinity in the V row of a token may reach rows of other
  *     tokens up to 127 positions earlier (a weight of zero times it). */
 SSA_API ssa_status_t ssa_fwd_window(const ssa_window_dims_t* dims, const ssa_tensor_t* Q, const ssa_tensor_t* K,
@@ -399,7 +399,7 @@ SSA_API ssa_status_t ssa_fwd_window(const ssa_window_dims_t* dims, const ssa_ten
  * dK and dV are summed over the g query heads of each kv head.  No atomics:
  * the same inputs give the same bits.
  *   Q, K, V, h, lse: as passed to / written by ssa_fwd_window.
- *   g [B, Hq, N, d] dims->dtype (in, required; zero strides are fine).
+ *   g [B, Hq, N, d] dims->dtype (in, required).
  *   dQ [B, Hq, N, d], dK, dV [B, Hkv, N, d] (out): fully overwritten.
  *   ws: at least ssa_window_workspace_bytes(dims) bytes, 256-byte aligned. */
 SSA_API ssa_status_t ssa_bwd_window(const ssa_window_dims_t* dims, const ssa_tensor_t* Q, const ssa_tensor_t* K,
@@ -458,7 +458,7 @@ SSA_API ssa_status_t ssa_paged_append(const ssa_paged_dims_t* dims, const ssa_te
 /* Attention of the new tokens over their sequences' pages: one token per
  * sequence (decoding), chunks of a prompt, or both in one batch.  The cache
  * holds the new tokens' keys and values already (ssa_paged_append).
- *   q, h: packed [1, Hq, total_q, d] strided; lse [Hq, total_q] fp32, dense.
+ *   q, h: packed [1, Hq, total_q, d] strided, no broadcast heads; lse [Hq, total_q] fp32, dense.
  *   Rows behind q_start[num_seqs] are left as they were.  A row that sees no
  *     key (a negative position, missing pages) gets h = 0, lse = -INFINITY.
  *   ws: at least ssa_paged_workspace_bytes(dims) bytes, 256-byte aligned; two

@@ -101,16 +101,16 @@ def test_forward_and_backward(name, dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_strided_and_broadcast_inputs(dtype):
-    """[B, N, H, d] memory, keys and values shared by all heads and batches through zero strides, a zero-stride
-    upstream gradient, outputs written into slices of larger buffers that keep what lies around them."""
+    """[B, N, H, d] memory, keys and values shared by all heads and batches through zero strides, an upstream
+    gradient shared by all heads, outputs written into slices of larger buffers that keep what lies around them."""
     B, H, N, d, window, sinks = 2, 4, 150, 64, 33, 2
     host = _inputs(B, H, 1, N, d, dtype, 5)
     host["K"], host["V"] = (host[k][:1].expand(B, H, N, d) for k in ("K", "V"))
-    host["g"] = host["g"][:, :, :1].expand(B, H, N, d)
+    host["g"] = host["g"][:, :1].expand(B, H, N, d)
     dims = api.make_window_dims(B, H, H, N, d, window, sinks, dtype, scale=0.2)
     dev = dict(Q=host["Q"].cuda().transpose(1, 2).contiguous().transpose(1, 2),
                K=host["K"][:1, :1].cuda().expand(B, H, N, d), V=host["V"][:1, :1].cuda().expand(B, H, N, d),
-               g=host["g"][:, :, :1].cuda().expand(B, H, N, d))
+               g=host["g"][:, :1].cuda().expand(B, H, N, d))
     big = {k: torch.full((B, N + 2, H + 1, d + 8), 7.0, dtype=TYPES[dtype], device="cuda") for k in ("h", "dQ", "dK", "dV")}
     out = {k: v[:, 1:-1, :H, :d].transpose(1, 2) for k, v in big.items()}
     out["lse"] = torch.empty(B, H, N, device="cuda")
