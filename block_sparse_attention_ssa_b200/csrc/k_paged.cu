@@ -1,6 +1,8 @@
 // The paged cache's writer, and the join of attention partials.
 #include "win_common.cuh"
 
+#include <type_traits>
+
 namespace ssa {
 namespace {
 
@@ -138,16 +140,11 @@ template <int KT, int ROWS>
 cudaError_t launch_paged_join(const PagedDims& D, const PagedArgs& a, int ctas, int TI, int min_units, cudaStream_t st) {
   const Batch batch{a.q_start, a.kv_len, D.seqs, D.T, D.max_pages * D.page, TI, D.window, D.sinks, D.Hkv};
   const dim3 grid(ctas, 4);
-  if (D.dtype == SSA_BF16) {
-    if (D.d == 64)
-      paged_join_kernel<__nv_bfloat16, 64, KT, ROWS><<<grid, 256, 0, st>>>(a, batch, D.T, D.g, ctas, min_units);
-    else
-      paged_join_kernel<__nv_bfloat16, 128, KT, ROWS><<<grid, 256, 0, st>>>(a, batch, D.T, D.g, ctas, min_units);
-  } else if (D.d == 64) {
-    paged_join_kernel<float, 64, KT, ROWS><<<grid, 256, 0, st>>>(a, batch, D.T, D.g, ctas, min_units);
-  } else {
-    paged_join_kernel<float, 128, KT, ROWS><<<grid, 256, 0, st>>>(a, batch, D.T, D.g, ctas, min_units);
-  }
+  using T = std::conditional_t<KT == 128, __nv_bfloat16, float>;  // units of 128 keys are the bf16 kernel's
+  if (D.d == 64)
+    paged_join_kernel<T, 64, KT, ROWS><<<grid, 256, 0, st>>>(a, batch, D.T, D.g, ctas, min_units);
+  else
+    paged_join_kernel<T, 128, KT, ROWS><<<grid, 256, 0, st>>>(a, batch, D.T, D.g, ctas, min_units);
   count_launches(1);
   return cudaGetLastError();
 }

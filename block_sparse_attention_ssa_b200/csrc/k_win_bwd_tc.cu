@@ -1,0 +1,645 @@
+// Backward of window attention with sinks on tcgen05 (bf16, d = 64 or 128).
+//
+// Mathematics: p = 2^(s c - lse2), dP = g V^T, dx = p (dP - D) with D_t = g_t . h_t;
+// dV = p^T g, dK = scale dx^T Q, dQ = scale dx K.  Logits, p, dP, dx and all sums are
+// fp32; p and dx are rounded to bf16 (half a step each) as operands of the next product.
+// lse2 and D come from the preprocess in rows padded to 128 tokens; a padding row's lse2
+// is +infinity, which makes its weights zero.
+//
+// Two kernels of 320 threads (warps 0-7 compute, warp 8 loads by TMA, warp 9 issues the
+// products), each forming S and dP: a query tile's dQ and a key tile's dK, dV have
+// different owners, and joining them through memory costs more than the two extra
+// products (a dQ of fp32 additions in L2 moves 64 KB per 128 x 128 tile).  No atomics:
+// every output has one writer with a fixed order.
+//
+//   dkv  a 128-key tile and a chunk of its steps (query head, 128-query tile) per CTA.
+//        TMEM (512 columns at d = 128): dK, dV, S^T, dP^T.  The products go round
+//        dV(j), S^T(j+1), dK(j), dP^T(j+1): while the warps turn S^T into P^T the tensor
+//        core does dK and dP^T, while they turn dP^T into dx^T it does dV and S^T, so
+//        single buffers suffice and S^T takes N = 128 (an N = 64 product costs as much).
+//        P^T overwrites S^T, dx^T overwrites dP^T, each warp within its own columns.
+//   dq   a persistent CTA walks (query head, 128-query tile) items.  TMEM: dQ, two S, dP;
+//        S(j+1) runs while the warps finish dx(j), dQ(j) and dP(j+1) while they form p(j+1).
+#include "win_common.cuh"
+
+#include "sm100_ptx.cuh"
+
+namespace ssa {
+namespace {
+
+using namespace sm100;
+using bf16 = __nv_bfloat16;
+
+constexpr int TILE = 128;
+constexpr int NTHREADS = 320;
+constexpr int WARP_TMA = 8, WARP_MMA = 9;
+constexpr int kCtas = 148;  // one per SM
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int HALF = TILE * 128;  // 64 columns of a tile: 128 rows of 128 bytes
+constexpr int ROWB = TILE * 4;    // one fp32 row vector of a tile
+
+template <int HD>
+struct Cfg {
+  static constexpr int TB = TILE * HD * 2;
+  static constexpr uint32_t IDESC_S = idesc_bf16_f32(TILE, TILE, false, false);
+  static constexpr uint32_t IDESC_ACC = idesc_bf16_f32(TILE, HD, false, true);
+};
+
+struct BwdParams {
+  TensorRef dq, dk, dv;
+  const float* lse2;
+  const float* dsum;
+  float* part;
+  int32_t* status;
+  int B, Hq, Hkv, g, N, Npad, NT, window, sinks, L, partials;
+  int zq, zk, zv, zg;  // broadcast dimensions: bit 0 batch, bit 1 head
+  float c, scale;      // c = scale * log2(e)
+};
+
+// D (128 x 128) = A B^T over HD, both K-major tiles in shared memory.
+template <int HD>
+__device__ __forceinline__ void mma_logits(uint32_t d, uint32_t a, uint32_t b) {
+#pragma unroll
+  for (int kk = 0; kk < HD / 16; ++kk) {
+    const uint32_t o = (kk >> 2) * HALF + (kk & 3) * 32;
+    mma_ss(d, smem_desc_sw128(a + o, 16, 1024), smem_desc_sw128(b + o, 16, 1024), Cfg<HD>::IDESC_S, kk > 0 ? 1u : 0u);
+  }
+}
+
+// D (128 x HD) (+)= A B, A 128 x 128 as bf16 pairs in TMEM (reduction 0-63 in columns a.., 64-127 in
+// a + 64..), B 128 rows (the reduction) of a tile in shared memory.
+template <int HD>
+__device__ __forceinline__ void mma_grad(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
+#pragma unroll
+  for (int kk = 0; kk < TILE / 16; ++kk)
+    mma_ts(d, a + 64 * (kk >> 2) + 8 * (kk & 3), smem_desc_sw128(b + kk * 2048, HALF, 1024), Cfg<HD>::IDESC_ACC,
+           (accumulate || kk > 0) ? 1u : 0u);
+}
+
+template <int HD>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int row, int h, int b,
+                                          int zero) {
+#pragma unroll
+  for (int f = 0; f < HD / 64; ++f)
+    tma_load_4d(dst + f * HALF, map, bar, 64 * f, row, zero & 2 ? 0 : h, zero & 1 ? 0 : b);
+}
+
+__device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+
+__device__ __forceinline__ void ld64(uint32_t addr, float (&x)[64]) {
+  tmem_ld32(addr, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+  tmem_ld32(addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+}
+
+// 32 columns of an accumulator row, scaled, to bf16 memory.
+__device__ __forceinline__ void store32(bf16* dst, const uint32_t (&r)[32], float mul) {
+  uint4* d4 = reinterpret_cast<uint4*>(dst);
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[i] = pack_bf16(__uint_as_float(r[8 * v + 2 * i]) * mul, __uint_as_float(r[8 * v + 2 * i + 1]) * mul);
+    d4[v] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// ================================================================ dK, dV
+template <int HD>
+struct DkvCfg {
+  static constexpr int NS = HD == 128 ? 2 : 3;
+  static constexpr int TB = Cfg<HD>::TB;
+  static constexpr int STAGE = 2 * TB + 2 * ROWB;  // Q, g, lse2, D
+  static constexpr int OFF_V = TB, OFF_STAGE = 2 * TB, OFF_MISC = OFF_STAGE + NS * STAGE;
+  static_assert(STAGE % 1024 == 0, "stages keep the alignment of swizzled tiles");
+};
+struct DkvMisc {
+  uint64_t kv_full, q_full[3], q_empty[3], s_full, p_full, dp_full, ds_full, done, drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int HD>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    win_bwd_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
+                          const __grid_constant__ BwdParams p) {
+  using C = DkvCfg<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  DkvMisc& M = *reinterpret_cast<DkvMisc*>(smem + C::OFF_MISC);
+  volatile int* abort = &M.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int plane = (int)blockIdx.x % p.Hkv + (int)blockIdx.y * p.Hkv, kvh = plane % p.Hkv, b = blockIdx.y;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&M.kv_full, 1);
+    for (int i = 0; i < C::NS; ++i) {
+      mbar_init(&M.q_full[i], 1);
+      mbar_init(&M.q_empty[i], 1);
+    }
+    mbar_init(&M.s_full, 1);
+    mbar_init(&M.p_full, 8);
+    mbar_init(&M.dp_full, 1);
+    mbar_init(&M.ds_full, 8);
+    mbar_init(&M.done, 1);
+    mbar_init(&M.drain, 1);
+    M.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == WARP_MMA) {
+    tmem_alloc(&M.tmem_base, 512);
+    tmem_relinquish();
+  }
+  const Chunk ch = find_chunk<TILE>((int)blockIdx.x / p.Hkv, p.NT, p.L, p.g, p.N, p.window, p.sinks);
+  const int u0 = ch.kt * TILE, nq = query_tiles_of<TILE>(ch.kt, p.N, p.window, p.sinks);
+  const int first = ch.idx * p.L, T = min(p.L, nq * p.g - first);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = M.tmem_base;
+  const uint32_t cK = tmem, cV = tmem + HD, cS = tmem + 256, cP = tmem + 384;
+  uint8_t* sK = smem;
+  uint8_t* sV = smem + C::OFF_V;
+  auto stage = [&](int j) { return smem + C::OFF_STAGE + (j % C::NS) * C::STAGE; };
+
+  if (warp == WARP_TMA) {
+    if (lane == 0) {
+      prefetch_tensormap(&tmQ);
+      prefetch_tensormap(&tmG);
+      mbar_expect_tx(&M.kv_full, 2 * C::TB);
+      load_tile<HD>(sK, &tmK, &M.kv_full, u0, kvh, b, p.zk);
+      load_tile<HD>(sV, &tmV, &M.kv_full, u0, kvh, b, p.zv);
+      int issued = 0;
+      for (int j = 0; j < T; ++j) {
+        const int i = j % C::NS;
+        if (j >= C::NS && !mbar_wait(&M.q_empty[i], (uint32_t)(j / C::NS - 1) & 1u, abort)) break;
+        const int h = kvh * p.g + (first + j) / nq, t0 = (ch.kt + (first + j) % nq) * TILE;
+        uint8_t* sp = stage(j);
+        const int64_t ro = ((int64_t)b * p.Hq + h) * p.Npad + t0;
+        mbar_expect_tx(&M.q_full[i], 2 * C::TB + 2 * ROWB);
+        load_tile<HD>(sp, &tmQ, &M.q_full[i], t0, h, b, p.zq);
+        bulk_load(sp + 2 * C::TB, p.lse2 + ro, ROWB, &M.q_full[i]);
+        load_tile<HD>(sp + C::TB, &tmG, &M.q_full[i], t0, h, b, p.zg);
+        bulk_load(sp + 2 * C::TB + ROWB, p.dsum + ro, ROWB, &M.q_full[i]);
+        issued = j + 1;
+      }
+      int dummy = 0;
+      mbar_wait(&M.kv_full, 0, &dummy);
+      for (int j = issued > C::NS ? issued - C::NS : 0; j < issued; ++j) {
+        dummy = 0;
+        mbar_wait(&M.q_full[j % C::NS], (uint32_t)(j / C::NS) & 1u, &dummy);
+      }
+    }
+  } else if (warp == WARP_MMA) {
+    if (lane == 0) {
+      const uint32_t ak = smem_u32(sK), av = smem_u32(sV);
+      auto have = [&](int j) { return mbar_wait(&M.q_full[j % C::NS], (uint32_t)(j / C::NS) & 1u, abort); };
+      auto s_of = [&](int j) {
+        mma_logits<HD>(cS, ak, smem_u32(stage(j)));
+        tc_commit(&M.s_full);
+      };
+      auto dp_of = [&](int j) {
+        mma_logits<HD>(cP, av, smem_u32(stage(j)) + C::TB);
+        tc_commit(&M.dp_full);
+      };
+      bool ok = mbar_wait(&M.kv_full, 0, abort) && have(0);
+      if (ok) {
+        tc_fence_after();
+        s_of(0);
+        dp_of(0);
+      }
+      for (int j = 0; ok && j < T; ++j) {
+        if (!(ok = mbar_wait(&M.p_full, (uint32_t)j & 1u, abort))) break;
+        tc_fence_after();
+        mma_grad<HD>(cV, cS, smem_u32(stage(j)) + C::TB, j > 0);
+        if (j + 1 < T) {
+          if (!(ok = have(j + 1))) break;
+          tc_fence_after();
+          s_of(j + 1);
+        }
+        if (!(ok = mbar_wait(&M.ds_full, (uint32_t)j & 1u, abort))) break;
+        tc_fence_after();
+        mma_grad<HD>(cK, cP, smem_u32(stage(j)), j > 0);
+        tc_commit(&M.q_empty[j % C::NS]);
+        if (j + 1 < T) dp_of(j + 1);
+      }
+      tc_commit(&M.done);
+      tc_commit(&M.drain);
+      int dummy = 0;
+      mbar_wait(&M.drain, 0, &dummy);
+    }
+    __syncwarp();
+  } else {
+    const int quarter = warp & 3, half = warp >> 2;  // key rows 32 quarter.., query columns 64 half..
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const uint32_t aS = cS + lane_base + 64 * half, aP = cP + lane_base + 64 * half;
+    const int u = u0 + quarter * 32 + lane;
+    const int ua = u0 + quarter * 32, ub = ua + 31;
+    bool ok = true;
+    for (int j = 0; j < T; ++j) {
+      const int t0 = (ch.kt + (first + j) % nq) * TILE + 64 * half;  // this warp's first query
+      const float* ls = reinterpret_cast<const float*>(stage(j) + 2 * C::TB) + 64 * half;
+      const float* ds = ls + TILE;
+      // every lane reads the stage's row vectors: every lane waits for them
+      if (!__all_sync(0xffffffffu, mbar_wait(&M.q_full[j % C::NS], (uint32_t)(j / C::NS) & 1u, abort)) ||
+          !__all_sync(0xffffffffu, mbar_wait(&M.s_full, (uint32_t)j & 1u, abort))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const bool all = t0 >= ub && (t0 + 63 - ua < p.window || ub < p.sinks);
+      // queries c with lo <= c < hi see the key (c >= lo alone where it is a sink)
+      const int lo = u - t0, hi = u < p.sinks ? 64 : u + p.window - t0;
+      float x[64];
+      ld64(aS, x);
+      tmem_wait_ld();
+      uint32_t pk[32];
+#pragma unroll
+      for (int c = 0; c < 64; c += 4) {
+        const float4 l4 = *reinterpret_cast<const float4*>(ls + c);
+        x[c] = ex2(fmaf(x[c], p.c, -l4.x));
+        x[c + 1] = ex2(fmaf(x[c + 1], p.c, -l4.y));
+        x[c + 2] = ex2(fmaf(x[c + 2], p.c, -l4.z));
+        x[c + 3] = ex2(fmaf(x[c + 3], p.c, -l4.w));
+      }
+      if (!all) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (c < lo || c >= hi) x[c] = 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) pk[c / 2] = pack_bf16(x[c], x[c + 1]);
+      tmem_st32(aS, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&M.p_full);
+
+      if (!__all_sync(0xffffffffu, mbar_wait(&M.dp_full, (uint32_t)j & 1u, abort))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t y[32];
+        tmem_ld32(aP + 32 * q, y);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const float4 d4 = *reinterpret_cast<const float4*>(ds + 32 * q + c);
+          x[32 * q + c] *= __uint_as_float(y[c]) - d4.x;
+          x[32 * q + c + 1] *= __uint_as_float(y[c + 1]) - d4.y;
+          x[32 * q + c + 2] *= __uint_as_float(y[c + 2]) - d4.z;
+          x[32 * q + c + 3] *= __uint_as_float(y[c + 3]) - d4.w;
+        }
+      }
+      if (!all) {  // zero times a NaN or an infinity of a hidden pair
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (c < lo || c >= hi) x[c] = 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) pk[c / 2] = pack_bf16(x[c], x[c + 1]);
+      tmem_st32(aP, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&M.ds_full);
+    }
+    if (ok && __all_sync(0xffffffffu, mbar_wait(&M.done, 0, abort))) {
+      tc_fence_after();
+      // columns HD/2 half .. of dK and dV
+      constexpr int W = HD / 2;
+      const bool mine = u < p.N;
+      float* part = p.part + ((size_t)plane * p.partials + ch.slot + ch.idx) * (2 * TILE * HD) +
+                    (quarter * 32 + lane) * HD + W * half;
+#pragma unroll 1
+      for (int c0 = 0; c0 < 2 * W; c0 += 32) {
+        const int which = c0 / W, col = c0 % W;  // 0: dK, 1: dV
+        uint32_t r[32];
+        tmem_ld32((which ? cV : cK) + lane_base + W * half + col, r);
+        tmem_wait_ld();
+        if (!mine) continue;
+        if (ch.n == 1) {
+          const TensorRef& t = which ? p.dv : p.dk;
+          store32(row_ptr_w<bf16>(t, b, kvh, u) + W * half + col, r, which ? 1.0f : p.scale);
+        } else {
+          float4* d4 = reinterpret_cast<float4*>(part + which * TILE * HD + col);
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            d4[v] = make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]), __uint_as_float(r[4 * v + 2]),
+                                __uint_as_float(r[4 * v + 3]));
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (M.abort && threadIdx.x == 0) atomicCAS(p.status, 0, (int)SSA_ERR_TIMEOUT);
+  if (warp == WARP_MMA) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ================================================================ dQ
+template <int HD>
+struct DqCfg {
+  static constexpr int NSK = HD == 128 ? 3 : 4, NSV = HD == 128 ? 2 : 3;
+  static constexpr int TB = Cfg<HD>::TB;
+  static constexpr int OFF_G = TB, OFF_K = 2 * TB, OFF_V = OFF_K + NSK * TB, OFF_MISC = OFF_V + NSV * TB;
+};
+struct DqMisc {
+  uint64_t q_full, q_empty, k_full[4], k_empty[4], v_full[3], v_empty[3];
+  uint64_t s_full[2], dp_full, ds_full, dq_done, drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+struct DqItem {
+  int b, h, kvh, t0;
+  KeyTiles kt;
+};
+
+template <int HD>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    win_bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
+                         const __grid_constant__ BwdParams p) {
+  using C = DqCfg<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  DqMisc& M = *reinterpret_cast<DqMisc*>(smem + C::OFF_MISC);
+  volatile int* abort = &M.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&M.q_full, 1);
+    mbar_init(&M.q_empty, 1);
+    for (int i = 0; i < C::NSK; ++i) {
+      mbar_init(&M.k_full[i], 1);
+      mbar_init(&M.k_empty[i], 1);
+    }
+    for (int i = 0; i < C::NSV; ++i) {
+      mbar_init(&M.v_full[i], 1);
+      mbar_init(&M.v_empty[i], 1);
+    }
+    mbar_init(&M.s_full[0], 1);
+    mbar_init(&M.s_full[1], 1);
+    mbar_init(&M.dp_full, 1);
+    mbar_init(&M.ds_full, 8);
+    mbar_init(&M.dq_done, 1);
+    mbar_init(&M.drain, 1);
+    M.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == WARP_MMA) {
+    tmem_alloc(&M.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = M.tmem_base;
+  const uint32_t cQ = tmem, cS = tmem + 128, cP = tmem + 384;
+  uint8_t* sQ = smem;
+  uint8_t* sG = smem + C::OFF_G;
+  uint8_t* sK = smem + C::OFF_K;
+  uint8_t* sV = smem + C::OFF_V;
+
+  const int planes = p.B * p.Hq, items = planes * p.NT;
+  // The longest rows first; the heads of a group side by side, so that they share K and V in L2.
+  auto item = [&](int i) {
+    DqItem I;
+    const int plane = i % planes;
+    I.t0 = (p.NT - 1 - i / planes) * TILE;
+    I.b = plane / p.Hq;
+    I.h = plane % p.Hq;
+    I.kvh = I.h / p.g;
+    I.kt = key_tiles<TILE>(I.t0, min(I.t0 + TILE, p.N) - 1, p.window, p.sinks);
+    return I;
+  };
+
+  if (warp == WARP_TMA) {
+    if (lane == 0) {
+      prefetch_tensormap(&tmQ);
+      prefetch_tensormap(&tmK);
+      prefetch_tensormap(&tmV);
+      prefetch_tensormap(&tmG);
+      uint32_t n = 0, qn = 0, kn = 0, vn = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
+        const DqItem I = item(i);
+        if (qn > 0 && !mbar_wait(&M.q_empty, (qn - 1) & 1u, abort)) break;
+        mbar_expect_tx(&M.q_full, 2 * C::TB);
+        load_tile<HD>(sQ, &tmQ, &M.q_full, I.t0, I.h, I.b, p.zq);
+        load_tile<HD>(sG, &tmG, &M.q_full, I.t0, I.h, I.b, p.zg);
+        ++qn;
+        for (int j = 0; j < I.kt.count; ++j, ++n) {
+          const int u0 = I.kt.tile(j) * TILE, ik = (int)(n % C::NSK), iv = (int)(n % C::NSV);
+          if (n >= C::NSK && !(ok = mbar_wait(&M.k_empty[ik], (n / C::NSK - 1) & 1u, abort))) break;
+          mbar_expect_tx(&M.k_full[ik], C::TB);
+          load_tile<HD>(sK + ik * C::TB, &tmK, &M.k_full[ik], u0, I.kvh, I.b, p.zk);
+          kn = n + 1;
+          if (n >= C::NSV && !(ok = mbar_wait(&M.v_empty[iv], (n / C::NSV - 1) & 1u, abort))) break;
+          mbar_expect_tx(&M.v_full[iv], C::TB);
+          load_tile<HD>(sV + iv * C::TB, &tmV, &M.v_full[iv], u0, I.kvh, I.b, p.zv);
+          vn = n + 1;
+        }
+      }
+      int dummy = 0;
+      if (qn) mbar_wait(&M.q_full, (qn - 1) & 1u, &dummy);
+      for (uint32_t k = kn > C::NSK ? kn - C::NSK : 0; k < kn; ++k) {
+        dummy = 0;
+        mbar_wait(&M.k_full[k % C::NSK], (k / C::NSK) & 1u, &dummy);
+      }
+      for (uint32_t k = vn > C::NSV ? vn - C::NSV : 0; k < vn; ++k) {
+        dummy = 0;
+        mbar_wait(&M.v_full[k % C::NSV], (k / C::NSV) & 1u, &dummy);
+      }
+    }
+  } else if (warp == WARP_MMA) {
+    if (lane == 0) {
+      const uint32_t aq = smem_u32(sQ), ag = smem_u32(sG), ak = smem_u32(sK), av = smem_u32(sV);
+      uint32_t n = 0, qn = 0;  // key tiles and items so far
+      bool ok = true;
+      auto s_of = [&](uint32_t k) {
+        if (!mbar_wait(&M.k_full[k % C::NSK], (k / C::NSK) & 1u, abort)) return false;
+        tc_fence_after();
+        mma_logits<HD>(cS + TILE * (k & 1), aq, ak + (k % C::NSK) * C::TB);
+        tc_commit(&M.s_full[k & 1]);
+        return true;
+      };
+      auto dp_of = [&](uint32_t k, bool last) {
+        if (!mbar_wait(&M.v_full[k % C::NSV], (k / C::NSV) & 1u, abort)) return false;
+        tc_fence_after();
+        mma_logits<HD>(cP, ag, av + (k % C::NSV) * C::TB);
+        tc_commit(&M.dp_full);
+        tc_commit(&M.v_empty[k % C::NSV]);
+        if (last) tc_commit(&M.q_empty);
+        return true;
+      };
+      for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
+        const int T = item(i).kt.count;
+        if (!(ok = mbar_wait(&M.q_full, qn & 1u, abort))) break;
+        ++qn;
+        tc_fence_after();
+        ok = s_of(n) && dp_of(n, T == 1);
+        for (int j = 0; ok && j < T; ++j, ++n) {
+          if (j + 1 < T && !(ok = s_of(n + 1))) break;
+          if (!(ok = mbar_wait(&M.ds_full, n & 1u, abort))) break;
+          tc_fence_after();
+          mma_grad<HD>(cQ, cP, ak + (n % C::NSK) * C::TB, j > 0);
+          tc_commit(&M.k_empty[n % C::NSK]);
+          if (j + 1 == T) tc_commit(&M.dq_done);
+          if (j + 1 < T) ok = dp_of(n + 1, j + 2 == T);
+        }
+      }
+      tc_commit(&M.drain);
+      int dummy = 0;
+      mbar_wait(&M.drain, 0, &dummy);
+    }
+    __syncwarp();
+  } else {
+    const int quarter = warp & 3, half = warp >> 2;  // query rows 32 quarter.., key columns 64 half..
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const uint32_t aS = cS + lane_base + 64 * half, aP = cP + lane_base + 64 * half;
+    uint32_t n = 0, qn = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
+      const DqItem I = item(i);
+      const int t = I.t0 + quarter * 32 + lane, ta = I.t0 + quarter * 32, tb = ta + 31;
+      const int64_t ro = ((int64_t)I.b * p.Hq + I.h) * p.Npad + t;
+      const float lse2 = p.lse2[ro], dsum = p.dsum[ro];
+      for (int j = 0; j < I.kt.count; ++j, ++n) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&M.s_full[n & 1], (n >> 1) & 1u, abort))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int u0 = I.kt.tile(j) * TILE + 64 * half;  // this warp's first key
+        const bool all = u0 + 63 <= ta && (tb - u0 < p.window || u0 + 64 <= p.sinks);
+        const int hi = t - u0, lo = t - p.window - u0, sk = p.sinks - u0;  // sees lo < c <= hi, or c < sk
+        float x[64];
+        ld64(aS + TILE * (n & 1), x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 64; ++c) x[c] = ex2(fmaf(x[c], p.c, -lse2));
+        if (!__all_sync(0xffffffffu, mbar_wait(&M.dp_full, n & 1u, abort))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t y[32];
+          tmem_ld32(aP + 32 * q, y);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) x[32 * q + c] *= __uint_as_float(y[c]) - dsum;
+        }
+        if (!all) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (c > hi || (c <= lo && c >= sk)) x[c] = 0.f;
+        }
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) pk[c / 2] = pack_bf16(x[c], x[c + 1]);
+        tmem_st32(aP, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&M.ds_full);
+      }
+      if (!ok || !__all_sync(0xffffffffu, mbar_wait(&M.dq_done, qn & 1u, abort))) break;
+      ++qn;
+      tc_fence_after();
+      constexpr int W = HD / 2;
+#pragma unroll 1
+      for (int c0 = 0; c0 < W; c0 += 32) {
+        uint32_t r[32];
+        tmem_ld32(cQ + lane_base + W * half + c0, r);
+        tmem_wait_ld();
+        if (t < p.N) store32(row_ptr_w<bf16>(p.dq, I.b, I.h, t) + W * half + c0, r, p.scale);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (M.abort && threadIdx.x == 0) atomicCAS(p.status, 0, (int)SSA_ERR_TIMEOUT);
+  if (warp == WARP_MMA) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int HD>
+constexpr int dkv_smem() {
+  return DkvCfg<HD>::OFF_MISC + (int)sizeof(DkvMisc) + 1024;
+}
+template <int HD>
+constexpr int dq_smem() {
+  return DqCfg<HD>::OFF_MISC + (int)sizeof(DqMisc) + 1024;
+}
+static_assert(dkv_smem<128>() <= 232448 && dq_smem<128>() <= 232448, "shared memory of a CTA");
+
+template <int HD>
+cudaError_t launch(const WinDims& D, const WinBwdArgs& a, int32_t* status, cudaStream_t st) {
+  BwdParams p{};
+  CUtensorMap q, k, v, g;
+  if (!win_tma_map(&q, a.q, D.B, D.Hq, D.N, TILE, HD, &p.zq) || !win_tma_map(&k, a.k, D.B, D.Hkv, D.N, TILE, HD, &p.zk) ||
+      !win_tma_map(&v, a.v, D.B, D.Hkv, D.N, TILE, HD, &p.zv) || !win_tma_map(&g, a.g, D.B, D.Hq, D.N, TILE, HD, &p.zg))
+    return cudaErrorInvalidValue;
+  cudaError_t e = launch_win_bwd_pre(D, a, st);
+  if (e != cudaSuccess) return e;
+  const WinBwdLayout L = win_bwd_layout(D);
+  const ChunkPlan cp = chunk_plan<TILE>(D, kBwdChunks);
+  char* ws = static_cast<char*>(a.ws);
+  p.dq = a.dq;
+  p.dk = a.dk;
+  p.dv = a.dv;
+  p.lse2 = reinterpret_cast<const float*>(ws + L.lse2);
+  p.dsum = reinterpret_cast<const float*>(ws + L.dsum);
+  p.part = reinterpret_cast<float*>(ws + L.part);
+  p.status = status;
+  p.B = D.B;
+  p.Hq = D.Hq;
+  p.Hkv = D.Hkv;
+  p.g = D.g;
+  p.N = D.N;
+  p.Npad = L.Npad;
+  p.NT = cp.NT;
+  p.window = D.window;
+  p.sinks = D.sinks;
+  p.L = cp.L;
+  p.partials = cp.partials;
+  p.c = D.scale * kLog2e;
+  p.scale = D.scale;
+  auto dkv = win_bwd_dkv_tc_kernel<HD>;
+  if ((e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, dkv_smem<HD>())) != cudaSuccess) return e;
+  dkv<<<dim3(cp.chunks * D.Hkv, D.B), NTHREADS, dkv_smem<HD>(), st>>>(q, k, v, g, p);
+  count_launches(1);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_win_kvjoin<TILE>(D, a, cp, p.part, st)) != cudaSuccess) return e;
+  auto dq = win_bwd_dq_tc_kernel<HD>;
+  if ((e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, dq_smem<HD>())) != cudaSuccess) return e;
+  const int64_t items = (int64_t)D.B * D.Hq * cp.NT;
+  dq<<<(unsigned)(items < kCtas ? items : kCtas), NTHREADS, dq_smem<HD>(), st>>>(q, k, v, g, p);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_win_bwd_tc(const WinDims& D, const WinBwdArgs& a, int32_t* status, cudaStream_t st) {
+  return D.d == 64 ? launch<64>(D, a, status, st) : launch<128>(D, a, status, st);
+}
+
+}  // namespace ssa

@@ -1,4 +1,5 @@
-// Window attention with sinks and paged attention on CUDA cores.
+// Window attention with sinks and paged attention in fp32 on CUDA cores, and the
+// preprocess and the join of the backward for both types.
 //
 // Mathematics: the online softmax over the visible keys (base 2, scale folded in)
 // and, backward, p = 2^(x c - lse2), dx = p (g.v - D), dQ = scale dx K,
@@ -9,6 +10,8 @@
 // keys tx + 16 j: a step of four head dims is 8 16-byte shared loads (12 wavefronts) for
 // 64 multiply-adds a thread, so the FMA pipe, not shared memory, sets the pace.
 #include "win_common.cuh"
+
+#include <type_traits>
 
 namespace ssa {
 namespace {
@@ -421,7 +424,6 @@ __global__ void __launch_bounds__(NT_) win_bwd_dkv_simt_kernel(SimtBwd p) {
   float* sG = sQ + BT * Pitch<HD>::v;
   float* sS = sG + BT * Pitch<HD>::v;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int planes = p.Hkv * (int)gridDim.y;
   const int plane = (int)blockIdx.x % p.Hkv + (int)blockIdx.y * p.Hkv;
   const Chunk ch = find_chunk<BT>((int)blockIdx.x / p.Hkv, p.NT, p.L, p.grp, p.N, p.window, p.sinks);
   const int b = plane / p.Hkv, kvh = plane % p.Hkv;
@@ -470,7 +472,6 @@ __global__ void __launch_bounds__(NT_) win_bwd_dkv_simt_kernel(SimtBwd p) {
     __syncthreads();
     weighted<HD>(sS, sQ, tx, ty, dk);
   }
-  (void)planes;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int u = u0 + 4 * ty + i;
@@ -574,7 +575,7 @@ cudaError_t bwd_t(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
   cudaError_t e = launch_win_bwd_pre(D, a, st);
   if (e != cudaSuccess) return e;
   const WinBwdLayout L = win_bwd_layout(D);
-  const ChunkPlan cp = chunk_plan<BT>(D, kPagedCtas);
+  const ChunkPlan cp = chunk_plan<BT>(D, kBwdChunks);
   char* ws = static_cast<char*>(a.ws);
   SimtBwd p{};
   p.q = a.q;
@@ -664,33 +665,29 @@ cudaError_t paged_t(const PagedDims& D, const PagedArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// One of the four (type, head dim) instances.
-#define SSA_BY_TYPE(D, F, ...)                                                             \
-  ((D).dtype == SSA_BF16 ? ((D).d == 64 ? F<__nv_bfloat16, 64>(__VA_ARGS__) : F<__nv_bfloat16, 128>(__VA_ARGS__)) \
-                         : ((D).d == 64 ? F<float, 64>(__VA_ARGS__) : F<float, 128>(__VA_ARGS__)))
-
 cudaError_t launch_win_fwd_simt(const WinDims& D, const WinFwdArgs& a, cudaStream_t st) {
-  return SSA_BY_TYPE(D, fwd_t, D, a, st);
+  return D.d == 64 ? fwd_t<float, 64>(D, a, st) : fwd_t<float, 128>(D, a, st);
 }
 cudaError_t launch_win_bwd_pre(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
-  return SSA_BY_TYPE(D, pre_t, D, a, st);
+  if (D.dtype == SSA_BF16) return D.d == 64 ? pre_t<__nv_bfloat16, 64>(D, a, st) : pre_t<__nv_bfloat16, 128>(D, a, st);
+  return D.d == 64 ? pre_t<float, 64>(D, a, st) : pre_t<float, 128>(D, a, st);
 }
 cudaError_t launch_win_bwd_simt(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
-  return SSA_BY_TYPE(D, bwd_t, D, a, st);
+  return D.d == 64 ? bwd_t<float, 64>(D, a, st) : bwd_t<float, 128>(D, a, st);
 }
 cudaError_t launch_paged_simt(const PagedDims& D, const PagedArgs& a, cudaStream_t st) {
-  return SSA_BY_TYPE(D, paged_t, D, a, st);
+  return D.d == 64 ? paged_t<float, 64>(D, a, st) : paged_t<float, 128>(D, a, st);
 }
 
 template <int BTJ>
 cudaError_t launch_win_kvjoin(const WinDims& D, const WinBwdArgs& a, const ChunkPlan& p, const float* part,
                               cudaStream_t st) {
   if (p.partials == 0) return cudaSuccess;
-  if (D.dtype == SSA_BF16)
-    return D.d == 64 ? join_t<__nv_bfloat16, 64, BTJ>(D, a, p, part, st) : join_t<__nv_bfloat16, 128, BTJ>(D, a, p, part, st);
-  return D.d == 64 ? join_t<float, 64, BTJ>(D, a, p, part, st) : join_t<float, 128, BTJ>(D, a, p, part, st);
+  using T = std::conditional_t<BTJ == 128, __nv_bfloat16, float>;  // tiles of 128 tokens are the bf16 kernels'
+  return D.d == 64 ? join_t<T, 64, BTJ>(D, a, p, part, st) : join_t<T, 128, BTJ>(D, a, p, part, st);
 }
 template cudaError_t launch_win_kvjoin<64>(const WinDims&, const WinBwdArgs&, const ChunkPlan&, const float*, cudaStream_t);
+template cudaError_t launch_win_kvjoin<128>(const WinDims&, const WinBwdArgs&, const ChunkPlan&, const float*, cudaStream_t);
 
 WinBwdLayout win_bwd_layout(const WinDims& D) {
   WinBwdLayout L{};
@@ -703,8 +700,9 @@ WinBwdLayout win_bwd_layout(const WinDims& D) {
   L.dsum = o;
   o = up(o + rows * 4);
   L.part = o;
-  const ChunkPlan p = chunk_plan<BT>(D, kPagedCtas);
-  o = up(o + (size_t)D.B * D.Hkv * p.partials * 2 * BT * D.d * 4);
+  const int tile = D.dtype == SSA_BF16 ? 128 : BT;
+  const ChunkPlan p = D.dtype == SSA_BF16 ? chunk_plan<128>(D, kBwdChunks) : chunk_plan<BT>(D, kBwdChunks);
+  o = up(o + (size_t)D.B * D.Hkv * p.partials * 2 * tile * D.d * 4);
   L.bytes = o;
   return L;
 }

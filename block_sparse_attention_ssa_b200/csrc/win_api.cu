@@ -141,7 +141,11 @@ ssa_status_t ssa_bwd_window(const ssa_window_dims_t* dims, const ssa_tensor_t* Q
   if ((s = require_sm100()) != SSA_OK) return s;
   a.lse = lse;
   a.ws = ws;
-  return from_cuda(launch_win_bwd_simt(D, a, static_cast<cudaStream_t>(stream)));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (D.dtype == SSA_F32) return from_cuda(launch_win_bwd_simt(D, a, st));
+  int32_t* status = status_word();
+  if (status == nullptr) return SSA_ERR_CUDA;
+  return from_cuda(launch_win_bwd_tc(D, a, status, st));
 }
 
 size_t ssa_paged_workspace_bytes(const ssa_paged_dims_t* dims) {

@@ -189,6 +189,8 @@ __host__ __device__ __forceinline__ int query_tiles_of(int kt, int N, int window
   return (last < NT - 1 ? last : NT - 1) - kt + 1;
 }
 
+constexpr int kBwdChunks = 296;  // chunks to aim for, two per SM
+
 struct ChunkPlan {
   int L, NT, chunks, partials;  // per (batch, kv head)
 };
@@ -279,6 +281,7 @@ bool win_tma_map(CUtensorMap* map, const TensorRef& t, int64_t B, int64_t H, int
 
 // bf16 on tcgen05.
 cudaError_t launch_win_fwd_tc(const WinDims& D, const WinFwdArgs& a, int32_t* status, cudaStream_t st);
+cudaError_t launch_win_bwd_tc(const WinDims& D, const WinBwdArgs& a, int32_t* status, cudaStream_t st);
 cudaError_t launch_paged_tc(const PagedDims& D, const PagedArgs& a, int32_t* status, cudaStream_t st);
 size_t paged_tc_ws_bytes(const PagedDims& D);
 
