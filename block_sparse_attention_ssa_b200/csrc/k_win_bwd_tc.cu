@@ -56,24 +56,26 @@ struct BwdParams {
   float c, scale;      // c = scale * log2(e)
 };
 
-// D (128 x 128) = A B^T over HD, both K-major tiles in shared memory.
+// D (128 x 128) = A B^T over HD, both K-major tiles in shared memory (low descriptor words).
 template <int HD>
 __device__ __forceinline__ void mma_logits(uint32_t d, uint32_t a, uint32_t b) {
 #pragma unroll
   for (int kk = 0; kk < HD / 16; ++kk) {
-    const uint32_t o = (kk >> 2) * HALF + (kk & 3) * 32;
-    mma_ss(d, smem_desc_sw128(a + o, 16, 1024), smem_desc_sw128(b + o, 16, 1024), Cfg<HD>::IDESC_S, kk > 0 ? 1u : 0u);
+    const uint32_t o = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+    mma_ss_lo(d, a + o, b + o, Cfg<HD>::IDESC_S, kk > 0 ? 1u : 0u);
   }
 }
+__device__ __forceinline__ uint32_t kmajor(uint32_t saddr) { return desc_lo(saddr, 16); }
+__device__ __forceinline__ uint32_t mnmajor(uint32_t saddr) { return desc_lo(saddr, HALF); }
 
 // D (128 x HD) (+)= A B, A 128 x 128 as bf16 pairs in TMEM (reduction 0-63 in columns a.., 64-127 in
-// a + 64..), B 128 rows (the reduction) of a tile in shared memory.
+// a + 64..), B 128 rows (the reduction) of a tile in shared memory (low descriptor word).
 template <int HD>
 __device__ __forceinline__ void mma_grad(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
+  const uint32_t acc = accumulate ? 1u : 0u;
 #pragma unroll
   for (int kk = 0; kk < TILE / 16; ++kk)
-    mma_ts(d, a + 64 * (kk >> 2) + 8 * (kk & 3), smem_desc_sw128(b + kk * 2048, HALF, 1024), Cfg<HD>::IDESC_ACC,
-           (accumulate || kk > 0) ? 1u : 0u);
+    mma_ts_lo(d, a + 64 * (kk >> 2) + 8 * (kk & 3), b + kk * 128, Cfg<HD>::IDESC_ACC, kk > 0 ? 1u : acc);
 }
 
 template <int HD>
@@ -195,14 +197,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
   } else if (warp == WARP_MMA) {
     if (lane == 0) {
-      const uint32_t ak = smem_u32(sK), av = smem_u32(sV);
+      const uint32_t ak = kmajor(smem_u32(sK)), av = kmajor(smem_u32(sV));
       auto have = [&](int j) { return mbar_wait(&M.q_full[j % C::NS], (uint32_t)(j / C::NS) & 1u, abort); };
       auto s_of = [&](int j) {
-        mma_logits<HD>(cS, ak, smem_u32(stage(j)));
+        mma_logits<HD>(cS, ak, kmajor(smem_u32(stage(j))));
         tc_commit(&M.s_full);
       };
       auto dp_of = [&](int j) {
-        mma_logits<HD>(cP, av, smem_u32(stage(j)) + C::TB);
+        mma_logits<HD>(cP, av, kmajor(smem_u32(stage(j)) + C::TB));
         tc_commit(&M.dp_full);
       };
       bool ok = mbar_wait(&M.kv_full, 0, abort) && have(0);
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int j = 0; ok && j < T; ++j) {
         if (!(ok = mbar_wait(&M.p_full, (uint32_t)j & 1u, abort))) break;
         tc_fence_after();
-        mma_grad<HD>(cV, cS, smem_u32(stage(j)) + C::TB, j > 0);
+        mma_grad<HD>(cV, cS, mnmajor(smem_u32(stage(j)) + C::TB), j > 0);
         if (j + 1 < T) {
           if (!(ok = have(j + 1))) break;
           tc_fence_after();
@@ -222,7 +224,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         if (!(ok = mbar_wait(&M.ds_full, (uint32_t)j & 1u, abort))) break;
         tc_fence_after();
-        mma_grad<HD>(cK, cP, smem_u32(stage(j)), j > 0);
+        mma_grad<HD>(cK, cP, mnmajor(smem_u32(stage(j))), j > 0);
         tc_commit(&M.q_empty[j % C::NS]);
         if (j + 1 < T) dp_of(j + 1);
       }
@@ -465,20 +467,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
   } else if (warp == WARP_MMA) {
     if (lane == 0) {
-      const uint32_t aq = smem_u32(sQ), ag = smem_u32(sG), ak = smem_u32(sK), av = smem_u32(sV);
+      const uint32_t aq = kmajor(smem_u32(sQ)), ag = kmajor(smem_u32(sG)), ak = kmajor(smem_u32(sK)), av = kmajor(smem_u32(sV));
+      const uint32_t bk = mnmajor(smem_u32(sK));
       uint32_t n = 0, qn = 0;  // key tiles and items so far
       bool ok = true;
       auto s_of = [&](uint32_t k) {
         if (!mbar_wait(&M.k_full[k % C::NSK], (k / C::NSK) & 1u, abort)) return false;
         tc_fence_after();
-        mma_logits<HD>(cS + TILE * (k & 1), aq, ak + (k % C::NSK) * C::TB);
+        mma_logits<HD>(cS + TILE * (k & 1), aq, ak + (k % C::NSK) * (C::TB >> 4));
         tc_commit(&M.s_full[k & 1]);
         return true;
       };
       auto dp_of = [&](uint32_t k, bool last) {
         if (!mbar_wait(&M.v_full[k % C::NSV], (k / C::NSV) & 1u, abort)) return false;
         tc_fence_after();
-        mma_logits<HD>(cP, ag, av + (k % C::NSV) * C::TB);
+        mma_logits<HD>(cP, ag, av + (k % C::NSV) * (C::TB >> 4));
         tc_commit(&M.dp_full);
         tc_commit(&M.v_empty[k % C::NSV]);
         if (last) tc_commit(&M.q_empty);
@@ -494,7 +497,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (j + 1 < T && !(ok = s_of(n + 1))) break;
           if (!(ok = mbar_wait(&M.ds_full, n & 1u, abort))) break;
           tc_fence_after();
-          mma_grad<HD>(cQ, cP, ak + (n % C::NSK) * C::TB, j > 0);
+          mma_grad<HD>(cQ, cP, bk + (n % C::NSK) * (C::TB >> 4), j > 0);
           tc_commit(&M.k_empty[n % C::NSK]);
           if (j + 1 == T) tc_commit(&M.dq_done);
           if (j + 1 < T) ok = dp_of(n + 1, j + 2 == T);

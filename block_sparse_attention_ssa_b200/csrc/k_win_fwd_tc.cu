@@ -8,13 +8,21 @@
 // the row), its sum is taken before the rounding.
 //
 // A persistent CTA per SM walks work items of up to 256 query rows in two slots of 128
-// (TMEM lanes): warps 0-3 hold slot 0's softmax, warps 4-7 slot 1's, warp 8 loads by TMA,
-// warp 9 issues the products.  While one slot's softmax works, the tensor core runs the
-// other slot's products; the key tiles (128 keys) are shared by both.  TMEM: O of slot s
-// at HD s, S of slot s at 256 + 128 s; P (bf16 pairs) overwrites the second half of S and
-// feeds P V from TMEM.  An item whose rows fit one slot gives the odd key tiles to slot 1
-// with the same queries, and slot 0's warps join the two softmaxes at the end, so that a
-// decoding step has two chains in flight too.
+// (TMEM lanes).  Key tiles of 128 keys are shared by both slots; a step is half a tile, 64
+// keys.  Warps 4 (2 s + h) .. + 3 hold the softmax of half h of slot s's tiles, warp 16 loads
+// by TMA, one thread of warps 17 and 18 issues the products of slot 0 and slot 1 (one issuer
+// for both spent more cycles on its control flow than the products take).  TMEM: O of slot s
+// at HD s, its two S buffers of 64 columns at 256 + 128 s; P (bf16 pairs) overwrites the second
+// half of its S buffer and feeds P V from TMEM.  The next tile's logits are issued behind P V
+// of the same half, so they are ready when the softmax warps come to them.
+// A row's two softmax threads share one running maximum: a step's thread takes the one that
+// the step before published, publishes its own before it forms any exponential, and keeps its
+// own sum, so that only the maxima form a chain and four warps per scheduler hide the latency
+// of the exponentials (with one thread per row and two warps the schedulers issued in 35 % of
+// the cycles and a tile of both slots took 4200 of them).
+// An item whose rows fit one slot gives the odd key tiles to slot 1 with the same queries,
+// and slot 0's warps join the two softmaxes at the end, so that a decoding step has four
+// chains in flight too.
 //
 // Rows.  Window form: a row is a token of one query head.  Paged form: a row is a
 // (new token, head of the group) pair, so the g heads of a kv head share each K/V load
@@ -31,8 +39,10 @@ using namespace sm100;
 using bf16 = __nv_bfloat16;
 
 constexpr int TILE = 128;
-constexpr int NTHREADS = 320;
-constexpr int WARP_TMA = 8, WARP_MMA = 9;
+constexpr int UNIT = 64;  // keys of a step
+constexpr int NTHREADS = 640;
+constexpr int WARP_TMA = 16, WARP_MMA = 17;  // and WARP_MMA + 1 for slot 1; the last warp only fills its group
+
 constexpr int kCtas = 148;     // one per SM
 constexpr int kMinUnits = 4;   // key tiles worth a CTA of their own
 constexpr float kRescaleThreshold = 8.0f;
@@ -46,19 +56,27 @@ struct Cfg {
   static constexpr int TB = TILE * HD * 2;
   static constexpr int HALF = TILE * 128;  // 64 columns of a tile: 128 rows of 128 bytes
   static constexpr int OFF_K = 2 * TB, OFF_V = OFF_K + NSK * TB, OFF_MISC = OFF_V + NSV * TB;
-  static constexpr uint32_t IDESC_S = idesc_bf16_f32(TILE, TILE, false, false);
+  static constexpr uint32_t IDESC_S = idesc_bf16_f32(TILE, UNIT, false, false);
   static constexpr uint32_t IDESC_PV = idesc_bf16_f32(TILE, HD, false, true);
 };
 
 struct Misc {
   uint64_t q_full, q_empty, k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t s_full[2], p_full[2], pv_done[2], join_ready, join_done, drain;
+  // by half: who waits for a step knows the same half's step before done, and a barrier tells only
+  // neighbouring phases apart
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];
+  uint64_t m_ready[2][2][4];        // a warp's running maxima are published
+  uint64_t sum_ready[2][4], total_ready[2][4];
+  uint64_t o_free[2];               // O of the slot has been read
+  uint64_t join_ready, join_done, drain[2];
   uint32_t tmem_base;
   int abort;
+  int turn;  // 1 while an issuer feeds the tensor core
   int left;
   Place at;
   uint32_t bad[8];  // pages missing from a key tile, a bit per 16 keys (ring of 2 NSK tiles)
-  float jm[TILE], jl[TILE];
+  float mref[2][TILE];  // running maximum of each row
+  float sum[2][TILE];   // at an item's end: the first half's sum, then the whole one
 };
 
 struct TcParams {
@@ -69,6 +87,7 @@ struct TcParams {
   int zk, zv, zq;    // broadcast dimensions of K, V, Q: bit 0 batch, bit 1 head
   int rows_item;     // window form: tokens of an item (256, or 128 when those would leave SMs idle)
   float c;           // scale * log2(e)
+  bool wide;         // h in 32-byte pieces
   // paged form
   const int32_t* table;
   Batch batch;
@@ -76,75 +95,97 @@ struct TcParams {
   float* part;
 };
 
-// One work item as its roles see it.
+// One work item as a role of slot s sees it.
 struct Item {
-  int b, kvh, head0, row0, p0, g;   // row0: first token (window) or packed row (paged); p0: its position
-  int toks0, toks1;                 // tokens of the two slots
-  int T, off, seg, units;           // key tiles of this CTA's share, the first one's index
-  bool two, cut;                    // both slots hold rows; share of an item only
+  int b, kvh, head0, row0, p0, g;  // row0: first token (window) or packed row (paged); p0: its position
+  int toks, toks0;                 // tokens of the item and of slot 0
+  int T, off, seg, units;          // key tiles of this CTA's share, the first one's index
+  bool two, cut;                   // both slots hold rows; share of an item only
   KeyTiles kt;
-  int ns0, lo0, hi0, ns1, lo1, hi1; // two: the tiles that each slot sees
-  int step;                         // tokens of a full slot
+  // Two slots of rows: the slot uses the share's tiles j < A and B <= j < E (its sinks, its window),
+  // the other one j < oA and oB <= j < oE; every tile is used by one of them.  Alone, the slots take
+  // the tiles in turn.
+  int s, A, B, E, oA, oB, oE;
   __device__ __forceinline__ int tile(int j) const { return kt.tile(off + j); }
-  __device__ __forceinline__ bool active(int s, int j) const {
-    if (!two) return (j & 1) == s;
-    const int t = tile(j);
-    return t < (s ? ns1 : ns0) || (t >= (s ? lo1 : lo0) && t <= (s ? hi1 : hi0));
-  }
-  __device__ __forceinline__ int next(int s, int j) const {
-    while (j < T && !active(s, j)) ++j;
-    return j;
+  __device__ __forceinline__ bool shared(int j) const { return two && (j < oA || (j >= oB && j < oE)); }
+  __device__ __forceinline__ int next(int j) const {  // the slot's first tile at or after j (T: none)
+    if (!two) return min(j + ((j ^ s) & 1), T);
+    if (j >= A) {
+      j = max(j, B);
+      if (j >= E) j = T;
+    }
+    return min(j, T);
   }
 };
 
+// Waits (bounded) until the other issuer has left the tensor core's queue.
+__device__ __forceinline__ bool take_turn(Misc& M, volatile int* abort) {
+  if (atomicCAS(&M.turn, 0, 1) == 0) return true;
+  const long long t0 = clock64();
+  while (atomicCAS(&M.turn, 0, 1) != 0) {
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ void pass_turn(Misc& M) { atomicExch(&M.turn, 0); }
+
+// 16 bf16 values to memory: one 32-byte store where base and strides allow it (a full sector a lane; two
+// 16-byte ones take the store path twice).
+__device__ __forceinline__ void store32b(bf16* dst, const uint32_t (&v)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// The CTA's items in order.
 template <bool PAGED>
 struct Walk {
   const TcParams& p;
   Place at;
-  int left, idx, seg;
-  __device__ Walk(const TcParams& p_, const Misc& M) : p(p_), at(M.at), left(M.left), idx(blockIdx.x), seg(0) {}
+  int left, idx, seg, s;
+  __device__ Walk(const TcParams& p_, const Misc& M, int s_) : p(p_), at(M.at), left(M.left), idx(blockIdx.x), seg(0), s(s_) {}
 
   __device__ bool next(Item& I) {
     int toks, cap;
     if (PAGED) {
       if (left <= 0 || at.b >= p.batch.seqs) return false;
-      const Seq s = load_seq(p.batch.q_start, p.batch.kv_len, at.b, p.batch.T, p.batch.cap);
+      const Seq q = load_seq(p.batch.q_start, p.batch.kv_len, at.b, p.batch.T, p.batch.cap);
       const int i0 = at.run * p.batch.TI;
-      toks = min(p.batch.TI, s.n - i0);
+      toks = min(p.batch.TI, q.n - i0);
       cap = p.TQ;
       I.b = at.b;
       I.kvh = at.kvh;
       I.head0 = at.kvh * p.g;
       I.g = p.g;
-      I.row0 = s.q0 + i0;
-      I.p0 = s.len - s.n + i0;
+      I.row0 = q.q0 + i0;
+      I.p0 = q.len - q.n + i0;
     } else {
       const int planes = p.B * p.Hq, runs = (p.N + p.rows_item - 1) / p.rows_item;
       if (idx >= planes * runs) return false;
-      const int plane = idx % planes;
-      I.row0 = I.p0 = (runs - 1 - idx / planes) * p.rows_item;
+      const int run = idx / planes, plane = idx - run * planes;
+      I.row0 = I.p0 = (runs - 1 - run) * p.rows_item;
       toks = min(p.rows_item, p.N - I.p0);
       cap = TILE;
       I.b = plane / p.Hq;
-      I.head0 = plane % p.Hq;
+      I.head0 = plane - I.b * p.Hq;
       I.kvh = I.head0 / p.g;
       I.g = 1;
       idx += gridDim.x;
     }
-    I.step = cap;
+    I.s = s;
+    I.toks = toks;
     I.toks0 = min(toks, cap);
-    I.toks1 = toks - I.toks0;
-    I.two = I.toks1 > 0;
+    I.two = toks > cap;
     I.kt = key_tiles<TILE>(I.p0, I.p0 + toks - 1, p.window, p.sinks);
-    const int e0 = I.p0 + I.toks0 - 1, e1 = I.p0 + toks - 1;
-    const KeyTiles k0 = key_tiles<TILE>(I.p0, e0, p.window, p.sinks);
-    const KeyTiles k1 = key_tiles<TILE>(I.p0 + cap, e1, p.window, p.sinks);
-    I.ns0 = k0.ns;
-    I.lo0 = k0.lo;
-    I.hi0 = k0.count > 0 ? e0 / TILE : -1;
-    I.ns1 = k1.ns;
-    I.lo1 = k1.lo;
-    I.hi1 = k1.count > 0 ? e1 / TILE : -1;
     I.units = max(1, I.kt.count);
     I.off = 0;
     int take = I.units;
@@ -157,13 +198,22 @@ struct Walk {
         at.kvh = 0;
         ++at.run;
         while (at.b < p.batch.seqs) {
-          const Seq s = load_seq(p.batch.q_start, p.batch.kv_len, at.b, p.batch.T, p.batch.cap);
-          if (at.run * p.batch.TI < s.n) break;
+          const Seq q = load_seq(p.batch.q_start, p.batch.kv_len, at.b, p.batch.T, p.batch.cap);
+          if (at.run * p.batch.TI < q.n) break;
           at.run = 0;
           ++at.b;
         }
       }
     }
+    auto own = [&](int first, int last, int& A, int& B, int& E) {
+      const KeyTiles k = key_tiles<TILE>(first, last, p.window, p.sinks);
+      A = (k.ns > I.kt.lo ? I.kt.ns + k.ns - I.kt.lo : k.ns) - I.off;
+      B = I.kt.ns + k.lo - I.kt.lo - I.off;
+      E = k.count > 0 ? I.kt.ns + last / TILE - I.kt.lo + 1 - I.off : 0;
+    };
+    const int f = s ? cap : 0, e = s ? toks : I.toks0;  // tokens of the slot and of the other one
+    own(I.p0 + f, I.p0 + e - 1, I.A, I.B, I.E);
+    own(I.p0 + cap - f, I.p0 + toks + I.toks0 - e - 1, I.oA, I.oB, I.oE);
     I.cut = take < I.units;
     I.T = I.kt.count > 0 ? take : 0;
     I.seg = seg++;
@@ -176,32 +226,45 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     win_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TcParams p) {
   using C = Cfg<HD>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw;  // tiles need 1024-byte alignment: checked below
   Misc& M = *reinterpret_cast<Misc*>(smem + C::OFF_MISC);
   volatile int* abort = &M.abort;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
 
+  if (smem_u32(smem_raw) & 1023u) {  // no room for slack: shared memory starts on a 1024-byte boundary
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, (int)SSA_ERR_CUDA);
+    return;
+  }
   if (threadIdx.x == 0) {
     mbar_init(&M.q_full, 1);
-    mbar_init(&M.q_empty, 1);
+    mbar_init(&M.q_empty, 2);
     for (int i = 0; i < C::NSK; ++i) {
       mbar_init(&M.k_full[i], 1);
-      mbar_init(&M.k_empty[i], 1);
+      mbar_init(&M.k_empty[i], 2);  // each slot's issuer, or the only user of the tile twice
     }
     for (int i = 0; i < C::NSV; ++i) {
       mbar_init(&M.v_full[i], 1);
-      mbar_init(&M.v_empty[i], 1);
+      mbar_init(&M.v_empty[i], 2);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&M.s_full[s], 1);
-      mbar_init(&M.p_full[s], 4);
-      mbar_init(&M.pv_done[s], 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&M.s_full[s][i], 1);
+        mbar_init(&M.p_full[s][i], 4);
+        mbar_init(&M.pv_done[s][i], 1);
+        for (int w = 0; w < 4; ++w) mbar_init(&M.m_ready[s][i][w], 1);
+      }
+      for (int w = 0; w < 4; ++w) {
+        mbar_init(&M.sum_ready[s][w], 1);
+        mbar_init(&M.total_ready[s][w], 1);
+      }
+      mbar_init(&M.o_free[s], 8);
+      mbar_init(&M.drain[s], 1);
     }
-    mbar_init(&M.join_ready, 4);
-    mbar_init(&M.join_done, 4);
-    mbar_init(&M.drain, 1);
+    mbar_init(&M.join_ready, 8);
+    mbar_init(&M.join_done, 8);
     M.abort = 0;
+    M.turn = 0;
     fence_mbar_init();
   }
   if (warp == WARP_MMA) {
@@ -227,7 +290,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint8_t* sQ = smem;
   uint8_t* sK = smem + C::OFF_K;
   uint8_t* sV = smem + C::OFF_V;
-  Walk<PAGED> walk(p, M);
+  Walk<PAGED> walk(p, M, warp < WARP_TMA ? warp >> 3 : (warp == WARP_MMA + 1 ? 1 : 0));
   Item I;
   uint32_t base = 0;  // key tiles before this item
 
@@ -257,7 +320,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
       }
       ++q_issued;
-      const int pmax = I.p0 + I.toks0 + I.toks1 - 1, lo_min = I.p0 - p.window + 1;
+      const int pmax = I.p0 + I.toks - 1, lo_min = I.p0 - p.window + 1;
       // One key tile: its pages, a copy per lane (a page, or its half of the columns).
       auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int t, int zero, uint32_t* bad) {
         if (!PAGED) {
@@ -325,146 +388,159 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       dummy = 0;
       mbar_wait(&M.v_full[n % C::NSV], (n / C::NSV) & 1u, &dummy);
     }
-  } else if (warp == WARP_MMA) {
-    // ================================================================ MMA issuer (lane 0 issues)
-    const uint32_t aq = smem_u32(sQ), ak = smem_u32(sK), av = smem_u32(sV);
-    uint32_t items = 0, pc0 = 0, pc1 = 0;  // P tiles of each slot so far
-    bool ok = true;
-    while (ok && walk.next(I)) {
-      if (I.T == 0) continue;
-      if (!__all_sync(0xffffffffu, mbar_wait(&M.q_full, items & 1u, abort))) break;
-      ++items;
-      const int pmax = I.p0 + I.toks0 + I.toks1 - 1, lo_min = I.p0 - p.window + 1;
-      uint32_t half_read = 0;  // key tiles (mod 32) whose first of two logit products is issued
-      int nx0 = I.next(0, 0), nx1 = I.next(1, 0);
-      bool started0 = false, started1 = false;
-      auto issue_s = [&](int s) {
-        const int j = s ? nx1 : nx0;
-        const uint32_t n = base + j;
-        const int sk = (int)(n % C::NSK);
-        if (!__all_sync(0xffffffffu, mbar_wait(&M.k_full[sk], (n / C::NSK) & 1u, abort))) return false;
-        tc_fence_after();
-        const bool both = I.active(0, j) && I.active(1, j);
-        const bool last = !both || ((half_read >> (j & 31)) & 1u);
-        if (both) half_read ^= 1u << (j & 31);
-        const int nxt = I.next(s, j + 1);
-        if (s) nx1 = nxt; else nx0 = nxt;
-        if (lane == 0) {
-          const uint32_t q = aq + (I.two ? s * C::TB : 0);
+  } else if (warp == WARP_MMA || warp == WARP_MMA + 1) {
+    // ================================================================ MMA issuer of slot s
+    if (elect_one()) {
+      const int s = warp - WARP_MMA;
+      const uint32_t aq = desc_lo(smem_u32(sQ), 16), ak = desc_lo(smem_u32(sK), 16), av = desc_lo(smem_u32(sV), C::HALF);
+      const uint32_t cS = tmem + COL_S + TILE * s, cO = tmem + HD * s;
+      uint32_t items = 0, np = 0, outs = 0;  // items, tiles and items with tiles of the slot so far
+      bool ok = true;
+      // Logits of a tile's half, and P V of it.
+      auto logits = [&](uint32_t q, uint32_t k, int half) {
 #pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk) {
-            const uint32_t o = (kk >> 2) * C::HALF + (kk & 3) * 32;
-            mma_ss(tmem + COL_S + TILE * s, smem_desc_sw128(q + o, 16, 1024),
-                   smem_desc_sw128(ak + sk * C::TB + o, 16, 1024), C::IDESC_S, kk > 0 ? 1u : 0u);
-          }
-          tc_commit(&M.s_full[s]);
-          if (last) tc_commit(&M.k_empty[sk]);
-          if (nx0 >= I.T && nx1 >= I.T) tc_commit(&M.q_empty);
+        for (int kk = 0; kk < HD / 16; ++kk) {
+          const uint32_t o = ((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4;
+          mma_ss_lo(cS + UNIT * half, q + o, k + half * (UNIT * 128 >> 4) + o, C::IDESC_S, kk > 0 ? 1u : 0u);
         }
-        __syncwarp();
-        return true;
+        tc_commit(&M.s_full[s][half]);
       };
-      const int f = nx0 <= nx1 ? 0 : 1;
-      if ((f ? nx1 : nx0) < I.T) ok = issue_s(f);
-      if (ok && (f ? nx0 : nx1) < I.T) ok = issue_s(1 - f);
-      for (int j = 0; ok && j < I.T; ++j) {
-        const uint32_t n = base + j;
-        const int sv = (int)(n % C::NSV);
-        bool fixed = !PAGED;
-        const bool second = I.active(1, j);
-        const bool first = I.active(0, j);
-        for (int s = 0; ok && s < 2; ++s) {
-          if (!(s ? second : first)) continue;
-          if (!__all_sync(0xffffffffu, mbar_wait(&M.v_full[sv], (n / C::NSV) & 1u, abort))) {
-            ok = false;
-            break;
-          }
-          if (!fixed) {
-            // V rows that no query sees may hold anything (NaN times a zero weight is NaN): zeros instead
-            const int u0 = I.tile(j) * TILE;
-            if (u0 + TILE - 1 > pmax || (u0 < lo_min && u0 + TILE > p.sinks)) {
-              for (int e = lane; e < TILE * (HD / 64) * 8; e += 32) {
-                const int r = (e >> 3) % TILE, u = u0 + r;
-                if (u > pmax || (u < lo_min && u >= p.sinks))
-                  *reinterpret_cast<uint4*>(sV + sv * C::TB + (e >> 3) / TILE * C::HALF + r * 128 + (e & 7) * 16) =
-                      make_uint4(0u, 0u, 0u, 0u);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
-            fixed = true;
-          }
-          if (!__all_sync(0xffffffffu, mbar_wait(&M.p_full[s], (s ? pc1 : pc0) & 1u, abort))) {
-            ok = false;
-            break;
-          }
-          if (s) ++pc1; else ++pc0;
-          tc_fence_after();
-          if (lane == 0) {
+      auto weighted = [&](uint32_t v, int half, uint32_t acc) {
 #pragma unroll
-            for (int kk = 0; kk < TILE / 16; ++kk)
-              mma_ts(tmem + HD * s, tmem + COL_S + TILE * s + 64 + 8 * kk,
-                     smem_desc_sw128(av + sv * C::TB + kk * 2048, C::HALF, 1024), C::IDESC_PV,
-                     ((s ? started1 : started0) || kk > 0) ? 1u : 0u);
-            tc_commit(&M.pv_done[s]);
-            if (s == 1 || !second) tc_commit(&M.v_empty[sv]);
-          }
-          __syncwarp();
-          if (s) started1 = true; else started0 = true;
-          if ((s ? nx1 : nx0) < I.T) ok = issue_s(s);
+        for (int kk = 0; kk < UNIT / 16; ++kk)
+          mma_ts_lo(cO, cS + UNIT * half + 32 + 8 * kk, v + (4 * half + kk) * 128, C::IDESC_PV, kk > 0 ? 1u : acc);
+        tc_commit(&M.pv_done[s][half]);
+      };
+      auto release = [&](uint64_t* bar, int j) {
+        tc_commit(bar);
+        if (!I.shared(j)) tc_commit(bar);
+      };
+      while (ok && walk.next(I)) {
+        if (I.T == 0) continue;
+        if (!mbar_wait(&M.q_full, items & 1u, abort)) break;
+        ++items;
+        const uint32_t q = aq + (I.two ? s * (C::TB >> 4) : 0);
+        int j = I.next(0);
+        if (j < I.T) {
+          const uint32_t n = base + j, sk = n % C::NSK;
+          if (!(ok = mbar_wait(&M.k_full[sk], (n / C::NSK) & 1u, abort))) break;
+          tc_fence_after();
+          logits(q, ak + sk * (C::TB >> 4), 0);
+          logits(q, ak + sk * (C::TB >> 4), 1);
+          release(&M.k_empty[sk], j);
+        } else {
+          mbar_arrive(&M.q_empty);  // no tile of this share is the slot's
         }
+        if (j < I.T) {  // the item before has read O by the time this one's first P V is due
+          if (outs > 0 && !(ok = mbar_wait(&M.o_free[s], (outs - 1) & 1u, abort))) break;
+          ++outs;
+        }
+        for (uint32_t acc = 0; j < I.T; acc = 1) {
+          const int nj = I.next(j + 1);
+          const uint32_t n = base + j, sv = n % C::NSV, nn = base + nj, sk = nn % C::NSK;
+          const uint32_t v = av + sv * (C::TB >> 4), k = ak + sk * (C::TB >> 4);
+          if (nj >= I.T) tc_commit(&M.q_empty);  // the last logits are issued
+          if (!(ok = mbar_wait(&M.v_full[sv], (n / C::NSV) & 1u, abort) && mbar_wait(&M.p_full[s][0], np & 1u, abort))) break;
+          const bool more = nj < I.T;
+          auto k_there = [&] { return !more || mbar_wait(&M.k_full[sk], (nn / C::NSK) & 1u, abort); };
+          if (I.two) {
+            // P V of a half and the next logits of that half go in one piece: interleaved with the other slot's,
+            // all four softmax groups would wait for one another's products and then work side by side while
+            // the tensor core idles.  Everything awaited is there before the turn is taken.
+            if (!(ok = k_there() && take_turn(M, abort))) break;
+            tc_fence_after();
+            weighted(v, 0, acc);
+            if (more) logits(q, k, 0);
+            pass_turn(M);
+            if (!(ok = mbar_wait(&M.p_full[s][1], np & 1u, abort) && take_turn(M, abort))) break;
+            tc_fence_after();
+            weighted(v, 1, 1u);
+            if (more) logits(q, k, 1);
+            pass_turn(M);
+          } else {
+            // Few rows: bound by the loads, so V is released as early as its P allows, whether or not the
+            // next K has arrived.
+            tc_fence_after();
+            weighted(v, 0, acc);
+            if (!(ok = mbar_wait(&M.p_full[s][1], np & 1u, abort))) break;
+            tc_fence_after();
+            weighted(v, 1, 1u);
+          }
+          release(&M.v_empty[sv], j);
+          if (more && !I.two) {
+            if (!(ok = k_there())) break;
+            tc_fence_after();
+            logits(q, k, 0);
+            logits(q, k, 1);
+          }
+          if (more) release(&M.k_empty[sk], nj);
+          ++np;
+          j = nj;
+        }
+        base += I.T;
       }
-      base += I.T;
-    }
-    if (lane == 0) {
-      tc_commit(&M.drain);
+      tc_commit(&M.drain[s]);
       int dummy = 0;
-      mbar_wait(&M.drain, 0, &dummy);
+      mbar_wait(&M.drain[s], 0, &dummy);
     }
     __syncwarp();
-  } else {
+  } else if (warp < WARP_TMA) {
     // ================================================================ softmax
-    const int s = warp >> 2;
-    const int row = (warp & 3) * 32 + lane;  // row of the slot == TMEM lane
-    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t s_addr = lane_base + COL_S + TILE * s, o_addr = lane_base + HD * s;
-    uint32_t sc = 0, joins = 0;  // logit tiles and joined items so far
+    const int s = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
+    const int row = quarter * 32 + lane;  // row of the slot == TMEM lane
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t s_addr = lane_base + COL_S + TILE * s + UNIT * half;
+    float* mref = &M.mref[s][row];
+    // V rows that no query of the item sees may hold anything (NaN times a zero weight is NaN): zeros in
+    // shared memory instead, before this slot's weights go to the product.  Both slots may write them.
+    auto clear_v = [&](const Item& I, int j) {
+      const int u0 = I.tile(j) * TILE, pmax = I.p0 + I.toks - 1, lo_min = I.p0 - p.window + 1;
+      if (u0 + TILE - 1 <= pmax && (u0 >= lo_min || u0 + TILE <= p.sinks)) return;
+      const uint32_t n = base + j;
+      if (!mbar_wait(&M.v_full[n % C::NSV], (n / C::NSV) & 1u, abort)) return;  // noticed at the next wait
+      uint8_t* sv = sV + (n % C::NSV) * C::TB;
+      for (int e = threadIdx.x & 127; e < TILE * (HD / 64) * 8; e += 128) {
+        const int r = (e >> 3) % TILE, u = u0 + r;
+        if (u > pmax || (u < lo_min && u >= p.sinks))
+          *reinterpret_cast<uint4*>(sv + (e >> 3) / TILE * C::HALF + r * 128 + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u, abort)) != 0; };
+    uint32_t tc = 0, mc = 0, outs = 0, joins = 0;  // tiles; the warp's tiles and items with rows; joined items
     bool ok = true;
     while (ok && walk.next(I)) {
       const int g = I.g;
-      const int nrows = (s && I.two ? I.toks1 : I.toks0) * g;
-      const int pbase = I.p0 + (s && I.two ? I.step : 0);
-      const int pos = pbase + row / g;
-      const int r0 = (warp & 3) * 32, rlast = min(r0 + 31, nrows - 1);
+      const int shift = s && I.two ? I.toks0 : 0;  // the slot's first token within the item
+      const int nrows = (s && I.two ? I.toks - I.toks0 : I.toks0) * g;
+      const int pbase = I.p0 + shift;
+      const int r0 = quarter * 32, rlast = min(r0 + 31, nrows - 1);
       const bool live = r0 < nrows;  // the warp holds rows
-      const int wmin = pbase + r0 / g, wmax = pbase + rlast / g;
-      float m = kNegInf, l = 0.f;
-      int steps = 0;
-      for (int j = 0; j < I.T; ++j) {
-        if (!I.active(s, j)) continue;
-        if (!__all_sync(0xffffffffu, mbar_wait(&M.s_full[s], sc & 1u, abort))) {
-          ok = false;
-          break;
-        }
+      auto token = [&](int r) { return PAGED ? r / g : r; };
+      const int pos = pbase + token(row), wmin = pbase + token(r0), wmax = pbase + token(rlast);
+      float m = kNegInf, l = 0.f;  // the reference of this thread's sum, and the sum
+      bool any = false;            // a tile of this share is the slot's
+      for (int j = I.next(0); j < I.T; j = I.next(j + 1)) {
+        if (!(ok = wait(&M.s_full[s][half], tc))) break;
         tc_fence_after();
+        if (PAGED && half == 0) clear_v(I, j);
         if (live) {
-          const int u0 = I.tile(j) * TILE;
-          const uint32_t bad = PAGED ? M.bad[(base + j) & 7] : 0u;
-          const bool none = u0 > wmax || (u0 + TILE - 1 <= wmin - p.window && u0 >= p.sinks);
-          const bool all = u0 + TILE - 1 <= wmin && (u0 > wmax - p.window || u0 + TILE <= p.sinks) && bad == 0;
-          // 64 logits at a time stay in registers: the first half is read for its maximum and once
-          // more for its weights, the second half once.
-          float x[64];
-          auto load_half = [&](int q) {
-            tmem_ld32(s_addr + 64 * q, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
-            tmem_ld32(s_addr + 64 * q + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+          const int u0 = I.tile(j) * TILE + half * UNIT;
+          const uint32_t bad = PAGED ? (M.bad[(base + j) & 7] >> (half * 4)) & 15u : 0u;
+          const bool none = u0 > wmax || (u0 + UNIT - 1 <= wmin - p.window && u0 >= p.sinks);
+          const bool all = u0 + UNIT - 1 <= wmin && (u0 > wmax - p.window || u0 + UNIT <= p.sinks) && bad == 0;
+          // 32 logits at a time stay in registers (96 a thread): the first half of them is read for its
+          // maximum and once more for its weights.
+          float x[32];
+          auto load = [&](int q) {
+            tmem_ld32(s_addr + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
             tmem_wait_ld();
             if (!all) {
-              const int v0 = u0 + 64 * q;
+              const int v0 = u0 + 32 * q;
               const int hi = pos - v0, lo = pos - p.window - v0, sk = p.sinks - v0;  // sees lo < c <= hi, or c < sk
-              const uint32_t gone = bad >> (4 * q);
+              const uint32_t gone = bad >> (2 * q);
 #pragma unroll
-              for (int c = 0; c < 64; ++c)
+              for (int c = 0; c < 32; ++c)
                 if (c > hi || (c <= lo && c >= sk) || ((gone >> (c >> 4)) & 1u)) x[c] = kNegInf;
             }
           };
@@ -472,162 +548,201 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (!none) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              load_half(q);
+              load(q);
 #pragma unroll
-              for (int c = 0; c < 64; c += 4) {
-                a0 = fmaxf(a0, x[c]);
-                a1 = fmaxf(a1, x[c + 1]);
-                a2 = fmaxf(a2, x[c + 2]);
-                a3 = fmaxf(a3, x[c + 3]);
+              for (int c = 0; c < 32; c += 8) {
+                a0 = max3(a0, x[c], x[c + 1]);
+                a1 = max3(a1, x[c + 2], x[c + 3]);
+                a2 = max3(a2, x[c + 4], x[c + 5]);
+                a3 = max3(a3, x[c + 6], x[c + 7]);
               }
             }
           }
           const float mx = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * p.c;  // scale > 0
-          // Raise the running maximum when the tile exceeds it by more than the threshold; O (after the
-          // previous P V) and the sum are then rescaled.
-          const bool need = m != kNegInf && mx > m + kRescaleThreshold;
+          // The maximum up to the step before: the other half's.
+          float mp = kNegInf;
+          if (half || any) {
+            if (!(ok = wait(&M.m_ready[s][half ^ 1][quarter], mc - 1 + half))) break;
+            mp = *mref;
+          }
+          // Raise it when the step exceeds it by more than the threshold; O (after the step before's P V)
+          // is then rescaled.
+          const bool need = mp != kNegInf && mx > mp + kRescaleThreshold;
           if (__any_sync(0xffffffffu, need)) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&M.pv_done[s], (sc - 1) & 1u, abort))) {
-              ok = false;
-              break;
-            }
+            if (!(ok = wait(&M.pv_done[s][half ^ 1], tc - 1 + half))) break;
             tc_fence_after();
-            const float f = need ? ex2(m - mx) : 1.0f;
+            const float f = need ? ex2(mp - mx) : 1.0f;
 #pragma unroll 1
             for (int c0 = 0; c0 < HD; c0 += 16) {
               uint32_t r[16];
-              tmem_ld16(o_addr + c0, r);
+              tmem_ld16(lane_base + HD * s + c0, r);
               tmem_wait_ld();
 #pragma unroll
               for (int c = 0; c < 16; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * f);
-              tmem_st16(o_addr + c0, r);
-            }
-            if (need) {
-              l *= f;
-              m = mx;
+              tmem_st16(lane_base + HD * s + c0, r);
             }
           }
-          if (m == kNegInf) m = mx;
+          const float mn = need || mp == kNegInf ? mx : mp;
+          *mref = mn;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&M.m_ready[s][half][quarter]);
+          ++mc;
+          if (mn != m) {
+            l = m == kNegInf ? 0.f : l * ex2(m - mn);
+            m = mn;
+          }
           const float nm = m == kNegInf ? 0.f : -m;
-          uint32_t pk[32];
+          uint32_t pk[16];
           if (none) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) pk[c] = 0u;
-            tmem_st32(s_addr + 64, pk);
-            tmem_st32(s_addr + 96, pk);
+            for (int c = 0; c < 16; ++c) pk[c] = 0u;
+            tmem_st16(s_addr + 32, pk);
+            tmem_st16(s_addr + 48, pk);
           } else {
-            float s0 = 0.f, s1 = 0.f;
+            float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+            const float2 cc = make_float2(p.c, p.c), mm = make_float2(nm, nm);
 #pragma unroll
             for (int q = 1; q >= 0; --q) {
-              if (q == 0) load_half(0);
+              if (q == 0) load(0);
 #pragma unroll
-              for (int c = 0; c < 64; c += 2) {
-                const float e0 = ex2(fmaf(x[c], p.c, nm));
-                const float e1 = ex2(fmaf(x[c + 1], p.c, nm));
-                s0 += e0;
-                s1 += e1;
-                pk[c / 2] = pack_bf16(e0, e1);
+              for (int c = 0; c < 32; c += 4) {
+                const float2 y0 = fma2(make_float2(x[c], x[c + 1]), cc, mm), y1 = fma2(make_float2(x[c + 2], x[c + 3]), cc, mm);
+                const float2 e0 = make_float2(ex2(y0.x), ex2(y0.y)), e1 = make_float2(ex2(y1.x), ex2(y1.y));
+                sum0 = add2(sum0, e0);
+                sum1 = add2(sum1, e1);
+                pk[c / 2] = pack_bf16(e0.x, e0.y);
+                pk[c / 2 + 1] = pack_bf16(e1.x, e1.y);
               }
-              tmem_st32(s_addr + 64 + 32 * q, pk);
+              tmem_st16(s_addr + 32 + 16 * q, pk);
             }
-            l += s0 + s1;
+            l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
           }
           tmem_wait_st();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&M.p_full[s]);
-        ++sc;
-        ++steps;
+        if (lane == 0) mbar_arrive(&M.p_full[s][half]);
+        ++tc;
+        any = true;
       }
       if (!ok) break;
       base += I.T;
 
-      // ---- epilogue of the item
-      if (steps > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&M.pv_done[s], (sc - 1) & 1u, abort))) break;
+      // ---- the row's statistics: the last published maximum, both halves' sums
+      if (any && live) {
+        if (half == 0) {
+          if (!(ok = wait(&M.m_ready[s][1][quarter], mc - 1))) break;
+          const float mn = *mref;
+          if (mn != m) {
+            l = m == kNegInf ? 0.f : l * ex2(m - mn);
+            m = mn;
+          }
+          M.sum[s][row] = l;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&M.sum_ready[s][quarter]);
+          if (!(ok = wait(&M.total_ready[s][quarter], outs))) break;
+          l = M.sum[s][row];
+        } else {
+          if (!(ok = wait(&M.sum_ready[s][quarter], outs))) break;
+          l += M.sum[s][row];
+          M.sum[s][row] = l;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&M.total_ready[s][quarter]);
+        }
+        ++outs;
+      }
+      // ---- epilogue of the item: each half's warps take half of O's columns
+      if (any) {
+        if (!(ok = wait(&M.pv_done[s][1], tc - 1))) break;
         tc_fence_after();
       }
       const bool join = !I.two && I.T > 1;
       if (join && s == 1) {
-        M.jm[row] = m;
-        M.jl[row] = l;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&M.join_ready);
-        if (!__all_sync(0xffffffffu, mbar_wait(&M.join_done, joins & 1u, abort))) break;
-        ++joins;
-        tc_fence_after();
-        continue;
+        if (!(ok = wait(&M.join_done, joins))) break;
       }
-      if (!I.two && s == 1) continue;
-      float f0 = 1.f, f1 = 0.f;
-      if (join) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&M.join_ready, joins & 1u, abort))) break;
-        tc_fence_after();
-        const float m1 = M.jm[row], l1 = M.jl[row], mm = fmaxf(m, m1);
-        f0 = m == kNegInf ? 0.f : ex2(m - mm);
-        f1 = m1 == kNegInf ? 0.f : ex2(m1 - mm);
-        l = l * f0 + l1 * f1;
-        m = mm;
-      }
-      if (live) {
-        const bool mine = row < nrows;
-        const bool cut = PAGED && I.cut;
-        const float inv = cut ? 1.f : (l == 0.f ? 0.f : 1.0f / l);
-        f0 *= inv;
-        f1 *= inv;
-        const int tok = I.row0 + (s && I.two ? I.step : 0) + row / g, head = I.head0 + row % g;
-        float* po = nullptr;
-        bf16* ho = nullptr;
-        if (mine) {
-          if (cut) {
-            float* pb = p.part + (size_t)(2 * blockIdx.x + (I.seg ? 1 : 0)) * partial_floats(2 * TILE, HD);
-            const int pr = (s && I.two ? I.step * g : 0) + row;
-            po = pb + (size_t)pr * HD;
-            pb[2 * TILE * HD + pr] = m;
-            pb[2 * TILE * HD + 2 * TILE + pr] = l;
-          } else {
-            ho = row_ptr_w<bf16>(p.h, PAGED ? 0 : I.b, head, tok);
-            const int64_t o = PAGED ? (int64_t)head * p.batch.T + tok : ((int64_t)I.b * p.Hq + head) * p.N + tok;
-            p.lse[o] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
-          }
+      if (I.two || s == 0) {
+        float f0 = 1.f, f1 = 0.f;
+        if (join) {
+          if (!(ok = wait(&M.join_ready, joins))) break;
+          tc_fence_after();
+          const float m1 = live ? M.mref[1][row] : kNegInf, l1 = live ? M.sum[1][row] : 0.f, mm = fmaxf(m, m1);
+          f0 = m == kNegInf ? 0.f : ex2(m - mm);
+          f1 = m1 == kNegInf ? 0.f : ex2(m1 - mm);
+          l = l * f0 + l1 * f1;
+          m = mm;
         }
+        if (live) {
+          const bool mine = row < nrows;
+          const bool cut = PAGED && I.cut;
+          const float inv = cut ? 1.f : (l == 0.f ? 0.f : 1.0f / l);
+          f0 *= inv;
+          f1 *= inv;
+          constexpr int W = HD / 2;
+          const int tok = I.row0 + shift + token(row), head = I.head0 + (PAGED ? row % g : 0);
+          float* po = nullptr;
+          bf16* ho = nullptr;
+          if (mine) {
+            if (cut) {
+              float* pb = p.part + (size_t)(2 * blockIdx.x + (I.seg ? 1 : 0)) * partial_floats(2 * TILE, HD);
+              const int pr = shift * g + row;
+              po = pb + (size_t)pr * HD + W * half;
+              if (half == 0) {
+                pb[2 * TILE * HD + pr] = m;
+                pb[2 * TILE * HD + 2 * TILE + pr] = l;
+              }
+            } else {
+              ho = row_ptr_w<bf16>(p.h, PAGED ? 0 : I.b, head, tok) + W * half;
+              if (half == 0) {
+                const int64_t o = PAGED ? (int64_t)head * p.batch.T + tok : ((int64_t)I.b * p.Hq + head) * p.N + tok;
+                p.lse[o] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+              }
+            }
+          }
+          const uint32_t o_addr = lane_base + HD * s + W * half;
 #pragma unroll 1
-        for (int c0 = 0; c0 < HD; c0 += 32) {
-          float o[32];
-          uint32_t r[32];
-          if (steps > 0) {
-            tmem_ld32(o_addr + c0, r);
-            tmem_wait_ld();
-          }
-          // a row without weight stays zero whatever the accumulator holds
+          for (int c0 = 0; c0 < W; c0 += 16) {
+            uint32_t r[16];
+            if (any) {
+              tmem_ld16(o_addr + c0, r);
+              tmem_wait_ld();
+            }
+            // a row without weight stays zero whatever the accumulator holds
 #pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] = steps > 0 && f0 != 0.f ? __uint_as_float(r[c]) * f0 : 0.f;
-          if (join) {
-            tmem_ld32(o_addr + HD + c0, r);
-            tmem_wait_ld();
+            for (int c = 0; c < 16; ++c) r[c] = any && f0 != 0.f ? __float_as_uint(__uint_as_float(r[c]) * f0) : 0u;
+            if (join) {
+              uint32_t r1[16];
+              tmem_ld16(o_addr + HD + c0, r1);
+              tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] += f1 != 0.f ? __uint_as_float(r[c]) * f1 : 0.f;
-          }
-          if (po != nullptr) {
+              for (int c = 0; c < 16; ++c)
+                if (f1 != 0.f) r[c] = __float_as_uint(fmaf(__uint_as_float(r1[c]), f1, __uint_as_float(r[c])));
+            }
+            if (po != nullptr) {
 #pragma unroll
-            for (int c = 0; c < 32; c += 4)
-              *reinterpret_cast<float4*>(po + c0 + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
-          } else if (ho != nullptr) {
-            uint4* dst = reinterpret_cast<uint4*>(ho + c0);
+              for (int c = 0; c < 16; c += 4)
+                *reinterpret_cast<uint4*>(po + c0 + c) = make_uint4(r[c], r[c + 1], r[c + 2], r[c + 3]);
+            } else if (ho != nullptr) {
+              uint32_t h8[8];
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
-              dst[v] = make_uint4(pack_bf16(o[8 * v], o[8 * v + 1]), pack_bf16(o[8 * v + 2], o[8 * v + 3]),
-                                  pack_bf16(o[8 * v + 4], o[8 * v + 5]), pack_bf16(o[8 * v + 6], o[8 * v + 7]));
+              for (int c = 0; c < 8; ++c) h8[c] = pack_bf16(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1]));
+              store32b(ho + c0, h8, p.wide);
+            }
           }
         }
+        if (join) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&M.join_done);
+        }
       }
-      if (join) {
+      if (join) ++joins;
+      if (any) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&M.join_done);
-        ++joins;
+        if (lane == 0) mbar_arrive(&M.o_free[s]);
       }
     }
   }
@@ -645,7 +760,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
 template <int HD>
 constexpr int smem_bytes() {
-  return Cfg<HD>::OFF_MISC + (int)sizeof(Misc) + 1024;
+  return Cfg<HD>::OFF_MISC + (int)sizeof(Misc);
 }
 static_assert(smem_bytes<128>() <= 232448, "shared memory of a CTA");
 
@@ -678,6 +793,7 @@ cudaError_t launch_win_fwd_tc(const WinDims& D, const WinFwdArgs& a, int32_t* st
   p.window = D.window;
   p.sinks = D.sinks;
   p.c = D.scale * kLog2e;
+  p.wide = reinterpret_cast<uintptr_t>(a.h.p) % 32 == 0 && a.h.sb % 16 == 0 && a.h.sh % 16 == 0 && a.h.sn % 16 == 0;
   const int64_t planes = (int64_t)D.B * D.Hq;
   p.rows_item = planes * ((D.N + 255) / 256) >= kCtas ? 256 : 128;
   const int64_t items = planes * ((D.N + p.rows_item - 1) / p.rows_item);
@@ -707,6 +823,7 @@ cudaError_t launch_paged_tc(const PagedDims& D, const PagedArgs& a, int32_t* sta
   p.window = D.window;
   p.sinks = D.sinks;
   p.c = D.scale * kLog2e;
+  p.wide = reinterpret_cast<uintptr_t>(a.h.p) % 32 == 0 && a.h.sb % 16 == 0 && a.h.sh % 16 == 0 && a.h.sn % 16 == 0;
   p.table = a.table;
   p.page = D.page;
   p.num_pages = D.num_pages;
