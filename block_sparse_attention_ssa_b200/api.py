@@ -301,37 +301,48 @@ def make_paged_dims(num_seqs: int, total_q: int, Hq: int, Hkv: int, d: int, page
                             EVERYTHING if window is None else window, sinks, float(scale), _DTYPES[dtype])
 
 
-def _like(name: str, x: torch.Tensor, shape: tuple, dtype: torch.dtype, device: torch.device, dense: bool = False) -> None:
-    if tuple(x.shape) != shape or x.dtype != dtype:
-        raise ValueError(f"{name}: expected {dtype} {shape}, got {x.dtype} {tuple(x.shape)}")
-    if x.device != device or device.type != "cuda":
-        raise ValueError(f"{name}: expected a tensor on one CUDA device ({device}), got {x.device}")
-    if dense and not x.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor")
+def _wrong(name: str, x: torch.Tensor, shape: tuple, dtype: torch.dtype, device: torch.device) -> ValueError:
+    return ValueError(f"{name}: expected a {dtype} tensor {tuple(shape)} with a contiguous last dimension on one CUDA "
+                      f"device ({device}), got {x.dtype} {tuple(x.shape)} on {x.device}")
 
 
-def _bhnd(x: torch.Tensor) -> ctypes._Pointer:
-    """ssa_tensor_t of a [B, H, N, d] view; dimensions of length one get a stride that fits."""
-    sb, sh, sn, sd = x.stride()
-    if sd != 1:
-        raise ValueError("expected a contiguous last dimension")
-    d = x.shape[3]
-    return ctypes.pointer(ssa_tensor_t(x.data_ptr(), sb if x.shape[0] > 1 else d, sh if x.shape[1] > 1 else d,
-                                       sn if x.shape[2] > 1 else d))
+def _arg(name: str, x: torch.Tensor, shape: tuple, dtype: torch.dtype, device: torch.device, b: int, h: int, n: int):
+    """ssa_tensor_t of a checked tensor whose dimensions b, h, n are the C ABI's batch, head and row (b = -1: none)."""
+    if x.shape != shape or x.dtype is not dtype or x.device != device or not x.is_cuda:
+        raise _wrong(name, x, shape, dtype, device)
+    st, d = x.stride(), shape[-1]
+    if st[-1] != 1:
+        raise _wrong(name, x, shape, dtype, device)
+    # a dimension of length one has no stride of its own: one that fits
+    return ctypes.byref(ssa_tensor_t(x.data_ptr(), st[b] if b >= 0 and shape[b] > 1 else d, st[h] if shape[h] > 1 else d,
+                                     st[n] if shape[n] > 1 else d))
 
 
-def _call(fn: str, device: torch.device, *args, stream=None) -> None:
-    if device.index is None or device.index == torch.cuda.current_device():
-        _check(fn, getattr(load_library(), fn)(*args, _stream(stream)))
-        return
-    with torch.cuda.device(device):
-        _check(fn, getattr(load_library(), fn)(*args, _stream(stream)))
+def _array(name: str, x: torch.Tensor, shape: tuple, dtype: torch.dtype, device: torch.device) -> int:
+    """Address of a checked dense array."""
+    if x.shape != shape or x.dtype is not dtype or x.device != device or not x.is_cuda or not x.is_contiguous():
+        raise _wrong(name, x, shape, dtype, device)
+    return x.data_ptr()
 
 
-def _bytes(ws: torch.Tensor, device: torch.device) -> tuple[ctypes.c_void_p, int]:
+def _call(fn: str, device: torch.device, stream, *args) -> None:
+    if stream is None:  # the raw handle of the device's current stream: a Stream object costs microseconds
+        stream = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        stream = _stream(stream)
+    if device.index == torch.cuda.current_device():
+        code = getattr(load_library(), fn)(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            code = getattr(load_library(), fn)(*args, stream)
+    if code != SSA_OK:
+        _check(fn, code)
+
+
+def _scratch(ws: torch.Tensor, device: torch.device) -> tuple[int, int]:
     if ws.device != device or not ws.is_contiguous():
         raise ValueError("ws: expected a contiguous tensor on the inputs' device")
-    return ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def ssa_window_workspace_bytes(dims: ssa_window_dims_t) -> int:
@@ -344,60 +355,45 @@ def ssa_paged_workspace_bytes(dims: ssa_paged_dims_t) -> int:
 
 def ssa_fwd_window(dims, Q, K, V, h, lse, stream=None) -> None:
     """Window attention with sinks: Q, h [B, Hq, N, d], K, V [B, Hkv, N, d], lse [B, Hq, N] fp32."""
-    dt, dev = dims.torch_dtype, Q.device
-    q, kv = (dims.B, dims.Hq, dims.N, dims.d), (dims.B, dims.Hkv, dims.N, dims.d)
-    for name, x, shape in (("Q", Q, q), ("K", K, kv), ("V", V, kv), ("h", h, q)):
-        _like(name, x, shape, dt, dev)
-    _like("lse", lse, q[:3], torch.float32, dev, dense=True)
-    _call("ssa_fwd_window", dev, ctypes.byref(dims), _bhnd(Q), _bhnd(K), _bhnd(V), _bhnd(h), _p(lse), stream=stream)
+    dt, dev, N, d = dims.torch_dtype, Q.device, dims.N, dims.d
+    q, kv = (dims.B, dims.Hq, N, d), (dims.B, dims.Hkv, N, d)
+    _call("ssa_fwd_window", dev, stream, ctypes.byref(dims), _arg("Q", Q, q, dt, dev, 0, 1, 2), _arg("K", K, kv, dt, dev, 0, 1, 2),
+          _arg("V", V, kv, dt, dev, 0, 1, 2), _arg("h", h, q, dt, dev, 0, 1, 2), _array("lse", lse, q[:3], torch.float32, dev))
 
 
 def ssa_bwd_window(dims, Q, K, V, h, lse, g, dQ, dK, dV, ws, stream=None) -> None:
     """Gradients of <g, h> for what ssa_fwd_window computed."""
-    dt, dev = dims.torch_dtype, Q.device
-    q, kv = (dims.B, dims.Hq, dims.N, dims.d), (dims.B, dims.Hkv, dims.N, dims.d)
-    for name, x, shape in (("Q", Q, q), ("K", K, kv), ("V", V, kv), ("h", h, q), ("g", g, q), ("dQ", dQ, q),
-                           ("dK", dK, kv), ("dV", dV, kv)):
-        _like(name, x, shape, dt, dev)
-    _like("lse", lse, q[:3], torch.float32, dev, dense=True)
-    _call("ssa_bwd_window", dev, ctypes.byref(dims), _bhnd(Q), _bhnd(K), _bhnd(V), _bhnd(h), _p(lse), _bhnd(g),
-          _bhnd(dQ), _bhnd(dK), _bhnd(dV), *_bytes(ws, dev), stream=stream)
+    dt, dev, N, d = dims.torch_dtype, Q.device, dims.N, dims.d
+    q, kv = (dims.B, dims.Hq, N, d), (dims.B, dims.Hkv, N, d)
+    _call("ssa_bwd_window", dev, stream, ctypes.byref(dims), _arg("Q", Q, q, dt, dev, 0, 1, 2), _arg("K", K, kv, dt, dev, 0, 1, 2),
+          _arg("V", V, kv, dt, dev, 0, 1, 2), _arg("h", h, q, dt, dev, 0, 1, 2), _array("lse", lse, q[:3], torch.float32, dev),
+          _arg("g", g, q, dt, dev, 0, 1, 2), _arg("dQ", dQ, q, dt, dev, 0, 1, 2), _arg("dK", dK, kv, dt, dev, 0, 1, 2),
+          _arg("dV", dV, kv, dt, dev, 0, 1, 2), *_scratch(ws, dev))
 
 
-def _packed(name: str, x: torch.Tensor, dims, heads: int, dev) -> ctypes._Pointer:
-    """[total_q, heads, d] rows as the C ABI's packed [1, heads, total_q, d]."""
-    _like(name, x, (dims.total_q, heads, dims.d), dims.torch_dtype, dev)
-    return _bhnd(x.transpose(0, 1).unsqueeze(0))
-
-
-def _cache(name: str, x: torch.Tensor, dims, dev) -> ctypes._Pointer:
-    """A [num_pages, page, Hkv, d] cache (any strides) as the C ABI's [num_pages, Hkv, page, d]."""
-    _like(name, x, (dims.num_pages, dims.page, dims.Hkv, dims.d), dims.torch_dtype, dev)
-    return _bhnd(x.transpose(1, 2))
-
-
-def _batch(q_start, kv_len, page_table, dims, dev) -> tuple:
-    _like("q_start", q_start, (dims.num_seqs + 1,), torch.int32, dev, dense=True)
-    _like("kv_len", kv_len, (dims.num_seqs,), torch.int32, dev, dense=True)
-    _like("page_table", page_table, (dims.num_seqs, dims.max_pages), torch.int32, dev, dense=True)
-    return _p(q_start), _p(kv_len), _p(page_table)
+def _batch(q_start, kv_len, page_table, dims, dev) -> tuple[int, int, int]:
+    S, i32 = dims.num_seqs, torch.int32
+    return (_array("q_start", q_start, (S + 1,), i32, dev), _array("kv_len", kv_len, (S,), i32, dev),
+            _array("page_table", page_table, (S, dims.max_pages), i32, dev))
 
 
 def ssa_paged_append(dims, k, v, q_start, kv_len, page_table, K, V, stream=None) -> None:
-    """Writes the new rows k, v [total_q, Hkv, d] into the caches K, V [num_pages, page, Hkv, d]."""
-    dev = k.device
-    _call("ssa_paged_append", dev, ctypes.byref(dims), _packed("k", k, dims, dims.Hkv, dev),
-          _packed("v", v, dims, dims.Hkv, dev), *_batch(q_start, kv_len, page_table, dims, dev),
-          _cache("K", K, dims, dev), _cache("V", V, dims, dev), stream=stream)
+    """Writes the new rows k, v [total_q, Hkv, d] into the caches K, V [num_pages, page, Hkv, d] (any strides)."""
+    dt, dev, Hkv, d = dims.torch_dtype, k.device, dims.Hkv, dims.d
+    new, cache = (dims.total_q, Hkv, d), (dims.num_pages, dims.page, Hkv, d)
+    _call("ssa_paged_append", dev, stream, ctypes.byref(dims), _arg("k", k, new, dt, dev, -1, 1, 0),
+          _arg("v", v, new, dt, dev, -1, 1, 0), *_batch(q_start, kv_len, page_table, dims, dev),
+          _arg("K", K, cache, dt, dev, 0, 2, 1), _arg("V", V, cache, dt, dev, 0, 2, 1))
 
 
 def ssa_paged_attention(dims, q, K, V, q_start, kv_len, page_table, h, lse, ws, stream=None) -> None:
     """Attention of the new rows q [total_q, Hq, d] over the caches: h [total_q, Hq, d], lse [Hq, total_q] fp32."""
-    dev = q.device
-    _like("lse", lse, (dims.Hq, dims.total_q), torch.float32, dev, dense=True)
-    _call("ssa_paged_attention", dev, ctypes.byref(dims), _packed("q", q, dims, dims.Hq, dev),
-          _cache("K", K, dims, dev), _cache("V", V, dims, dev), *_batch(q_start, kv_len, page_table, dims, dev),
-          _packed("h", h, dims, dims.Hq, dev), _p(lse), *_bytes(ws, dev), stream=stream)
+    dt, dev, T, Hq, d = dims.torch_dtype, q.device, dims.total_q, dims.Hq, dims.d
+    rows, cache = (T, Hq, d), (dims.num_pages, dims.page, dims.Hkv, d)
+    _call("ssa_paged_attention", dev, stream, ctypes.byref(dims), _arg("q", q, rows, dt, dev, -1, 1, 0),
+          _arg("K", K, cache, dt, dev, 0, 2, 1), _arg("V", V, cache, dt, dev, 0, 2, 1),
+          *_batch(q_start, kv_len, page_table, dims, dev), _arg("h", h, rows, dt, dev, -1, 1, 0),
+          _array("lse", lse, (Hq, T), torch.float32, dev), *_scratch(ws, dev))
 
 
 def ssa_launch_count() -> int:

@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint8_t* smem = align1024(smem_raw);
   DkvMisc& M = *reinterpret_cast<DkvMisc*>(smem + C::OFF_MISC);
   volatile int* abort = &M.abort;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
   const int plane = (int)blockIdx.x % p.Hkv + (int)blockIdx.y * p.Hkv, kvh = plane % p.Hkv, b = blockIdx.y;
 
   if (threadIdx.x == 0) {
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
     }
   } else if (warp == WARP_MMA) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t ak = kmajor(smem_u32(sK)), av = kmajor(smem_u32(sV));
       auto have = [&](int j) { return mbar_wait(&M.q_full[j % C::NS], (uint32_t)(j / C::NS) & 1u, abort); };
       auto s_of = [&](int j) {
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint8_t* smem = align1024(smem_raw);
   DqMisc& M = *reinterpret_cast<DqMisc*>(smem + C::OFF_MISC);
   volatile int* abort = &M.abort;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
 
   if (threadIdx.x == 0) {
     mbar_init(&M.q_full, 1);
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
     }
   } else if (warp == WARP_MMA) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t aq = kmajor(smem_u32(sQ)), ag = kmajor(smem_u32(sG)), ak = kmajor(smem_u32(sK)), av = kmajor(smem_u32(sV));
       const uint32_t bk = mnmajor(smem_u32(sK));
       uint32_t n = 0, qn = 0;  // key tiles and items so far

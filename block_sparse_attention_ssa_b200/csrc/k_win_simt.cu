@@ -319,35 +319,44 @@ __global__ void __launch_bounds__(NT_) win_fwd_simt_kernel(SimtParams p) {
 }
 
 // ================================================================ backward
-// D_t = g_t . h_t and lse in base 2, one warp per row, rows padded to 128 tokens.
+// D_t = g_t . h_t and lse in base 2, rows padded to 128 tokens.  Bound by reading h and g: a row is LPR
+// lanes of 16 bytes, and a warp has four rows' loads of each in flight per lane group.
 template <typename T, int HD>
 __global__ void __launch_bounds__(256) win_bwd_pre_kernel(TensorRef h, TensorRef g, const float* lse, float* lse2,
-                                                          float* dsum, int Hq, int N, int Npad, int64_t rows) {
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= rows) return;
-  const int64_t bh = row / Npad;
-  const int t = (int)(row % Npad), b = (int)(bh / Hq), hd = (int)(bh % Hq);
-  float s = 0.f, ls = __builtin_huge_valf();  // 2^(x - inf) = 0 in the padding
-  if (t < N) {
-    constexpr int V = Vec16<T>::kN;
-    const T* hp = row_ptr<T>(h, b, hd, t);
-    const T* gp = row_ptr<T>(g, b, hd, t);
-    for (int c = lane * V; c < HD; c += 32 * V) {
-      float x[V], y[V];
-      Vec16<T>::load(hp + c, x);
-      Vec16<T>::load(gp + c, y);
+                                                          float* dsum, int Hq, int N, int Npad) {
+  constexpr int V = Vec16<T>::kN, LPR = HD / V, RPW = 32 / LPR, U = 4;
+  const int lane = threadIdx.x & 31, c = lane % LPR * V;
+  const int bh = blockIdx.y, b = bh / Hq, hd = bh % Hq;
+  const int t0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * (RPW * U) + lane / LPR;
+  uint4 x[U], y[U];
 #pragma unroll
-      for (int i = 0; i < V; ++i) s = fmaf(x[i], y[i], s);
+  for (int i = 0; i < U; ++i) {
+    const int t = t0 + i * RPW;
+    x[i] = y[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (t < N) {
+      x[i] = *reinterpret_cast<const uint4*>(row_ptr<T>(h, b, hd, t) + c);
+      y[i] = *reinterpret_cast<const uint4*>(row_ptr<T>(g, b, hd, t) + c);
     }
-    ls = lse[bh * N + t] * kLog2e;
-    if (ls == kNegInf) ls = __builtin_huge_valf();
   }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) {
-    lse2[row] = ls;
-    dsum[row] = s;
+  for (int i = 0; i < U; ++i) {
+    const int t = t0 + i * RPW;
+    float u[V], v[V], s = 0.f;
+    Vec16<T>::load(reinterpret_cast<const T*>(&x[i]), u);
+    Vec16<T>::load(reinterpret_cast<const T*>(&y[i]), v);
+#pragma unroll
+    for (int e = 0; e < V; ++e) s = fmaf(u[e], v[e], s);
+#pragma unroll
+    for (int o = LPR / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane % LPR == 0 && t < Npad) {
+      float ls = __builtin_huge_valf();  // 2^(x - inf) = 0 in the padding and in rows without weight
+      if (t < N) {
+        const float l = lse[(int64_t)bh * N + t] * kLog2e;
+        if (l != kNegInf) ls = l;
+      }
+      lse2[(int64_t)bh * Npad + t] = ls;
+      dsum[(int64_t)bh * Npad + t] = s;
+    }
   }
 }
 
@@ -617,10 +626,9 @@ template <typename T, int HD>
 cudaError_t pre_t(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
   const WinBwdLayout L = win_bwd_layout(D);
   char* ws = static_cast<char*>(a.ws);
-  const int64_t rows = (int64_t)D.B * D.Hq * L.Npad;
-  win_bwd_pre_kernel<T, HD><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(
-      a.h, a.g, a.lse, reinterpret_cast<float*>(ws + L.lse2), reinterpret_cast<float*>(ws + L.dsum), D.Hq, D.N, L.Npad,
-      rows);
+  constexpr int per = 8 * 4 * (32 / (HD / Vec16<T>::kN));  // rows of a CTA
+  win_bwd_pre_kernel<T, HD><<<dim3((L.Npad + per - 1) / per, D.B * D.Hq), 256, 0, st>>>(
+      a.h, a.g, a.lse, reinterpret_cast<float*>(ws + L.lse2), reinterpret_cast<float*>(ws + L.dsum), D.Hq, D.N, L.Npad);
   count_launches(1);
   return cudaGetLastError();
 }

@@ -24,7 +24,7 @@ ssa_status_t check_window(const ssa_window_dims_t* in, WinDims* out, bool* empty
   if ((D.d != 64 && D.d != 128) || D.N > kMaxTokens) return SSA_ERR_UNSUPPORTED;
   *empty = (int64_t)D.B * D.Hq == 0 || D.N == 0;
   // grid limits: planes in one grid dimension, tiles x planes in another
-  if ((int64_t)D.B * D.Hkv > 65535 || (int64_t)D.B * D.Hq * ((D.N + 63) / 64) > (1LL << 30)) return SSA_ERR_UNSUPPORTED;
+  if ((int64_t)D.B * D.Hq > 65535 || (int64_t)D.B * D.Hq * ((D.N + 63) / 64) > (1LL << 30)) return SSA_ERR_UNSUPPORTED;
   D.g = D.Hq / D.Hkv;
   if (D.window > D.N) D.window = D.N > 0 ? D.N : 1;
   if (D.sinks > D.N) D.sinks = D.N;
