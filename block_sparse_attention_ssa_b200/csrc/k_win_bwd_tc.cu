@@ -3,11 +3,11 @@
 // Mathematics: p = 2^(s c - lse2), dP = g V^T, dx = p (dP - D) with D_t = g_t . h_t;
 // dV = p^T g, dK = scale dx^T Q, dQ = scale dx K.  Logits, p, dP, dx and all sums are
 // fp32; p and dx are rounded to bf16 (half a step each) as operands of the next product.
-// lse2 and D come from the preprocess in rows padded to 128 tokens; a padding row's lse2
-// is +infinity, which makes its weights zero.
+// -lse2 and -D come from the preprocess in rows padded to 128 tokens; a padding row's -lse2
+// is -infinity, which makes its weights zero.
 //
-// Two kernels of 320 threads (warps 0-7 compute, warp 8 loads by TMA, warp 9 issues the
-// products), each forming S and dP: a query tile's dQ and a key tile's dK, dV have
+// Two kernels of 576 threads (warps 0-15 compute, 32 columns of their TMEM lanes each, warp 16
+// loads by TMA, warp 17 issues the products), each forming S and dP: a query tile's dQ and a key tile's dK, dV have
 // different owners, and joining them through memory costs more than the two extra
 // products (a dQ of fp32 additions in L2 moves 64 KB per 128 x 128 tile).  No atomics:
 // every output has one writer with a fixed order.
@@ -31,8 +31,9 @@ using namespace sm100;
 using bf16 = __nv_bfloat16;
 
 constexpr int TILE = 128;
-constexpr int NTHREADS = 320;
-constexpr int WARP_TMA = 8, WARP_MMA = 9;
+constexpr int NTHREADS = 576;
+constexpr int WARP_TMA = 16, WARP_MMA = 17;
+constexpr int COLS = 32;  // columns of a compute warp
 constexpr int kCtas = 148;  // one per SM
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int HALF = TILE * 128;  // 64 columns of a tile: 128 rows of 128 bytes
@@ -68,14 +69,14 @@ __device__ __forceinline__ void mma_logits(uint32_t d, uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t kmajor(uint32_t saddr) { return desc_lo(saddr, 16); }
 __device__ __forceinline__ uint32_t mnmajor(uint32_t saddr) { return desc_lo(saddr, HALF); }
 
-// D (128 x HD) (+)= A B, A 128 x 128 as bf16 pairs in TMEM (reduction 0-63 in columns a.., 64-127 in
-// a + 64..), B 128 rows (the reduction) of a tile in shared memory (low descriptor word).
+// D (128 x HD) (+)= A B, A 128 x 128 as bf16 pairs in TMEM (32 of the reduction in columns a + 32 i .. + 15
+// for i = 0 .. 3), B 128 rows (the reduction) of a tile in shared memory (low descriptor word).
 template <int HD>
 __device__ __forceinline__ void mma_grad(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
   const uint32_t acc = accumulate ? 1u : 0u;
 #pragma unroll
   for (int kk = 0; kk < TILE / 16; ++kk)
-    mma_ts_lo(d, a + 64 * (kk >> 2) + 8 * (kk & 3), b + kk * 128, Cfg<HD>::IDESC_ACC, kk > 0 ? 1u : acc);
+    mma_ts_lo(d, a + 32 * (kk >> 1) + 8 * (kk & 1), b + kk * 128, Cfg<HD>::IDESC_ACC, kk > 0 ? 1u : acc);
 }
 
 template <int HD>
@@ -90,16 +91,11 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
-__device__ __forceinline__ void ld64(uint32_t addr, float (&x)[64]) {
-  tmem_ld32(addr, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
-  tmem_ld32(addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
-}
-
-// 32 columns of an accumulator row, scaled, to bf16 memory.
-__device__ __forceinline__ void store32(bf16* dst, const uint32_t (&r)[32], float mul) {
+// 16 columns of an accumulator row, scaled, to bf16 memory.
+__device__ __forceinline__ void store16(bf16* dst, const uint32_t (&r)[16], float mul) {
   uint4* d4 = reinterpret_cast<uint4*>(dst);
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
+  for (int v = 0; v < 2; ++v) {
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -143,9 +139,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       mbar_init(&M.q_empty[i], 1);
     }
     mbar_init(&M.s_full, 1);
-    mbar_init(&M.p_full, 8);
+    mbar_init(&M.p_full, 16);
     mbar_init(&M.dp_full, 1);
-    mbar_init(&M.ds_full, 8);
+    mbar_init(&M.ds_full, 16);
     mbar_init(&M.done, 1);
     mbar_init(&M.drain, 1);
     M.abort = 0;
@@ -235,15 +231,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
     __syncwarp();
   } else {
-    const int quarter = warp & 3, half = warp >> 2;  // key rows 32 quarter.., query columns 64 half..
+    const int quarter = warp & 3, cg = warp >> 2;  // key rows 32 quarter.., query columns 32 cg..
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const uint32_t aS = cS + lane_base + 64 * half, aP = cP + lane_base + 64 * half;
+    const uint32_t aS = cS + lane_base + COLS * cg, aP = cP + lane_base + COLS * cg;
     const int u = u0 + quarter * 32 + lane;
     const int ua = u0 + quarter * 32, ub = ua + 31;
+    const float2 cc = make_float2(p.c, p.c);
+    int qt = first % nq;  // query tile of the step, from the key tile on
     bool ok = true;
     for (int j = 0; j < T; ++j) {
-      const int t0 = (ch.kt + (first + j) % nq) * TILE + 64 * half;  // this warp's first query
-      const float* ls = reinterpret_cast<const float*>(stage(j) + 2 * C::TB) + 64 * half;
+      const int t0 = (ch.kt + qt) * TILE + COLS * cg;  // this warp's first query
+      if (++qt == nq) qt = 0;
+      const float* ls = reinterpret_cast<const float*>(stage(j) + 2 * C::TB) + COLS * cg;
       const float* ds = ls + TILE;
       // every lane reads the stage's row vectors: every lane waits for them
       if (!__all_sync(0xffffffffu, mbar_wait(&M.q_full[j % C::NS], (uint32_t)(j / C::NS) & 1u, abort)) ||
@@ -252,29 +251,31 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         break;
       }
       tc_fence_after();
-      const bool all = t0 >= ub && (t0 + 63 - ua < p.window || ub < p.sinks);
+      const bool all = t0 >= ub && (t0 + COLS - 1 - ua < p.window || ub < p.sinks);
       // queries c with lo <= c < hi see the key (c >= lo alone where it is a sink)
-      const int lo = u - t0, hi = u < p.sinks ? 64 : u + p.window - t0;
-      float x[64];
-      ld64(aS, x);
+      const int lo = u - t0, hi = u < p.sinks ? COLS : u + p.window - t0;
+      float x[COLS];
+      tmem_ld32(aS, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
       tmem_wait_ld();
-      uint32_t pk[32];
+      uint32_t pk[COLS / 2];
 #pragma unroll
-      for (int c = 0; c < 64; c += 4) {
-        const float4 l4 = *reinterpret_cast<const float4*>(ls + c);
-        x[c] = ex2(fmaf(x[c], p.c, -l4.x));
-        x[c + 1] = ex2(fmaf(x[c + 1], p.c, -l4.y));
-        x[c + 2] = ex2(fmaf(x[c + 2], p.c, -l4.z));
-        x[c + 3] = ex2(fmaf(x[c + 3], p.c, -l4.w));
+      for (int c = 0; c < COLS; c += 4) {
+        const float4 l4 = *reinterpret_cast<const float4*>(ls + c);  // -lse2
+        const float2 y0 = fma2(make_float2(x[c], x[c + 1]), cc, make_float2(l4.x, l4.y));
+        const float2 y1 = fma2(make_float2(x[c + 2], x[c + 3]), cc, make_float2(l4.z, l4.w));
+        x[c] = ex2(y0.x);
+        x[c + 1] = ex2(y0.y);
+        x[c + 2] = ex2(y1.x);
+        x[c + 3] = ex2(y1.y);
       }
       if (!all) {
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
+        for (int c = 0; c < COLS; ++c)
           if (c < lo || c >= hi) x[c] = 0.f;
       }
 #pragma unroll
-      for (int c = 0; c < 64; c += 2) pk[c / 2] = pack_bf16(x[c], x[c + 1]);
-      tmem_st32(aS, pk);
+      for (int c = 0; c < COLS; c += 2) pk[c / 2] = pack_bf16(x[c], x[c + 1]);
+      tmem_st16(aS, pk);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -285,28 +286,27 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         break;
       }
       tc_fence_after();
+      uint32_t y[COLS];
+      tmem_ld32(aP, y);
+      tmem_wait_ld();
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t y[32];
-        tmem_ld32(aP + 32 * q, y);
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 d4 = *reinterpret_cast<const float4*>(ds + 32 * q + c);
-          x[32 * q + c] *= __uint_as_float(y[c]) - d4.x;
-          x[32 * q + c + 1] *= __uint_as_float(y[c + 1]) - d4.y;
-          x[32 * q + c + 2] *= __uint_as_float(y[c + 2]) - d4.z;
-          x[32 * q + c + 3] *= __uint_as_float(y[c + 3]) - d4.w;
-        }
+      for (int c = 0; c < COLS; c += 4) {
+        const float4 d4 = *reinterpret_cast<const float4*>(ds + c);  // -D
+        const float2 z0 = mul2(make_float2(x[c], x[c + 1]), add2(make_float2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), make_float2(d4.x, d4.y)));
+        const float2 z1 = mul2(make_float2(x[c + 2], x[c + 3]), add2(make_float2(__uint_as_float(y[c + 2]), __uint_as_float(y[c + 3])), make_float2(d4.z, d4.w)));
+        x[c] = z0.x;
+        x[c + 1] = z0.y;
+        x[c + 2] = z1.x;
+        x[c + 3] = z1.y;
       }
       if (!all) {  // zero times a NaN or an infinity of a hidden pair
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
+        for (int c = 0; c < COLS; ++c)
           if (c < lo || c >= hi) x[c] = 0.f;
       }
 #pragma unroll
-      for (int c = 0; c < 64; c += 2) pk[c / 2] = pack_bf16(x[c], x[c + 1]);
-      tmem_st32(aP, pk);
+      for (int c = 0; c < COLS; c += 2) pk[c / 2] = pack_bf16(x[c], x[c + 1]);
+      tmem_st16(aP, pk);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -314,27 +314,25 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
     if (ok && __all_sync(0xffffffffu, mbar_wait(&M.done, 0, abort))) {
       tc_fence_after();
-      // columns HD/2 half .. of dK and dV
-      constexpr int W = HD / 2;
+      // columns HD/4 cg .. of dK and dV
+      constexpr int W = HD / 4;
       const bool mine = u < p.N;
       float* part = p.part + ((size_t)plane * p.partials + ch.slot + ch.idx) * (2 * TILE * HD) +
-                    (quarter * 32 + lane) * HD + W * half;
+                    (quarter * 32 + lane) * HD + W * cg;
 #pragma unroll 1
-      for (int c0 = 0; c0 < 2 * W; c0 += 32) {
+      for (int c0 = 0; c0 < 2 * W; c0 += 16) {
         const int which = c0 / W, col = c0 % W;  // 0: dK, 1: dV
-        uint32_t r[32];
-        tmem_ld32((which ? cV : cK) + lane_base + W * half + col, r);
+        uint32_t r[16];
+        tmem_ld16((which ? cV : cK) + lane_base + W * cg + col, r);
         tmem_wait_ld();
         if (!mine) continue;
         if (ch.n == 1) {
           const TensorRef& t = which ? p.dv : p.dk;
-          store32(row_ptr_w<bf16>(t, b, kvh, u) + W * half + col, r, which ? 1.0f : p.scale);
+          store16(row_ptr_w<bf16>(t, b, kvh, u) + W * cg + col, r, which ? 1.0f : p.scale);
         } else {
-          float4* d4 = reinterpret_cast<float4*>(part + which * TILE * HD + col);
+          uint4* d4 = reinterpret_cast<uint4*>(part + which * TILE * HD + col);
 #pragma unroll
-          for (int v = 0; v < 8; ++v)
-            d4[v] = make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]), __uint_as_float(r[4 * v + 2]),
-                                __uint_as_float(r[4 * v + 3]));
+          for (int v = 0; v < 4; ++v) d4[v] = make_uint4(r[4 * v], r[4 * v + 1], r[4 * v + 2], r[4 * v + 3]);
         }
       }
     }
@@ -394,7 +392,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     mbar_init(&M.s_full[0], 1);
     mbar_init(&M.s_full[1], 1);
     mbar_init(&M.dp_full, 1);
-    mbar_init(&M.ds_full, 8);
+    mbar_init(&M.ds_full, 16);
     mbar_init(&M.dq_done, 1);
     mbar_init(&M.drain, 1);
     M.abort = 0;
@@ -509,52 +507,57 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
     __syncwarp();
   } else {
-    const int quarter = warp & 3, half = warp >> 2;  // query rows 32 quarter.., key columns 64 half..
+    const int quarter = warp & 3, cg = warp >> 2;  // query rows 32 quarter.., key columns 32 cg..
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const uint32_t aS = cS + lane_base + 64 * half, aP = cP + lane_base + 64 * half;
+    const uint32_t aS = cS + lane_base + COLS * cg, aP = cP + lane_base + COLS * cg;
     uint32_t n = 0, qn = 0;
     bool ok = true;
     for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
       const DqItem I = item(i);
       const int t = I.t0 + quarter * 32 + lane, ta = I.t0 + quarter * 32, tb = ta + 31;
       const int64_t ro = ((int64_t)I.b * p.Hq + I.h) * p.Npad + t;
-      const float lse2 = p.lse2[ro], dsum = p.dsum[ro];
+      const float nl = p.lse2[ro], nd = p.dsum[ro];  // -lse2, -D
+      const float2 cc = make_float2(p.c, p.c), ll = make_float2(nl, nl), dd = make_float2(nd, nd);
       for (int j = 0; j < I.kt.count; ++j, ++n) {
         if (!__all_sync(0xffffffffu, mbar_wait(&M.s_full[n & 1], (n >> 1) & 1u, abort))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const int u0 = I.kt.tile(j) * TILE + 64 * half;  // this warp's first key
-        const bool all = u0 + 63 <= ta && (tb - u0 < p.window || u0 + 64 <= p.sinks);
+        const int u0 = I.kt.tile(j) * TILE + COLS * cg;  // this warp's first key
+        const bool all = u0 + COLS - 1 <= ta && (tb - u0 < p.window || u0 + COLS <= p.sinks);
         const int hi = t - u0, lo = t - p.window - u0, sk = p.sinks - u0;  // sees lo < c <= hi, or c < sk
-        float x[64];
-        ld64(aS + TILE * (n & 1), x);
+        float x[COLS];
+        tmem_ld32(aS + TILE * (n & 1), *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 64; ++c) x[c] = ex2(fmaf(x[c], p.c, -lse2));
+        for (int c = 0; c < COLS; c += 2) {
+          const float2 y = fma2(make_float2(x[c], x[c + 1]), cc, ll);
+          x[c] = ex2(y.x);
+          x[c + 1] = ex2(y.y);
+        }
         if (!__all_sync(0xffffffffu, mbar_wait(&M.dp_full, n & 1u, abort))) {
           ok = false;
           break;
         }
         tc_fence_after();
+        uint32_t y[COLS], pk[COLS / 2];
+        tmem_ld32(aP, y);
+        tmem_wait_ld();
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t y[32];
-          tmem_ld32(aP + 32 * q, y);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 32; ++c) x[32 * q + c] *= __uint_as_float(y[c]) - dsum;
+        for (int c = 0; c < COLS; c += 2) {
+          const float2 z = mul2(make_float2(x[c], x[c + 1]), add2(make_float2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), dd));
+          x[c] = z.x;
+          x[c + 1] = z.y;
         }
         if (!all) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
+          for (int c = 0; c < COLS; ++c)
             if (c > hi || (c <= lo && c >= sk)) x[c] = 0.f;
         }
-        uint32_t pk[32];
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) pk[c / 2] = pack_bf16(x[c], x[c + 1]);
-        tmem_st32(aP, pk);
+        for (int c = 0; c < COLS; c += 2) pk[c / 2] = pack_bf16(x[c], x[c + 1]);
+        tmem_st16(aP, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -563,13 +566,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (!ok || !__all_sync(0xffffffffu, mbar_wait(&M.dq_done, qn & 1u, abort))) break;
       ++qn;
       tc_fence_after();
-      constexpr int W = HD / 2;
+      constexpr int W = HD / 4;
 #pragma unroll 1
-      for (int c0 = 0; c0 < W; c0 += 32) {
-        uint32_t r[32];
-        tmem_ld32(cQ + lane_base + W * half + c0, r);
+      for (int c0 = 0; c0 < W; c0 += 16) {
+        uint32_t r[16];
+        tmem_ld16(cQ + lane_base + W * cg + c0, r);
         tmem_wait_ld();
-        if (t < p.N) store32(row_ptr_w<bf16>(p.dq, I.b, I.h, t) + W * half + c0, r, p.scale);
+        if (t < p.N) store16(row_ptr_w<bf16>(p.dq, I.b, I.h, t) + W * cg + c0, r, p.scale);
       }
     }
   }

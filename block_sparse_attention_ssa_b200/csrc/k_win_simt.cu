@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(NT_) win_fwd_simt_kernel(SimtParams p) {
 }
 
 // ================================================================ backward
-// D_t = g_t . h_t and lse in base 2, rows padded to 128 tokens.  Bound by reading h and g: a row is LPR
+// -D_t = -(g_t . h_t) and -lse in base 2, rows padded to 128 tokens.  Bound by reading h and g: a row is LPR
 // lanes of 16 bytes, and a warp has four rows' loads of each in flight per lane group.
 template <typename T, int HD>
 __global__ void __launch_bounds__(256) win_bwd_pre_kernel(TensorRef h, TensorRef g, const float* lse, float* lse2,
@@ -349,13 +349,13 @@ __global__ void __launch_bounds__(256) win_bwd_pre_kernel(TensorRef h, TensorRef
 #pragma unroll
     for (int o = LPR / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane % LPR == 0 && t < Npad) {
-      float ls = __builtin_huge_valf();  // 2^(x - inf) = 0 in the padding and in rows without weight
+      float ls = kNegInf;  // 2^(x - inf) = 0 in the padding and in rows without weight
       if (t < N) {
         const float l = lse[(int64_t)bh * N + t] * kLog2e;
-        if (l != kNegInf) ls = l;
+        if (l != kNegInf) ls = -l;
       }
       lse2[(int64_t)bh * Npad + t] = ls;
-      dsum[(int64_t)bh * Npad + t] = s;
+      dsum[(int64_t)bh * Npad + t] = -s;
     }
   }
 }
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(NT_) win_bwd_dq_simt_kernel(SimtBwd p) {
   const KeyTiles kt = key_tiles<BT>(q0, q0 + nrows - 1, p.window, p.sinks);
   load_rows<T, HD>(sQ, [&](int r) -> const T* { return r < nrows ? row_ptr<T>(p.q, b, h, q0 + r) : nullptr; });
   load_rows<T, HD>(sG, [&](int r) -> const T* { return r < nrows ? row_ptr<T>(p.g, b, h, q0 + r) : nullptr; });
-  float ls[4], ds[4], acc[4][HD / 16];
+  float ls[4], ds[4], acc[4][HD / 16];  // -lse2, -D
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t o = ((int64_t)b * p.Hq + h) * p.Npad + q0 + 4 * ty + i;
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(NT_) win_bwd_dq_simt_kernel(SimtBwd p) {
       for (int jj = 0; jj < 4; ++jj) {
         const int u = u0 + tx + 16 * jj, t = q0 + 4 * ty + i;
         const bool see = u <= t && (t - u < p.window || u < p.sinks);
-        sS[(4 * ty + i) * SP + tx + 16 * jj] = see ? exp2f(fmaf(x[i][jj], p.c, -ls[i])) * (y[i][jj] - ds[i]) : 0.f;
+        sS[(4 * ty + i) * SP + tx + 16 * jj] = see ? exp2f(fmaf(x[i][jj], p.c, ls[i])) * (y[i][jj] + ds[i]) : 0.f;
       }
     __syncthreads();
     weighted<HD>(sS, sK, tx, ty, acc);
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(NT_) win_bwd_dkv_simt_kernel(SimtBwd p) {
     __syncthreads();
     load_rows<T, HD>(sQ, [&](int r) -> const T* { return q0 + r < p.N ? row_ptr<T>(p.q, b, h, q0 + r) : nullptr; });
     load_rows<T, HD>(sG, [&](int r) -> const T* { return q0 + r < p.N ? row_ptr<T>(p.g, b, h, q0 + r) : nullptr; });
-    float ls[4], ds[4];
+    float ls[4], ds[4];  // -lse2, -D
 #pragma unroll
     for (int jj = 0; jj < 4; ++jj) {
       const int64_t o = ((int64_t)b * p.Hq + h) * p.Npad + q0 + tx + 16 * jj;
@@ -467,9 +467,9 @@ __global__ void __launch_bounds__(NT_) win_bwd_dkv_simt_kernel(SimtBwd p) {
       for (int jj = 0; jj < 4; ++jj) {
         const int u = u0 + 4 * ty + i, t = q0 + tx + 16 * jj;
         const bool see = u <= t && (t - u < p.window || u < p.sinks);
-        const float pv = see ? exp2f(fmaf(x[i][jj], p.c, -ls[jj])) : 0.f;
+        const float pv = see ? exp2f(fmaf(x[i][jj], p.c, ls[jj])) : 0.f;
         sS[(4 * ty + i) * SP + tx + 16 * jj] = pv;
-        y[i][jj] = see ? pv * (y[i][jj] - ds[jj]) : 0.f;
+        y[i][jj] = see ? pv * (y[i][jj] + ds[jj]) : 0.f;
       }
     __syncthreads();
     weighted<HD>(sS, sG, tx, ty, dv);

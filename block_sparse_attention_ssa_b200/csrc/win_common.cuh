@@ -253,13 +253,13 @@ __device__ __forceinline__ Chunk find_chunk(int ci, int NT, int L, int g, int N,
 // ---------------------------------------------------------------- launchers
 cudaError_t launch_win_fwd_simt(const WinDims& D, const WinFwdArgs& a, cudaStream_t st);
 
-// Workspace of the backward: lse (base 2) and D_t in rows padded to 128 tokens, then partials.
+// Workspace of the backward: -lse (base 2) and -D_t in rows padded to 128 tokens, then partials.
 struct WinBwdLayout {
   size_t lse2, dsum, part, bytes;
   int Npad;
 };
 WinBwdLayout win_bwd_layout(const WinDims& D);
-// Fills lse2 (+infinity in padding rows) and dsum.
+// Fills lse2 (-infinity in padding rows) and dsum.
 cudaError_t launch_win_bwd_pre(const WinDims& D, const WinBwdArgs& a, cudaStream_t st);
 cudaError_t launch_win_bwd_simt(const WinDims& D, const WinBwdArgs& a, cudaStream_t st);
 // Adds the chunks' partials of key tiles of BT tokens into dK, dV.
