@@ -6,20 +6,22 @@
 // -lse2 and -D come from the preprocess in rows padded to 128 tokens; a padding row's -lse2
 // is -infinity, which makes its weights zero.
 //
-// Two kernels of 576 threads (warps 0-15 compute, 32 columns of their TMEM lanes each, warp 16
-// loads by TMA, warp 17 issues the products), each forming S and dP: a query tile's dQ and a key tile's dK, dV have
-// different owners, and joining them through memory costs more than the two extra
-// products (a dQ of fp32 additions in L2 moves 64 KB per 128 x 128 tile).  No atomics:
-// every output has one writer with a fixed order.
+// Two kernels of 576 threads, each forming S and dP: a query tile's dQ and a key tile's dK,
+// dV have different owners, and joining them through memory costs more than the two extra
+// products (a dQ of fp32 additions in L2 moves 64 KB per 128 x 128 tile).  No atomics, and one
+// thread issues all products of a CTA: every output has one writer with a fixed order.
+// Warps 0-7 and 8-15 are two groups that take the units (64 queries or 64 keys) in turn, a
+// warp 32 rows by 32 columns; warp 16 loads by TMA, warp 17 issues.  While one group turns
+// logits into weights the other forms gradients, so that the exponentials (16 a cycle and SM)
+// and the tensor core work side by side; with all warps on one 128-wide step they took turns
+// (4000 cycles a 128 x 128 tile of dkv against 2560 of products).
 //
-//   dkv  a 128-key tile and a chunk of its steps (query head, 128-query tile) per CTA.
-//        TMEM (512 columns at d = 128): dK, dV, S^T, dP^T.  The products go round
-//        dV(j), S^T(j+1), dK(j), dP^T(j+1): while the warps turn S^T into P^T the tensor
-//        core does dK and dP^T, while they turn dP^T into dx^T it does dV and S^T, so
-//        single buffers suffice and S^T takes N = 128 (an N = 64 product costs as much).
-//        P^T overwrites S^T, dx^T overwrites dP^T, each warp within its own columns.
-//   dq   a persistent CTA walks (query head, 128-query tile) items.  TMEM: dQ, two S, dP;
-//        S(j+1) runs while the warps finish dx(j), dQ(j) and dP(j+1) while they form p(j+1).
+//   dkv  a 128-key tile and a chunk of its units (query head, 64 queries) per CTA.  TMEM
+//        (512 columns at d = 128): dK, dV, two S^T, two dP^T.  The products go round dV(i),
+//        S^T(i+2), dK(i-1), dP^T(i+1); P^T overwrites S^T, dx^T overwrites dP^T, each warp
+//        within its own columns.
+//   dq   a persistent CTA walks (query head, 128-query tile) items over units of 64 keys.
+//        TMEM: dQ, two S, two dP; the products go round dQ(i), S(i+2), dP(i+2).
 #include "win_common.cuh"
 
 #include "sm100_ptx.cuh"
@@ -31,18 +33,20 @@ using namespace sm100;
 using bf16 = __nv_bfloat16;
 
 constexpr int TILE = 128;
+constexpr int UNIT = 64;
 constexpr int NTHREADS = 576;
 constexpr int WARP_TMA = 16, WARP_MMA = 17;
 constexpr int COLS = 32;  // columns of a compute warp
 constexpr int kCtas = 148;  // one per SM
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int HALF = TILE * 128;  // 64 columns of a tile: 128 rows of 128 bytes
-constexpr int ROWB = TILE * 4;    // one fp32 row vector of a tile
+constexpr int HALF = TILE * 128;   // 64 columns of a 128-row tile: rows of 128 bytes
+constexpr int UHALF = UNIT * 128;  // 64 columns of a unit's rows
+constexpr int ROWB = UNIT * 4;     // one fp32 row vector of a unit
 
 template <int HD>
 struct Cfg {
-  static constexpr int TB = TILE * HD * 2;
-  static constexpr uint32_t IDESC_S = idesc_bf16_f32(TILE, TILE, false, false);
+  static constexpr int TB = TILE * HD * 2, UB = UNIT * HD * 2;  // a tile, a unit
+  static constexpr uint32_t IDESC_S = idesc_bf16_f32(TILE, UNIT, false, false);
   static constexpr uint32_t IDESC_ACC = idesc_bf16_f32(TILE, HD, false, true);
 };
 
@@ -57,38 +61,40 @@ struct BwdParams {
   float c, scale;      // c = scale * log2(e)
 };
 
-// D (128 x 128) = A B^T over HD, both K-major tiles in shared memory (low descriptor words).
+// D (128 x 64) = A B^T over HD: a 128-row tile and a unit, both K-major in shared memory (low descriptor words).
 template <int HD>
 __device__ __forceinline__ void mma_logits(uint32_t d, uint32_t a, uint32_t b) {
 #pragma unroll
-  for (int kk = 0; kk < HD / 16; ++kk) {
-    const uint32_t o = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
-    mma_ss_lo(d, a + o, b + o, Cfg<HD>::IDESC_S, kk > 0 ? 1u : 0u);
-  }
+  for (int kk = 0; kk < HD / 16; ++kk)
+    mma_ss_lo(d, a + (((kk >> 2) * HALF + (kk & 3) * 32) >> 4), b + (((kk >> 2) * UHALF + (kk & 3) * 32) >> 4),
+              Cfg<HD>::IDESC_S, kk > 0 ? 1u : 0u);
 }
 __device__ __forceinline__ uint32_t kmajor(uint32_t saddr) { return desc_lo(saddr, 16); }
-__device__ __forceinline__ uint32_t mnmajor(uint32_t saddr) { return desc_lo(saddr, HALF); }
+__device__ __forceinline__ uint32_t mnmajor(uint32_t saddr) { return desc_lo(saddr, UHALF); }  // a unit's rows
 
-// D (128 x HD) (+)= A B, A 128 x 128 as bf16 pairs in TMEM (32 of the reduction in columns a + 32 i .. + 15
-// for i = 0 .. 3), B 128 rows (the reduction) of a tile in shared memory (low descriptor word).
+// D (128 x HD) (+)= A B, A 128 x 64 as bf16 pairs in TMEM (32 of the reduction in columns a.., 32 in a + 32..),
+// B the 64 rows (the reduction) of a unit in shared memory (low descriptor word).
 template <int HD>
-__device__ __forceinline__ void mma_grad(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
-  const uint32_t acc = accumulate ? 1u : 0u;
+__device__ __forceinline__ void mma_grad(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
 #pragma unroll
-  for (int kk = 0; kk < TILE / 16; ++kk)
+  for (int kk = 0; kk < UNIT / 16; ++kk)
     mma_ts_lo(d, a + 32 * (kk >> 1) + 8 * (kk & 1), b + kk * 128, Cfg<HD>::IDESC_ACC, kk > 0 ? 1u : acc);
 }
 
+// Rows of a tile or a unit (`half`: bytes of 64 of its columns).
 template <int HD>
 __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int row, int h, int b,
-                                          int zero) {
+                                          int zero, int half) {
 #pragma unroll
   for (int f = 0; f < HD / 64; ++f)
-    tma_load_4d(dst + f * HALF, map, bar, 64 * f, row, zero & 2 ? 0 : h, zero & 1 ? 0 : b);
+    tma_load_4d(dst + f * half, map, bar, 64 * f, row, zero & 2 ? 0 : h, zero & 1 ? 0 : b);
 }
 
-__device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
-  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+// Shared memory is filled to the last kilobyte: its start has to be a 1024-byte boundary as it is.
+__device__ __forceinline__ bool misaligned(const uint8_t* smem, int32_t* status) {
+  if ((smem_u32(smem) & 1023u) == 0) return false;
+  if (threadIdx.x == 0) atomicCAS(status, 0, (int)SSA_ERR_CUDA);
+  return true;
 }
 
 // 16 columns of an accumulator row, scaled, to bf16 memory.
@@ -107,14 +113,13 @@ __device__ __forceinline__ void store16(bf16* dst, const uint32_t (&r)[16], floa
 // ================================================================ dK, dV
 template <int HD>
 struct DkvCfg {
-  static constexpr int NS = HD == 128 ? 2 : 3;
-  static constexpr int TB = Cfg<HD>::TB;
-  static constexpr int STAGE = 2 * TB + 2 * ROWB;  // Q, g, lse2, D
-  static constexpr int OFF_V = TB, OFF_STAGE = 2 * TB, OFF_MISC = OFF_STAGE + NS * STAGE;
-  static_assert(STAGE % 1024 == 0, "stages keep the alignment of swizzled tiles");
+  static constexpr int NS = HD == 128 ? 5 : 8;  // units in flight
+  static constexpr int TB = Cfg<HD>::TB, UB = Cfg<HD>::UB;
+  static constexpr int OFF_V = TB, OFF_Q = 2 * TB, OFF_ROW = OFF_Q + NS * 2 * UB;  // Q, g of each unit; -lse2, -D
+  static constexpr int OFF_MISC = OFF_ROW + NS * 2 * ROWB;
 };
 struct DkvMisc {
-  uint64_t kv_full, q_full[3], q_empty[3], s_full, p_full, dp_full, ds_full, done, drain;
+  uint64_t kv_full, q_full[8], q_empty[8], s_full[2], p_full[2], dp_full[2], ds_full[2], done, drain;
   uint32_t tmem_base;
   int abort;
 };
@@ -125,8 +130,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                           const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
                           const __grid_constant__ BwdParams p) {
   using C = DkvCfg<HD>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align1024(smem_raw);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (misaligned(smem, p.status)) return;
   DkvMisc& M = *reinterpret_cast<DkvMisc*>(smem + C::OFF_MISC);
   volatile int* abort = &M.abort;
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
@@ -138,10 +143,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       mbar_init(&M.q_full[i], 1);
       mbar_init(&M.q_empty[i], 1);
     }
-    mbar_init(&M.s_full, 1);
-    mbar_init(&M.p_full, 16);
-    mbar_init(&M.dp_full, 1);
-    mbar_init(&M.ds_full, 16);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&M.s_full[i], 1);
+      mbar_init(&M.p_full[i], 8);
+      mbar_init(&M.dp_full[i], 1);
+      mbar_init(&M.ds_full[i], 8);
+    }
     mbar_init(&M.done, 1);
     mbar_init(&M.drain, 1);
     M.abort = 0;
@@ -153,7 +160,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
   const Chunk ch = find_chunk<TILE>((int)blockIdx.x / p.Hkv, p.NT, p.L, p.g, p.N, p.window, p.sinks);
   const int u0 = ch.kt * TILE, nq = query_tiles_of<TILE>(ch.kt, p.N, p.window, p.sinks);
-  const int first = ch.idx * p.L, T = min(p.L, nq * p.g - first);
+  const int first = ch.idx * p.L, T = 2 * min(p.L, nq * p.g - first);  // units: step (head, query tile), half
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -161,68 +168,86 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const uint32_t cK = tmem, cV = tmem + HD, cS = tmem + 256, cP = tmem + 384;
   uint8_t* sK = smem;
   uint8_t* sV = smem + C::OFF_V;
-  auto stage = [&](int j) { return smem + C::OFF_STAGE + (j % C::NS) * C::STAGE; };
+  auto unit = [&](int i) { return smem + C::OFF_Q + (i % C::NS) * 2 * C::UB; };
+  auto rows = [&](int i) { return smem + C::OFF_ROW + (i % C::NS) * 2 * ROWB; };
 
   if (warp == WARP_TMA) {
-    if (lane == 0) {
+    if (elect_one()) {
       prefetch_tensormap(&tmQ);
       prefetch_tensormap(&tmG);
       mbar_expect_tx(&M.kv_full, 2 * C::TB);
-      load_tile<HD>(sK, &tmK, &M.kv_full, u0, kvh, b, p.zk);
-      load_tile<HD>(sV, &tmV, &M.kv_full, u0, kvh, b, p.zv);
-      int issued = 0;
-      for (int j = 0; j < T; ++j) {
-        const int i = j % C::NS;
-        if (j >= C::NS && !mbar_wait(&M.q_empty[i], (uint32_t)(j / C::NS - 1) & 1u, abort)) break;
-        const int h = kvh * p.g + (first + j) / nq, t0 = (ch.kt + (first + j) % nq) * TILE;
-        uint8_t* sp = stage(j);
+      load_tile<HD>(sK, &tmK, &M.kv_full, u0, kvh, b, p.zk, HALF);
+      load_tile<HD>(sV, &tmV, &M.kv_full, u0, kvh, b, p.zv, HALF);
+      int issued = 0, h = kvh * p.g + first / nq, qt = first % nq;
+      for (int i = 0; i < T; ++i) {
+        uint64_t* full = &M.q_full[i % C::NS];
+        if (i >= C::NS && !mbar_wait(&M.q_empty[i % C::NS], (uint32_t)(i / C::NS - 1) & 1u, abort)) break;
+        const int t0 = (ch.kt + qt) * TILE + (i & 1) * UNIT;
         const int64_t ro = ((int64_t)b * p.Hq + h) * p.Npad + t0;
-        mbar_expect_tx(&M.q_full[i], 2 * C::TB + 2 * ROWB);
-        load_tile<HD>(sp, &tmQ, &M.q_full[i], t0, h, b, p.zq);
-        bulk_load(sp + 2 * C::TB, p.lse2 + ro, ROWB, &M.q_full[i]);
-        load_tile<HD>(sp + C::TB, &tmG, &M.q_full[i], t0, h, b, p.zg);
-        bulk_load(sp + 2 * C::TB + ROWB, p.dsum + ro, ROWB, &M.q_full[i]);
-        issued = j + 1;
+        mbar_expect_tx(full, 2 * C::UB + 2 * ROWB);
+        load_tile<HD>(unit(i), &tmQ, full, t0, h, b, p.zq, UHALF);
+        bulk_load(rows(i), p.lse2 + ro, ROWB, full);
+        load_tile<HD>(unit(i) + C::UB, &tmG, full, t0, h, b, p.zg, UHALF);
+        bulk_load(rows(i) + ROWB, p.dsum + ro, ROWB, full);
+        issued = i + 1;
+        if (i & 1)
+          if (++qt == nq) {
+            qt = 0;
+            ++h;
+          }
       }
       int dummy = 0;
       mbar_wait(&M.kv_full, 0, &dummy);
-      for (int j = issued > C::NS ? issued - C::NS : 0; j < issued; ++j) {
+      for (int i = issued > C::NS ? issued - C::NS : 0; i < issued; ++i) {
         dummy = 0;
-        mbar_wait(&M.q_full[j % C::NS], (uint32_t)(j / C::NS) & 1u, &dummy);
+        mbar_wait(&M.q_full[i % C::NS], (uint32_t)(i / C::NS) & 1u, &dummy);
       }
     }
+    __syncwarp();
   } else if (warp == WARP_MMA) {
     if (elect_one()) {
       const uint32_t ak = kmajor(smem_u32(sK)), av = kmajor(smem_u32(sV));
-      auto have = [&](int j) { return mbar_wait(&M.q_full[j % C::NS], (uint32_t)(j / C::NS) & 1u, abort); };
-      auto s_of = [&](int j) {
-        mma_logits<HD>(cS, ak, kmajor(smem_u32(stage(j))));
-        tc_commit(&M.s_full);
+      const uint32_t bq = kmajor(smem_u32(smem + C::OFF_Q)), mq = mnmajor(smem_u32(smem + C::OFF_Q));
+      constexpr uint32_t US = 2 * C::UB >> 4, G = C::UB >> 4;  // from unit to unit, from Q to g
+      auto slot = [&](int i) { return (uint32_t)(i % C::NS) * US; };
+      auto have = [&](int i) { return mbar_wait(&M.q_full[i % C::NS], (uint32_t)(i / C::NS) & 1u, abort); };
+      auto s_of = [&](int i) {
+        mma_logits<HD>(cS + UNIT * (i & 1), ak, bq + slot(i));
+        tc_commit(&M.s_full[i & 1]);
       };
-      auto dp_of = [&](int j) {
-        mma_logits<HD>(cP, av, kmajor(smem_u32(stage(j)) + C::TB));
-        tc_commit(&M.dp_full);
+      auto dp_of = [&](int i) {
+        mma_logits<HD>(cP + UNIT * (i & 1), av, bq + slot(i) + G);
+        tc_commit(&M.dp_full[i & 1]);
       };
       bool ok = mbar_wait(&M.kv_full, 0, abort) && have(0);
       if (ok) {
         tc_fence_after();
         s_of(0);
         dp_of(0);
-      }
-      for (int j = 0; ok && j < T; ++j) {
-        if (!(ok = mbar_wait(&M.p_full, (uint32_t)j & 1u, abort))) break;
-        tc_fence_after();
-        mma_grad<HD>(cV, cS, mnmajor(smem_u32(stage(j)) + C::TB), j > 0);
-        if (j + 1 < T) {
-          if (!(ok = have(j + 1))) break;
+        if ((ok = have(1))) {  // T is even
           tc_fence_after();
-          s_of(j + 1);
+          s_of(1);
         }
-        if (!(ok = mbar_wait(&M.ds_full, (uint32_t)j & 1u, abort))) break;
-        tc_fence_after();
-        mma_grad<HD>(cK, cP, mnmajor(smem_u32(stage(j))), j > 0);
-        tc_commit(&M.q_empty[j % C::NS]);
-        if (j + 1 < T) dp_of(j + 1);
+      }
+      for (int i = 0; ok && i <= T; ++i) {
+        if (i < T) {
+          if (!(ok = mbar_wait(&M.p_full[i & 1], (uint32_t)(i >> 1) & 1u, abort))) break;
+          tc_fence_after();
+          mma_grad<HD>(cV, cS + UNIT * (i & 1), mq + slot(i) + G, i > 0 ? 1u : 0u);
+          if (i + 2 < T) {
+            if (!(ok = have(i + 2))) break;
+            tc_fence_after();
+            s_of(i + 2);
+          }
+        }
+        if (i > 0) {
+          const int k = i - 1;
+          if (!(ok = mbar_wait(&M.ds_full[k & 1], (uint32_t)(k >> 1) & 1u, abort))) break;
+          tc_fence_after();
+          mma_grad<HD>(cK, cP + UNIT * (k & 1), mq + slot(k), k > 0 ? 1u : 0u);
+          tc_commit(&M.q_empty[k % C::NS]);
+        }
+        if (i + 1 < T) dp_of(i + 1);
       }
       tc_commit(&M.done);
       tc_commit(&M.drain);
@@ -231,22 +256,24 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
     __syncwarp();
   } else {
-    const int quarter = warp & 3, cg = warp >> 2;  // key rows 32 quarter.., query columns 32 cg..
+    // key rows 32 quarter.., query columns 32 cg.. of the group's units
+    const int quarter = warp & 3, cg = (warp >> 2) & 1, grp = warp >> 3;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const uint32_t aS = cS + lane_base + COLS * cg, aP = cP + lane_base + COLS * cg;
+    const uint32_t aS = cS + lane_base + UNIT * grp + COLS * cg, aP = cP + lane_base + UNIT * grp + COLS * cg;
     const int u = u0 + quarter * 32 + lane;
     const int ua = u0 + quarter * 32, ub = ua + 31;
     const float2 cc = make_float2(p.c, p.c);
     int qt = first % nq;  // query tile of the step, from the key tile on
     bool ok = true;
-    for (int j = 0; j < T; ++j) {
-      const int t0 = (ch.kt + qt) * TILE + COLS * cg;  // this warp's first query
+    for (int i = grp; i < T; i += 2) {
+      const uint32_t ph = (uint32_t)(i >> 1);
+      const int t0 = (ch.kt + qt) * TILE + UNIT * grp + COLS * cg;  // this warp's first query
       if (++qt == nq) qt = 0;
-      const float* ls = reinterpret_cast<const float*>(stage(j) + 2 * C::TB) + COLS * cg;
-      const float* ds = ls + TILE;
-      // every lane reads the stage's row vectors: every lane waits for them
-      if (!__all_sync(0xffffffffu, mbar_wait(&M.q_full[j % C::NS], (uint32_t)(j / C::NS) & 1u, abort)) ||
-          !__all_sync(0xffffffffu, mbar_wait(&M.s_full, (uint32_t)j & 1u, abort))) {
+      const float* ls = reinterpret_cast<const float*>(rows(i)) + COLS * cg;
+      const float* ds = ls + UNIT;
+      // every lane reads the unit's row vectors: every lane waits for them
+      if (!__all_sync(0xffffffffu, mbar_wait(&M.q_full[i % C::NS], (uint32_t)(i / C::NS) & 1u, abort)) ||
+          !__all_sync(0xffffffffu, mbar_wait(&M.s_full[grp], ph & 1u, abort))) {
         ok = false;
         break;
       }
@@ -279,9 +306,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&M.p_full);
+      if (lane == 0) mbar_arrive(&M.p_full[grp]);
 
-      if (!__all_sync(0xffffffffu, mbar_wait(&M.dp_full, (uint32_t)j & 1u, abort))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&M.dp_full[grp], ph & 1u, abort))) {
         ok = false;
         break;
       }
@@ -292,8 +319,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
       for (int c = 0; c < COLS; c += 4) {
         const float4 d4 = *reinterpret_cast<const float4*>(ds + c);  // -D
-        const float2 z0 = mul2(make_float2(x[c], x[c + 1]), add2(make_float2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), make_float2(d4.x, d4.y)));
-        const float2 z1 = mul2(make_float2(x[c + 2], x[c + 3]), add2(make_float2(__uint_as_float(y[c + 2]), __uint_as_float(y[c + 3])), make_float2(d4.z, d4.w)));
+        const float2 z0 = mul2(make_float2(x[c], x[c + 1]),
+                               add2(make_float2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), make_float2(d4.x, d4.y)));
+        const float2 z1 = mul2(make_float2(x[c + 2], x[c + 3]),
+                               add2(make_float2(__uint_as_float(y[c + 2]), __uint_as_float(y[c + 3])), make_float2(d4.z, d4.w)));
         x[c] = z0.x;
         x[c + 1] = z0.y;
         x[c + 2] = z1.x;
@@ -310,25 +339,26 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&M.ds_full);
+      if (lane == 0) mbar_arrive(&M.ds_full[grp]);
     }
     if (ok && __all_sync(0xffffffffu, mbar_wait(&M.done, 0, abort))) {
       tc_fence_after();
-      // columns HD/4 cg .. of dK and dV
+      // columns HD/4 (warp / 4) .. of dK and dV
       constexpr int W = HD / 4;
+      const int col0 = W * (warp >> 2);
       const bool mine = u < p.N;
       float* part = p.part + ((size_t)plane * p.partials + ch.slot + ch.idx) * (2 * TILE * HD) +
-                    (quarter * 32 + lane) * HD + W * cg;
+                    (quarter * 32 + lane) * HD + col0;
 #pragma unroll 1
       for (int c0 = 0; c0 < 2 * W; c0 += 16) {
         const int which = c0 / W, col = c0 % W;  // 0: dK, 1: dV
         uint32_t r[16];
-        tmem_ld16((which ? cV : cK) + lane_base + W * cg + col, r);
+        tmem_ld16((which ? cV : cK) + lane_base + col0 + col, r);
         tmem_wait_ld();
         if (!mine) continue;
         if (ch.n == 1) {
           const TensorRef& t = which ? p.dv : p.dk;
-          store16(row_ptr_w<bf16>(t, b, kvh, u) + W * cg + col, r, which ? 1.0f : p.scale);
+          store16(row_ptr_w<bf16>(t, b, kvh, u) + col0 + col, r, which ? 1.0f : p.scale);
         } else {
           uint4* d4 = reinterpret_cast<uint4*>(part + which * TILE * HD + col);
 #pragma unroll
@@ -350,20 +380,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 // ================================================================ dQ
 template <int HD>
 struct DqCfg {
-  static constexpr int NSK = HD == 128 ? 3 : 4, NSV = HD == 128 ? 2 : 3;
-  static constexpr int TB = Cfg<HD>::TB;
-  static constexpr int OFF_G = TB, OFF_K = 2 * TB, OFF_V = OFF_K + NSK * TB, OFF_MISC = OFF_V + NSV * TB;
+  static constexpr int NS = HD == 128 ? 5 : 8;  // K units and V units in flight
+  static constexpr int TB = Cfg<HD>::TB, UB = Cfg<HD>::UB;
+  static constexpr int OFF_G = TB, OFF_K = 2 * TB, OFF_V = OFF_K + NS * UB, OFF_MISC = OFF_V + NS * UB;
 };
 struct DqMisc {
-  uint64_t q_full, q_empty, k_full[4], k_empty[4], v_full[3], v_empty[3];
-  uint64_t s_full[2], dp_full, ds_full, dq_done, drain;
+  uint64_t q_full, q_empty, k_full[8], k_empty[8], v_full[8], v_empty[8];
+  uint64_t s_full[2], dp_full[2], ds_full[2], dq_done, dq_free, drain;
   uint32_t tmem_base;
   int abort;
 };
 
 struct DqItem {
   int b, h, kvh, t0;
-  KeyTiles kt;
+  KeyTiles kt;  // units of 64 keys
 };
 
 template <int HD>
@@ -372,8 +402,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
                          const __grid_constant__ BwdParams p) {
   using C = DqCfg<HD>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align1024(smem_raw);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (misaligned(smem, p.status)) return;
   DqMisc& M = *reinterpret_cast<DqMisc*>(smem + C::OFF_MISC);
   volatile int* abort = &M.abort;
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
@@ -381,19 +411,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (threadIdx.x == 0) {
     mbar_init(&M.q_full, 1);
     mbar_init(&M.q_empty, 1);
-    for (int i = 0; i < C::NSK; ++i) {
+    for (int i = 0; i < C::NS; ++i) {
       mbar_init(&M.k_full[i], 1);
       mbar_init(&M.k_empty[i], 1);
-    }
-    for (int i = 0; i < C::NSV; ++i) {
       mbar_init(&M.v_full[i], 1);
       mbar_init(&M.v_empty[i], 1);
     }
-    mbar_init(&M.s_full[0], 1);
-    mbar_init(&M.s_full[1], 1);
-    mbar_init(&M.dp_full, 1);
-    mbar_init(&M.ds_full, 16);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&M.s_full[i], 1);
+      mbar_init(&M.dp_full[i], 1);
+      mbar_init(&M.ds_full[i], 8);
+    }
     mbar_init(&M.dq_done, 1);
+    mbar_init(&M.dq_free, 16);
     mbar_init(&M.drain, 1);
     M.abort = 0;
     fence_mbar_init();
@@ -406,7 +436,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = M.tmem_base;
-  const uint32_t cQ = tmem, cS = tmem + 128, cP = tmem + 384;
+  const uint32_t cQ = tmem, cS = tmem + 256, cP = tmem + 384;
   uint8_t* sQ = smem;
   uint8_t* sG = smem + C::OFF_G;
   uint8_t* sK = smem + C::OFF_K;
@@ -421,12 +451,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     I.b = plane / p.Hq;
     I.h = plane % p.Hq;
     I.kvh = I.h / p.g;
-    I.kt = key_tiles<TILE>(I.t0, min(I.t0 + TILE, p.N) - 1, p.window, p.sinks);
+    I.kt = key_tiles<UNIT>(I.t0, min(I.t0 + TILE, p.N) - 1, p.window, p.sinks);
     return I;
   };
 
   if (warp == WARP_TMA) {
-    if (lane == 0) {
+    if (elect_one()) {
       prefetch_tensormap(&tmQ);
       prefetch_tensormap(&tmK);
       prefetch_tensormap(&tmV);
@@ -437,68 +467,71 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const DqItem I = item(i);
         if (qn > 0 && !mbar_wait(&M.q_empty, (qn - 1) & 1u, abort)) break;
         mbar_expect_tx(&M.q_full, 2 * C::TB);
-        load_tile<HD>(sQ, &tmQ, &M.q_full, I.t0, I.h, I.b, p.zq);
-        load_tile<HD>(sG, &tmG, &M.q_full, I.t0, I.h, I.b, p.zg);
+        load_tile<HD>(sQ, &tmQ, &M.q_full, I.t0, I.h, I.b, p.zq, HALF);
+        load_tile<HD>(sG, &tmG, &M.q_full, I.t0, I.h, I.b, p.zg, HALF);
         ++qn;
         for (int j = 0; j < I.kt.count; ++j, ++n) {
-          const int u0 = I.kt.tile(j) * TILE, ik = (int)(n % C::NSK), iv = (int)(n % C::NSV);
-          if (n >= C::NSK && !(ok = mbar_wait(&M.k_empty[ik], (n / C::NSK - 1) & 1u, abort))) break;
-          mbar_expect_tx(&M.k_full[ik], C::TB);
-          load_tile<HD>(sK + ik * C::TB, &tmK, &M.k_full[ik], u0, I.kvh, I.b, p.zk);
+          const int u0 = I.kt.tile(j) * UNIT, st = (int)(n % C::NS);
+          const uint32_t use = n / C::NS;
+          if (n >= C::NS && !(ok = mbar_wait(&M.k_empty[st], (use - 1) & 1u, abort))) break;
+          mbar_expect_tx(&M.k_full[st], C::UB);
+          load_tile<HD>(sK + st * C::UB, &tmK, &M.k_full[st], u0, I.kvh, I.b, p.zk, UHALF);
           kn = n + 1;
-          if (n >= C::NSV && !(ok = mbar_wait(&M.v_empty[iv], (n / C::NSV - 1) & 1u, abort))) break;
-          mbar_expect_tx(&M.v_full[iv], C::TB);
-          load_tile<HD>(sV + iv * C::TB, &tmV, &M.v_full[iv], u0, I.kvh, I.b, p.zv);
+          if (n >= C::NS && !(ok = mbar_wait(&M.v_empty[st], (use - 1) & 1u, abort))) break;
+          mbar_expect_tx(&M.v_full[st], C::UB);
+          load_tile<HD>(sV + st * C::UB, &tmV, &M.v_full[st], u0, I.kvh, I.b, p.zv, UHALF);
           vn = n + 1;
         }
       }
       int dummy = 0;
       if (qn) mbar_wait(&M.q_full, (qn - 1) & 1u, &dummy);
-      for (uint32_t k = kn > C::NSK ? kn - C::NSK : 0; k < kn; ++k) {
+      for (uint32_t k = kn > C::NS ? kn - C::NS : 0; k < kn; ++k) {
         dummy = 0;
-        mbar_wait(&M.k_full[k % C::NSK], (k / C::NSK) & 1u, &dummy);
+        mbar_wait(&M.k_full[k % C::NS], (k / C::NS) & 1u, &dummy);
       }
-      for (uint32_t k = vn > C::NSV ? vn - C::NSV : 0; k < vn; ++k) {
+      for (uint32_t k = vn > C::NS ? vn - C::NS : 0; k < vn; ++k) {
         dummy = 0;
-        mbar_wait(&M.v_full[k % C::NSV], (k / C::NSV) & 1u, &dummy);
+        mbar_wait(&M.v_full[k % C::NS], (k / C::NS) & 1u, &dummy);
       }
     }
+    __syncwarp();
   } else if (warp == WARP_MMA) {
     if (elect_one()) {
-      const uint32_t aq = kmajor(smem_u32(sQ)), ag = kmajor(smem_u32(sG)), ak = kmajor(smem_u32(sK)), av = kmajor(smem_u32(sV));
-      const uint32_t bk = mnmajor(smem_u32(sK));
-      uint32_t n = 0, qn = 0;  // key tiles and items so far
+      const uint32_t aq = kmajor(smem_u32(sQ)), ag = kmajor(smem_u32(sG)), bk = kmajor(smem_u32(sK)), bv = kmajor(smem_u32(sV));
+      const uint32_t mk = mnmajor(smem_u32(sK));
+      constexpr uint32_t US = C::UB >> 4;
+      uint32_t n = 0, qn = 0;  // units and items so far
       bool ok = true;
-      auto s_of = [&](uint32_t k) {
-        if (!mbar_wait(&M.k_full[k % C::NSK], (k / C::NSK) & 1u, abort)) return false;
+      // logits and dP of unit k (`last`: the item's last, after which Q and g are free)
+      auto front = [&](uint32_t k, bool last) {
+        const uint32_t st = k % C::NS, ph = (k / C::NS) & 1u;
+        if (!mbar_wait(&M.k_full[st], ph, abort)) return false;
         tc_fence_after();
-        mma_logits<HD>(cS + TILE * (k & 1), aq, ak + (k % C::NSK) * (C::TB >> 4));
+        mma_logits<HD>(cS + UNIT * (k & 1), aq, bk + st * US);
         tc_commit(&M.s_full[k & 1]);
-        return true;
-      };
-      auto dp_of = [&](uint32_t k, bool last) {
-        if (!mbar_wait(&M.v_full[k % C::NSV], (k / C::NSV) & 1u, abort)) return false;
+        if (!mbar_wait(&M.v_full[st], ph, abort)) return false;
         tc_fence_after();
-        mma_logits<HD>(cP, ag, av + (k % C::NSV) * (C::TB >> 4));
-        tc_commit(&M.dp_full);
-        tc_commit(&M.v_empty[k % C::NSV]);
+        mma_logits<HD>(cP + UNIT * (k & 1), ag, bv + st * US);
+        tc_commit(&M.dp_full[k & 1]);
+        tc_commit(&M.v_empty[st]);
         if (last) tc_commit(&M.q_empty);
         return true;
       };
       for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
         const int T = item(i).kt.count;
         if (!(ok = mbar_wait(&M.q_full, qn & 1u, abort))) break;
-        ++qn;
         tc_fence_after();
-        ok = s_of(n) && dp_of(n, T == 1);
+        ok = front(n, T == 1) && (T < 2 || front(n + 1, T == 2));
+        // every warp has read the item before's dQ
+        if (ok && qn > 0) ok = mbar_wait(&M.dq_free, (qn - 1) & 1u, abort);
+        ++qn;
         for (int j = 0; ok && j < T; ++j, ++n) {
-          if (j + 1 < T && !(ok = s_of(n + 1))) break;
-          if (!(ok = mbar_wait(&M.ds_full, n & 1u, abort))) break;
+          if (!(ok = mbar_wait(&M.ds_full[n & 1], (n >> 1) & 1u, abort))) break;
           tc_fence_after();
-          mma_grad<HD>(cQ, cP, bk + (n % C::NSK) * (C::TB >> 4), j > 0);
-          tc_commit(&M.k_empty[n % C::NSK]);
+          mma_grad<HD>(cQ, cP + UNIT * (n & 1), mk + (n % C::NS) * US, j > 0 ? 1u : 0u);
+          tc_commit(&M.k_empty[n % C::NS]);
           if (j + 1 == T) tc_commit(&M.dq_done);
-          if (j + 1 < T) ok = dp_of(n + 1, j + 2 == T);
+          if (j + 2 < T) ok = front(n + 2, j + 3 == T);
         }
       }
       tc_commit(&M.drain);
@@ -507,9 +540,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
     __syncwarp();
   } else {
-    const int quarter = warp & 3, cg = warp >> 2;  // query rows 32 quarter.., key columns 32 cg..
+    // query rows 32 quarter.., key columns 32 cg.. of the group's units
+    const int quarter = warp & 3, cg = (warp >> 2) & 1, grp = warp >> 3;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const uint32_t aS = cS + lane_base + COLS * cg, aP = cP + lane_base + COLS * cg;
+    const uint32_t aS = cS + lane_base + UNIT * grp + COLS * cg, aP = cP + lane_base + UNIT * grp + COLS * cg;
     uint32_t n = 0, qn = 0;
     bool ok = true;
     for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
@@ -518,17 +552,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const int64_t ro = ((int64_t)I.b * p.Hq + I.h) * p.Npad + t;
       const float nl = p.lse2[ro], nd = p.dsum[ro];  // -lse2, -D
       const float2 cc = make_float2(p.c, p.c), ll = make_float2(nl, nl), dd = make_float2(nd, nd);
-      for (int j = 0; j < I.kt.count; ++j, ++n) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&M.s_full[n & 1], (n >> 1) & 1u, abort))) {
+      // the groups take the units of all items in turn (buffer n & 1)
+      for (uint32_t k = n + ((n ^ (uint32_t)grp) & 1u); k < n + I.kt.count; k += 2) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&M.s_full[grp], (k >> 1) & 1u, abort))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const int u0 = I.kt.tile(j) * TILE + COLS * cg;  // this warp's first key
+        const int u0 = I.kt.tile((int)(k - n)) * UNIT + COLS * cg;  // this warp's first key
         const bool all = u0 + COLS - 1 <= ta && (tb - u0 < p.window || u0 + COLS <= p.sinks);
         const int hi = t - u0, lo = t - p.window - u0, sk = p.sinks - u0;  // sees lo < c <= hi, or c < sk
         float x[COLS];
-        tmem_ld32(aS + TILE * (n & 1), *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+        tmem_ld32(aS, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
         tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < COLS; c += 2) {
@@ -536,7 +571,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           x[c] = ex2(y.x);
           x[c + 1] = ex2(y.y);
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(&M.dp_full, n & 1u, abort))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&M.dp_full[grp], (k >> 1) & 1u, abort))) {
           ok = false;
           break;
         }
@@ -561,8 +596,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&M.ds_full);
+        if (lane == 0) mbar_arrive(&M.ds_full[grp]);
       }
+      n += I.kt.count;
       if (!ok || !__all_sync(0xffffffffu, mbar_wait(&M.dq_done, qn & 1u, abort))) break;
       ++qn;
       tc_fence_after();
@@ -570,10 +606,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll 1
       for (int c0 = 0; c0 < W; c0 += 16) {
         uint32_t r[16];
-        tmem_ld16(cQ + lane_base + W * cg + c0, r);
+        tmem_ld16(cQ + lane_base + W * (warp >> 2) + c0, r);
         tmem_wait_ld();
-        if (t < p.N) store16(row_ptr_w<bf16>(p.dq, I.b, I.h, t) + W * cg + c0, r, p.scale);
+        if (t < p.N) store16(row_ptr_w<bf16>(p.dq, I.b, I.h, t) + W * (warp >> 2) + c0, r, p.scale);
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&M.dq_free);
     }
   }
   tc_fence_before();
@@ -588,20 +627,25 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
 template <int HD>
 constexpr int dkv_smem() {
-  return DkvCfg<HD>::OFF_MISC + (int)sizeof(DkvMisc) + 1024;
+  return DkvCfg<HD>::OFF_MISC + (int)sizeof(DkvMisc);
 }
 template <int HD>
 constexpr int dq_smem() {
-  return DqCfg<HD>::OFF_MISC + (int)sizeof(DqMisc) + 1024;
+  return DqCfg<HD>::OFF_MISC + (int)sizeof(DqMisc);
 }
 static_assert(dkv_smem<128>() <= 232448 && dq_smem<128>() <= 232448, "shared memory of a CTA");
 
 template <int HD>
 cudaError_t launch(const WinDims& D, const WinBwdArgs& a, int32_t* status, cudaStream_t st) {
   BwdParams p{};
-  CUtensorMap q, k, v, g;
-  if (!win_tma_map(&q, a.q, D.B, D.Hq, D.N, TILE, HD, &p.zq) || !win_tma_map(&k, a.k, D.B, D.Hkv, D.N, TILE, HD, &p.zk) ||
-      !win_tma_map(&v, a.v, D.B, D.Hkv, D.N, TILE, HD, &p.zv) || !win_tma_map(&g, a.g, D.B, D.Hq, D.N, TILE, HD, &p.zg))
+  // Boxes: the CTA's own tile of 128 rows, the other side's units of 64.
+  CUtensorMap qt, kt, vt, gt, qu, ku, vu, gu;
+  auto map = [&](CUtensorMap* m, const TensorRef& t, int H, int rows, int* zero) {
+    return win_tma_map(m, t, D.B, H, D.N, rows, HD, zero);
+  };
+  if (!map(&qt, a.q, D.Hq, TILE, &p.zq) || !map(&gt, a.g, D.Hq, TILE, &p.zg) || !map(&kt, a.k, D.Hkv, TILE, &p.zk) ||
+      !map(&vt, a.v, D.Hkv, TILE, &p.zv) || !map(&qu, a.q, D.Hq, UNIT, &p.zq) || !map(&gu, a.g, D.Hq, UNIT, &p.zg) ||
+      !map(&ku, a.k, D.Hkv, UNIT, &p.zk) || !map(&vu, a.v, D.Hkv, UNIT, &p.zv))
     return cudaErrorInvalidValue;
   cudaError_t e = launch_win_bwd_pre(D, a, st);
   if (e != cudaSuccess) return e;
@@ -630,14 +674,14 @@ cudaError_t launch(const WinDims& D, const WinBwdArgs& a, int32_t* status, cudaS
   p.scale = D.scale;
   auto dkv = win_bwd_dkv_tc_kernel<HD>;
   if ((e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, dkv_smem<HD>())) != cudaSuccess) return e;
-  dkv<<<dim3(cp.chunks * D.Hkv, D.B), NTHREADS, dkv_smem<HD>(), st>>>(q, k, v, g, p);
+  dkv<<<dim3(cp.chunks * D.Hkv, D.B), NTHREADS, dkv_smem<HD>(), st>>>(qu, kt, vt, gu, p);
   count_launches(1);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if ((e = launch_win_kvjoin<TILE>(D, a, cp, p.part, st)) != cudaSuccess) return e;
   auto dq = win_bwd_dq_tc_kernel<HD>;
   if ((e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, dq_smem<HD>())) != cudaSuccess) return e;
   const int64_t items = (int64_t)D.B * D.Hq * cp.NT;
-  dq<<<(unsigned)(items < kCtas ? items : kCtas), NTHREADS, dq_smem<HD>(), st>>>(q, k, v, g, p);
+  dq<<<(unsigned)(items < kCtas ? items : kCtas), NTHREADS, dq_smem<HD>(), st>>>(qt, ku, vu, gt, p);
   count_launches(1);
   return cudaGetLastError();
 }
