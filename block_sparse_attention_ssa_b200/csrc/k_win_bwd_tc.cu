@@ -10,18 +10,19 @@
 // dV have different owners, and joining them through memory costs more than the two extra
 // products (a dQ of fp32 additions in L2 moves 64 KB per 128 x 128 tile).  No atomics, and one
 // thread issues all products of a CTA: every output has one writer with a fixed order.
-// Warps 0-7 and 8-15 are two groups that take the units (64 queries or 64 keys) in turn, a
-// warp 32 rows by 32 columns; warp 16 loads by TMA, warp 17 issues.  While one group turns
-// logits into weights the other forms gradients, so that the exponentials (16 a cycle and SM)
-// and the tensor core work side by side; with all warps on one 128-wide step they took turns
-// (4000 cycles a 128 x 128 tile of dkv against 2560 of products).
+// Warps 0-15 compute, 32 rows by 32 columns each, warp 16 loads by TMA, warp 17 issues.
 //
 //   dkv  a 128-key tile and a chunk of its units (query head, 64 queries) per CTA.  TMEM
-//        (512 columns at d = 128): dK, dV, two S^T, two dP^T.  The products go round dV(i),
-//        S^T(i+2), dK(i-1), dP^T(i+1); P^T overwrites S^T, dx^T overwrites dP^T, each warp
-//        within its own columns.
-//   dq   a persistent CTA walks (query head, 128-query tile) items over units of 64 keys.
-//        TMEM: dQ, two S, two dP; the products go round dQ(i), S(i+2), dP(i+2).
+//        (512 columns at d = 128): dK, dV, two S^T, two dP^T.  Two groups of eight warps take
+//        the units in turn, one turning logits into weights while the other forms gradients,
+//        so that the exponentials (16 a cycle and SM) and the tensor core work side by side;
+//        with all warps on one 128-wide step they took turns (4000 cycles a 128 x 128 tile).
+//        The products go round dV(i), S^T(i+2), dK(i-1), dP^T(i+1); P^T overwrites S^T, dx^T
+//        overwrites dP^T, each warp within its own columns.
+//   dq   a persistent CTA walks (query head, 128-query tile) items over tiles of 128 keys.
+//        TMEM: dQ, two S, dP.  dx overwrites the S it came from, so that dP(j+1) can be formed
+//        as soon as dP(j) is read; the products go round dP(j+1), dQ(j), S(j+2), and the warps
+//        form the weights of j + 1 meanwhile.
 #include "win_common.cuh"
 
 #include "sm100_ptx.cuh"
@@ -46,7 +47,8 @@ constexpr int ROWB = UNIT * 4;     // one fp32 row vector of a unit
 template <int HD>
 struct Cfg {
   static constexpr int TB = TILE * HD * 2, UB = UNIT * HD * 2;  // a tile, a unit
-  static constexpr uint32_t IDESC_S = idesc_bf16_f32(TILE, UNIT, false, false);
+  static constexpr uint32_t IDESC_U = idesc_bf16_f32(TILE, UNIT, false, false);
+  static constexpr uint32_t IDESC_T = idesc_bf16_f32(TILE, TILE, false, false);
   static constexpr uint32_t IDESC_ACC = idesc_bf16_f32(TILE, HD, false, true);
 };
 
@@ -61,23 +63,24 @@ struct BwdParams {
   float c, scale;      // c = scale * log2(e)
 };
 
-// D (128 x 64) = A B^T over HD: a 128-row tile and a unit, both K-major in shared memory (low descriptor words).
-template <int HD>
+// D (128 x R) = A B^T over HD: a 128-row tile and R rows (a tile's or a unit's), both K-major in shared memory
+// (low descriptor words).
+template <int HD, int R>
 __device__ __forceinline__ void mma_logits(uint32_t d, uint32_t a, uint32_t b) {
 #pragma unroll
   for (int kk = 0; kk < HD / 16; ++kk)
-    mma_ss_lo(d, a + (((kk >> 2) * HALF + (kk & 3) * 32) >> 4), b + (((kk >> 2) * UHALF + (kk & 3) * 32) >> 4),
-              Cfg<HD>::IDESC_S, kk > 0 ? 1u : 0u);
+    mma_ss_lo(d, a + (((kk >> 2) * HALF + (kk & 3) * 32) >> 4), b + (((kk >> 2) * R * 128 + (kk & 3) * 32) >> 4),
+              R == UNIT ? Cfg<HD>::IDESC_U : Cfg<HD>::IDESC_T, kk > 0 ? 1u : 0u);
 }
 __device__ __forceinline__ uint32_t kmajor(uint32_t saddr) { return desc_lo(saddr, 16); }
-__device__ __forceinline__ uint32_t mnmajor(uint32_t saddr) { return desc_lo(saddr, UHALF); }  // a unit's rows
+__device__ __forceinline__ uint32_t mnmajor(uint32_t saddr, uint32_t half) { return desc_lo(saddr, half); }
 
-// D (128 x HD) (+)= A B, A 128 x 64 as bf16 pairs in TMEM (32 of the reduction in columns a.., 32 in a + 32..),
-// B the 64 rows (the reduction) of a unit in shared memory (low descriptor word).
-template <int HD>
+// D (128 x HD) (+)= A B, A 128 x R as bf16 pairs in TMEM (32 of the reduction in columns a + 32 i .. + 15),
+// B the R rows (the reduction) of a tile or a unit in shared memory (low descriptor word).
+template <int HD, int R>
 __device__ __forceinline__ void mma_grad(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
 #pragma unroll
-  for (int kk = 0; kk < UNIT / 16; ++kk)
+  for (int kk = 0; kk < R / 16; ++kk)
     mma_ts_lo(d, a + 32 * (kk >> 1) + 8 * (kk & 1), b + kk * 128, Cfg<HD>::IDESC_ACC, kk > 0 ? 1u : acc);
 }
 
@@ -207,16 +210,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   } else if (warp == WARP_MMA) {
     if (elect_one()) {
       const uint32_t ak = kmajor(smem_u32(sK)), av = kmajor(smem_u32(sV));
-      const uint32_t bq = kmajor(smem_u32(smem + C::OFF_Q)), mq = mnmajor(smem_u32(smem + C::OFF_Q));
+      const uint32_t bq = kmajor(smem_u32(smem + C::OFF_Q)), mq = mnmajor(smem_u32(smem + C::OFF_Q), UHALF);
       constexpr uint32_t US = 2 * C::UB >> 4, G = C::UB >> 4;  // from unit to unit, from Q to g
       auto slot = [&](int i) { return (uint32_t)(i % C::NS) * US; };
       auto have = [&](int i) { return mbar_wait(&M.q_full[i % C::NS], (uint32_t)(i / C::NS) & 1u, abort); };
       auto s_of = [&](int i) {
-        mma_logits<HD>(cS + UNIT * (i & 1), ak, bq + slot(i));
+        mma_logits<HD, UNIT>(cS + UNIT * (i & 1), ak, bq + slot(i));
         tc_commit(&M.s_full[i & 1]);
       };
       auto dp_of = [&](int i) {
-        mma_logits<HD>(cP + UNIT * (i & 1), av, bq + slot(i) + G);
+        mma_logits<HD, UNIT>(cP + UNIT * (i & 1), av, bq + slot(i) + G);
         tc_commit(&M.dp_full[i & 1]);
       };
       bool ok = mbar_wait(&M.kv_full, 0, abort) && have(0);
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (i < T) {
           if (!(ok = mbar_wait(&M.p_full[i & 1], (uint32_t)(i >> 1) & 1u, abort))) break;
           tc_fence_after();
-          mma_grad<HD>(cV, cS + UNIT * (i & 1), mq + slot(i) + G, i > 0 ? 1u : 0u);
+          mma_grad<HD, UNIT>(cV, cS + UNIT * (i & 1), mq + slot(i) + G, i > 0 ? 1u : 0u);
           if (i + 2 < T) {
             if (!(ok = have(i + 2))) break;
             tc_fence_after();
@@ -244,7 +247,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           const int k = i - 1;
           if (!(ok = mbar_wait(&M.ds_full[k & 1], (uint32_t)(k >> 1) & 1u, abort))) break;
           tc_fence_after();
-          mma_grad<HD>(cK, cP + UNIT * (k & 1), mq + slot(k), k > 0 ? 1u : 0u);
+          mma_grad<HD, UNIT>(cK, cP + UNIT * (k & 1), mq + slot(k), k > 0 ? 1u : 0u);
           tc_commit(&M.q_empty[k % C::NS]);
         }
         if (i + 1 < T) dp_of(i + 1);
@@ -380,20 +383,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 // ================================================================ dQ
 template <int HD>
 struct DqCfg {
-  static constexpr int NS = HD == 128 ? 5 : 8;  // K units and V units in flight
-  static constexpr int TB = Cfg<HD>::TB, UB = Cfg<HD>::UB;
-  static constexpr int OFF_G = TB, OFF_K = 2 * TB, OFF_V = OFF_K + NS * UB, OFF_MISC = OFF_V + NS * UB;
+  static constexpr int NSK = HD == 128 ? 3 : 5, NSV = HD == 128 ? 2 : 4;  // K, V tiles in flight
+  static constexpr int TB = Cfg<HD>::TB;
+  static constexpr int OFF_G = TB, OFF_K = 2 * TB, OFF_V = OFF_K + NSK * TB, OFF_MISC = OFF_V + NSV * TB;
 };
 struct DqMisc {
-  uint64_t q_full, q_empty, k_full[8], k_empty[8], v_full[8], v_empty[8];
-  uint64_t s_full[2], dp_full[2], ds_full[2], dq_done, dq_free, drain;
+  uint64_t q_full, q_empty, k_full[5], k_empty[5], v_full[4], v_empty[4];
+  uint64_t s_full[2], dp_full, ds_full, dq_done, dq_free, drain;
   uint32_t tmem_base;
   int abort;
 };
 
 struct DqItem {
   int b, h, kvh, t0;
-  KeyTiles kt;  // units of 64 keys
+  KeyTiles kt;
 };
 
 template <int HD>
@@ -411,17 +414,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (threadIdx.x == 0) {
     mbar_init(&M.q_full, 1);
     mbar_init(&M.q_empty, 1);
-    for (int i = 0; i < C::NS; ++i) {
+    for (int i = 0; i < C::NSK; ++i) {
       mbar_init(&M.k_full[i], 1);
       mbar_init(&M.k_empty[i], 1);
+    }
+    for (int i = 0; i < C::NSV; ++i) {
       mbar_init(&M.v_full[i], 1);
       mbar_init(&M.v_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&M.s_full[i], 1);
-      mbar_init(&M.dp_full[i], 1);
-      mbar_init(&M.ds_full[i], 8);
-    }
+    mbar_init(&M.s_full[0], 1);
+    mbar_init(&M.s_full[1], 1);
+    mbar_init(&M.dp_full, 1);
+    mbar_init(&M.ds_full, 16);
     mbar_init(&M.dq_done, 1);
     mbar_init(&M.dq_free, 16);
     mbar_init(&M.drain, 1);
@@ -436,7 +440,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = M.tmem_base;
-  const uint32_t cQ = tmem, cS = tmem + 256, cP = tmem + 384;
+  const uint32_t cQ = tmem, cS = tmem + 128, cP = tmem + 384;
   uint8_t* sQ = smem;
   uint8_t* sG = smem + C::OFF_G;
   uint8_t* sK = smem + C::OFF_K;
@@ -451,7 +455,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     I.b = plane / p.Hq;
     I.h = plane % p.Hq;
     I.kvh = I.h / p.g;
-    I.kt = key_tiles<UNIT>(I.t0, min(I.t0 + TILE, p.N) - 1, p.window, p.sinks);
+    I.kt = key_tiles<TILE>(I.t0, min(I.t0 + TILE, p.N) - 1, p.window, p.sinks);
     return I;
   };
 
@@ -471,67 +475,69 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         load_tile<HD>(sG, &tmG, &M.q_full, I.t0, I.h, I.b, p.zg, HALF);
         ++qn;
         for (int j = 0; j < I.kt.count; ++j, ++n) {
-          const int u0 = I.kt.tile(j) * UNIT, st = (int)(n % C::NS);
-          const uint32_t use = n / C::NS;
-          if (n >= C::NS && !(ok = mbar_wait(&M.k_empty[st], (use - 1) & 1u, abort))) break;
-          mbar_expect_tx(&M.k_full[st], C::UB);
-          load_tile<HD>(sK + st * C::UB, &tmK, &M.k_full[st], u0, I.kvh, I.b, p.zk, UHALF);
+          const int u0 = I.kt.tile(j) * TILE, ik = (int)(n % C::NSK), iv = (int)(n % C::NSV);
+          if (n >= C::NSK && !(ok = mbar_wait(&M.k_empty[ik], (n / C::NSK - 1) & 1u, abort))) break;
+          mbar_expect_tx(&M.k_full[ik], C::TB);
+          load_tile<HD>(sK + ik * C::TB, &tmK, &M.k_full[ik], u0, I.kvh, I.b, p.zk, HALF);
           kn = n + 1;
-          if (n >= C::NS && !(ok = mbar_wait(&M.v_empty[st], (use - 1) & 1u, abort))) break;
-          mbar_expect_tx(&M.v_full[st], C::UB);
-          load_tile<HD>(sV + st * C::UB, &tmV, &M.v_full[st], u0, I.kvh, I.b, p.zv, UHALF);
+          if (n >= C::NSV && !(ok = mbar_wait(&M.v_empty[iv], (n / C::NSV - 1) & 1u, abort))) break;
+          mbar_expect_tx(&M.v_full[iv], C::TB);
+          load_tile<HD>(sV + iv * C::TB, &tmV, &M.v_full[iv], u0, I.kvh, I.b, p.zv, HALF);
           vn = n + 1;
         }
       }
       int dummy = 0;
       if (qn) mbar_wait(&M.q_full, (qn - 1) & 1u, &dummy);
-      for (uint32_t k = kn > C::NS ? kn - C::NS : 0; k < kn; ++k) {
+      for (uint32_t k = kn > C::NSK ? kn - C::NSK : 0; k < kn; ++k) {
         dummy = 0;
-        mbar_wait(&M.k_full[k % C::NS], (k / C::NS) & 1u, &dummy);
+        mbar_wait(&M.k_full[k % C::NSK], (k / C::NSK) & 1u, &dummy);
       }
-      for (uint32_t k = vn > C::NS ? vn - C::NS : 0; k < vn; ++k) {
+      for (uint32_t k = vn > C::NSV ? vn - C::NSV : 0; k < vn; ++k) {
         dummy = 0;
-        mbar_wait(&M.v_full[k % C::NS], (k / C::NS) & 1u, &dummy);
+        mbar_wait(&M.v_full[k % C::NSV], (k / C::NSV) & 1u, &dummy);
       }
     }
     __syncwarp();
   } else if (warp == WARP_MMA) {
     if (elect_one()) {
       const uint32_t aq = kmajor(smem_u32(sQ)), ag = kmajor(smem_u32(sG)), bk = kmajor(smem_u32(sK)), bv = kmajor(smem_u32(sV));
-      const uint32_t mk = mnmajor(smem_u32(sK));
-      constexpr uint32_t US = C::UB >> 4;
-      uint32_t n = 0, qn = 0;  // units and items so far
+      const uint32_t mk = mnmajor(smem_u32(sK), HALF);
+      constexpr uint32_t TS = C::TB >> 4;
+      uint32_t n = 0, qn = 0;  // tiles and items so far
       bool ok = true;
-      // logits and dP of unit k (`last`: the item's last, after which Q and g are free)
-      auto front = [&](uint32_t k, bool last) {
-        const uint32_t st = k % C::NS, ph = (k / C::NS) & 1u;
-        if (!mbar_wait(&M.k_full[st], ph, abort)) return false;
+      auto s_of = [&](uint32_t k) {
+        if (!mbar_wait(&M.k_full[k % C::NSK], (k / C::NSK) & 1u, abort)) return false;
         tc_fence_after();
-        mma_logits<HD>(cS + UNIT * (k & 1), aq, bk + st * US);
+        mma_logits<HD, TILE>(cS + TILE * (k & 1), aq, bk + (k % C::NSK) * TS);
         tc_commit(&M.s_full[k & 1]);
-        if (!mbar_wait(&M.v_full[st], ph, abort)) return false;
+        return true;
+      };
+      auto dp_of = [&](uint32_t k) {
+        if (!mbar_wait(&M.v_full[k % C::NSV], (k / C::NSV) & 1u, abort)) return false;
         tc_fence_after();
-        mma_logits<HD>(cP + UNIT * (k & 1), ag, bv + st * US);
-        tc_commit(&M.dp_full[k & 1]);
-        tc_commit(&M.v_empty[st]);
-        if (last) tc_commit(&M.q_empty);
+        mma_logits<HD, TILE>(cP, ag, bv + (k % C::NSV) * TS);
+        tc_commit(&M.dp_full);
+        tc_commit(&M.v_empty[k % C::NSV]);
         return true;
       };
       for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
         const int T = item(i).kt.count;
         if (!(ok = mbar_wait(&M.q_full, qn & 1u, abort))) break;
         tc_fence_after();
-        ok = front(n, T == 1) && (T < 2 || front(n + 1, T == 2));
+        ok = s_of(n) && dp_of(n) && (T < 2 || s_of(n + 1));
+        if (T == 1) tc_commit(&M.q_empty);
         // every warp has read the item before's dQ
         if (ok && qn > 0) ok = mbar_wait(&M.dq_free, (qn - 1) & 1u, abort);
         ++qn;
         for (int j = 0; ok && j < T; ++j, ++n) {
-          if (!(ok = mbar_wait(&M.ds_full[n & 1], (n >> 1) & 1u, abort))) break;
+          if (!(ok = mbar_wait(&M.ds_full, n & 1u, abort))) break;  // dP(j) is read, dx(j) written
           tc_fence_after();
-          mma_grad<HD>(cQ, cP + UNIT * (n & 1), mk + (n % C::NS) * US, j > 0 ? 1u : 0u);
-          tc_commit(&M.k_empty[n % C::NS]);
+          if (j + 1 < T && !(ok = dp_of(n + 1))) break;
+          if (j + 2 == T) tc_commit(&M.q_empty);  // the last S and dP of the item are issued
+          mma_grad<HD, TILE>(cQ, cS + TILE * (n & 1), mk + (n % C::NSK) * TS, j > 0 ? 1u : 0u);
+          tc_commit(&M.k_empty[n % C::NSK]);
           if (j + 1 == T) tc_commit(&M.dq_done);
-          if (j + 2 < T) ok = front(n + 2, j + 3 == T);
+          if (j + 2 < T) ok = s_of(n + 2);
         }
       }
       tc_commit(&M.drain);
@@ -540,10 +546,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
     __syncwarp();
   } else {
-    // query rows 32 quarter.., key columns 32 cg.. of the group's units
-    const int quarter = warp & 3, cg = (warp >> 2) & 1, grp = warp >> 3;
+    const int quarter = warp & 3, cg = warp >> 2;  // query rows 32 quarter.., key columns 32 cg..
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const uint32_t aS = cS + lane_base + UNIT * grp + COLS * cg, aP = cP + lane_base + UNIT * grp + COLS * cg;
+    const uint32_t aP = cP + lane_base + COLS * cg;
     uint32_t n = 0, qn = 0;
     bool ok = true;
     for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
@@ -552,14 +557,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const int64_t ro = ((int64_t)I.b * p.Hq + I.h) * p.Npad + t;
       const float nl = p.lse2[ro], nd = p.dsum[ro];  // -lse2, -D
       const float2 cc = make_float2(p.c, p.c), ll = make_float2(nl, nl), dd = make_float2(nd, nd);
-      // the groups take the units of all items in turn (buffer n & 1)
-      for (uint32_t k = n + ((n ^ (uint32_t)grp) & 1u); k < n + I.kt.count; k += 2) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&M.s_full[grp], (k >> 1) & 1u, abort))) {
+      for (uint32_t k = n; k < n + I.kt.count; ++k) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&M.s_full[k & 1], (k >> 1) & 1u, abort))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const int u0 = I.kt.tile((int)(k - n)) * UNIT + COLS * cg;  // this warp's first key
+        const uint32_t aS = cS + lane_base + TILE * (k & 1) + COLS * cg;
+        const int u0 = I.kt.tile((int)(k - n)) * TILE + COLS * cg;  // this warp's first key
         const bool all = u0 + COLS - 1 <= ta && (tb - u0 < p.window || u0 + COLS <= p.sinks);
         const int hi = t - u0, lo = t - p.window - u0, sk = p.sinks - u0;  // sees lo < c <= hi, or c < sk
         float x[COLS];
@@ -571,7 +576,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           x[c] = ex2(y.x);
           x[c + 1] = ex2(y.y);
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(&M.dp_full[grp], (k >> 1) & 1u, abort))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&M.dp_full, k & 1u, abort))) {
           ok = false;
           break;
         }
@@ -592,11 +597,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
 #pragma unroll
         for (int c = 0; c < COLS; c += 2) pk[c / 2] = pack_bf16(x[c], x[c + 1]);
-        tmem_st16(aP, pk);
+        tmem_st16(aS, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&M.ds_full[grp]);
+        if (lane == 0) mbar_arrive(&M.ds_full);
       }
       n += I.kt.count;
       if (!ok || !__all_sync(0xffffffffu, mbar_wait(&M.dq_done, qn & 1u, abort))) break;
@@ -606,9 +611,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll 1
       for (int c0 = 0; c0 < W; c0 += 16) {
         uint32_t r[16];
-        tmem_ld16(cQ + lane_base + W * (warp >> 2) + c0, r);
+        tmem_ld16(cQ + lane_base + W * cg + c0, r);
         tmem_wait_ld();
-        if (t < p.N) store16(row_ptr_w<bf16>(p.dq, I.b, I.h, t) + W * (warp >> 2) + c0, r, p.scale);
+        if (t < p.N) store16(row_ptr_w<bf16>(p.dq, I.b, I.h, t) + W * cg + c0, r, p.scale);
       }
       tc_fence_before();
       __syncwarp();
@@ -638,14 +643,13 @@ static_assert(dkv_smem<128>() <= 232448 && dq_smem<128>() <= 232448, "shared mem
 template <int HD>
 cudaError_t launch(const WinDims& D, const WinBwdArgs& a, int32_t* status, cudaStream_t st) {
   BwdParams p{};
-  // Boxes: the CTA's own tile of 128 rows, the other side's units of 64.
-  CUtensorMap qt, kt, vt, gt, qu, ku, vu, gu;
+  // Boxes of 128 rows, and of 64 for the units of queries.
+  CUtensorMap q, k, v, g, qu, gu;
   auto map = [&](CUtensorMap* m, const TensorRef& t, int H, int rows, int* zero) {
     return win_tma_map(m, t, D.B, H, D.N, rows, HD, zero);
   };
-  if (!map(&qt, a.q, D.Hq, TILE, &p.zq) || !map(&gt, a.g, D.Hq, TILE, &p.zg) || !map(&kt, a.k, D.Hkv, TILE, &p.zk) ||
-      !map(&vt, a.v, D.Hkv, TILE, &p.zv) || !map(&qu, a.q, D.Hq, UNIT, &p.zq) || !map(&gu, a.g, D.Hq, UNIT, &p.zg) ||
-      !map(&ku, a.k, D.Hkv, UNIT, &p.zk) || !map(&vu, a.v, D.Hkv, UNIT, &p.zv))
+  if (!map(&q, a.q, D.Hq, TILE, &p.zq) || !map(&g, a.g, D.Hq, TILE, &p.zg) || !map(&k, a.k, D.Hkv, TILE, &p.zk) ||
+      !map(&v, a.v, D.Hkv, TILE, &p.zv) || !map(&qu, a.q, D.Hq, UNIT, &p.zq) || !map(&gu, a.g, D.Hq, UNIT, &p.zg))
     return cudaErrorInvalidValue;
   cudaError_t e = launch_win_bwd_pre(D, a, st);
   if (e != cudaSuccess) return e;
@@ -674,14 +678,14 @@ cudaError_t launch(const WinDims& D, const WinBwdArgs& a, int32_t* status, cudaS
   p.scale = D.scale;
   auto dkv = win_bwd_dkv_tc_kernel<HD>;
   if ((e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, dkv_smem<HD>())) != cudaSuccess) return e;
-  dkv<<<dim3(cp.chunks * D.Hkv, D.B), NTHREADS, dkv_smem<HD>(), st>>>(qu, kt, vt, gu, p);
+  dkv<<<dim3(cp.chunks * D.Hkv, D.B), NTHREADS, dkv_smem<HD>(), st>>>(qu, k, v, gu, p);
   count_launches(1);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if ((e = launch_win_kvjoin<TILE>(D, a, cp, p.part, st)) != cudaSuccess) return e;
   auto dq = win_bwd_dq_tc_kernel<HD>;
   if ((e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, dq_smem<HD>())) != cudaSuccess) return e;
   const int64_t items = (int64_t)D.B * D.Hq * cp.NT;
-  dq<<<(unsigned)(items < kCtas ? items : kCtas), NTHREADS, dq_smem<HD>(), st>>>(qt, ku, vu, gt, p);
+  dq<<<(unsigned)(items < kCtas ? items : kCtas), NTHREADS, dq_smem<HD>(), st>>>(q, k, v, g, p);
   count_launches(1);
   return cudaGetLastError();
 }
