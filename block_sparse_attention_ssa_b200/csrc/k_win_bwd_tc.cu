@@ -61,6 +61,7 @@ struct BwdParams {
   int B, Hq, Hkv, g, N, Npad, NT, window, sinks, L, partials;
   int zq, zk, zv, zg;  // broadcast dimensions: bit 0 batch, bit 1 head
   float c, scale;      // c = scale * log2(e)
+  bool wide_q, wide_kv;  // gradients in 32-byte pieces
 };
 
 // D (128 x R) = A B^T over HD: a 128-row tile and R rows (a tile's or a unit's), both K-major in shared memory
@@ -101,16 +102,11 @@ __device__ __forceinline__ bool misaligned(const uint8_t* smem, int32_t* status)
 }
 
 // 16 columns of an accumulator row, scaled, to bf16 memory.
-__device__ __forceinline__ void store16(bf16* dst, const uint32_t (&r)[16], float mul) {
-  uint4* d4 = reinterpret_cast<uint4*>(dst);
+__device__ __forceinline__ void store16(bf16* dst, const uint32_t (&r)[16], float mul, bool wide) {
+  uint32_t o[8];
 #pragma unroll
-  for (int v = 0; v < 2; ++v) {
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      o[i] = pack_bf16(__uint_as_float(r[8 * v + 2 * i]) * mul, __uint_as_float(r[8 * v + 2 * i + 1]) * mul);
-    d4[v] = make_uint4(o[0], o[1], o[2], o[3]);
-  }
+  for (int i = 0; i < 8; ++i) o[i] = pack_bf16(__uint_as_float(r[2 * i]) * mul, __uint_as_float(r[2 * i + 1]) * mul);
+  store_32b(dst, o, wide);
 }
 
 // ================================================================ dK, dV
@@ -361,7 +357,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (!mine) continue;
         if (ch.n == 1) {
           const TensorRef& t = which ? p.dv : p.dk;
-          store16(row_ptr_w<bf16>(t, b, kvh, u) + col0 + col, r, which ? 1.0f : p.scale);
+          store16(row_ptr_w<bf16>(t, b, kvh, u) + col0 + col, r, which ? 1.0f : p.scale, p.wide_kv);
         } else {
           uint4* d4 = reinterpret_cast<uint4*>(part + which * TILE * HD + col);
 #pragma unroll
@@ -551,11 +547,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t aP = cP + lane_base + COLS * cg;
     uint32_t n = 0, qn = 0;
     bool ok = true;
+    DqItem I = item(blockIdx.x);
+    float nl, nd;  // -lse2, -D
+    auto statistics = [&](const DqItem& J) {
+      const int64_t ro = ((int64_t)J.b * p.Hq + J.h) * p.Npad + J.t0 + quarter * 32 + lane;
+      nl = p.lse2[ro];
+      nd = p.dsum[ro];
+    };
+    statistics(I);
     for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
-      const DqItem I = item(i);
       const int t = I.t0 + quarter * 32 + lane, ta = I.t0 + quarter * 32, tb = ta + 31;
-      const int64_t ro = ((int64_t)I.b * p.Hq + I.h) * p.Npad + t;
-      const float nl = p.lse2[ro], nd = p.dsum[ro];  // -lse2, -D
       const float2 cc = make_float2(p.c, p.c), ll = make_float2(nl, nl), dd = make_float2(nd, nd);
       for (uint32_t k = n; k < n + I.kt.count; ++k) {
         if (!__all_sync(0xffffffffu, mbar_wait(&M.s_full[k & 1], (k >> 1) & 1u, abort))) {
@@ -604,6 +605,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (lane == 0) mbar_arrive(&M.ds_full);
       }
       n += I.kt.count;
+      // The next item's coordinates and statistics are fetched while the last product runs.
+      DqItem J = I;
+      if (i + (int)gridDim.x < items) {
+        J = item(i + gridDim.x);
+        statistics(J);
+      }
       if (!ok || !__all_sync(0xffffffffu, mbar_wait(&M.dq_done, qn & 1u, abort))) break;
       ++qn;
       tc_fence_after();
@@ -613,11 +620,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         uint32_t r[16];
         tmem_ld16(cQ + lane_base + W * cg + c0, r);
         tmem_wait_ld();
-        if (t < p.N) store16(row_ptr_w<bf16>(p.dq, I.b, I.h, t) + W * cg + c0, r, p.scale);
+        if (t < p.N) store16(row_ptr_w<bf16>(p.dq, I.b, I.h, t) + W * cg + c0, r, p.scale, p.wide_q);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&M.dq_free);
+      I = J;
     }
   }
   tc_fence_before();
@@ -676,6 +684,8 @@ cudaError_t launch(const WinDims& D, const WinBwdArgs& a, int32_t* status, cudaS
   p.partials = cp.partials;
   p.c = D.scale * kLog2e;
   p.scale = D.scale;
+  p.wide_q = wide_rows(a.dq);
+  p.wide_kv = wide_rows(a.dk) && wide_rows(a.dv);
   auto dkv = win_bwd_dkv_tc_kernel<HD>;
   if ((e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, dkv_smem<HD>())) != cudaSuccess) return e;
   dkv<<<dim3(cp.chunks * D.Hkv, D.B), NTHREADS, dkv_smem<HD>(), st>>>(qu, k, v, gu, p);

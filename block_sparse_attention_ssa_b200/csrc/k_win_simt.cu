@@ -42,25 +42,29 @@ struct SimtParams {
   float* part;
 };
 
-// 64 rows of HD values into shared memory as fp32; a null row pointer gives zeros.
-template <typename T, int HD, typename F>
-__device__ __forceinline__ void load_rows(float* dst, F row) {
-  constexpr int V = Vec16<T>::kN, PER = HD / V;
-  for (int e = threadIdx.x; e < BT * PER; e += NT_) {
-    const int r = e / PER, c = (e % PER) * V;
-    float x[V];
-    const T* p = row(r);
-    if (p != nullptr) {
-      Vec16<T>::load(p + c, x);
-    } else {
+// A 64-row tile on its way through registers, so that its loads are in flight while the tile before is used; a
+// null row pointer gives zeros.
+template <int HD, int THREADS>
+struct TileRegs {
+  static constexpr int PER = HD / 4, N = BT * PER / THREADS;
+  float4 v[N];
+  template <typename F>
+  __device__ __forceinline__ void fetch(F row) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) x[i] = 0.f;
+    for (int i = 0; i < N; ++i) {
+      const int e = threadIdx.x + i * THREADS;
+      const float* p = row(e / PER);
+      v[i] = p != nullptr ? *reinterpret_cast<const float4*>(p + (e % PER) * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-#pragma unroll
-    for (int i = 0; i < V; i += 4)
-      *reinterpret_cast<float4*>(dst + r * Pitch<HD>::v + c + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
   }
-}
+  __device__ __forceinline__ void put(float* dst) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = threadIdx.x + i * THREADS;
+      *reinterpret_cast<float4*>(dst + (e / PER) * Pitch<HD>::v + (e % PER) * 4) = v[i];
+    }
+  }
+};
 
 // s[i][j] = A[4 ty + i] . B[tx + 16 j]
 template <int HD>
@@ -119,12 +123,12 @@ __device__ __forceinline__ void weighted(const float* W, const float* X, int tx,
   }
 }
 
-template <typename T, int HD>
-__device__ __forceinline__ void store_row(T* dst, const float* acc, int tx, float mul) {
+template <int HD>
+__device__ __forceinline__ void store_row(float* dst, const float* acc, int tx, float mul) {
 #pragma unroll
   for (int q = 0; q < HD / 64; ++q)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) dst[64 * q + 4 * tx + i] = from_f32<T>(acc[4 * q + i] * mul);
+    *reinterpret_cast<float4*>(dst + 64 * q + 4 * tx) =
+        make_float4(acc[4 * q] * mul, acc[4 * q + 1] * mul, acc[4 * q + 2] * mul, acc[4 * q + 3] * mul);
 }
 
 template <int HD>
@@ -133,8 +137,8 @@ constexpr size_t fwd_smem() {
 }
 
 // ================================================================ forward
-template <typename T, int HD, bool PAGED>
-__global__ void __launch_bounds__(NT_) win_fwd_simt_kernel(SimtParams p) {
+template <int HD, bool PAGED>
+__global__ void __launch_bounds__(NT_, 2) win_fwd_simt_kernel(SimtParams p) {
   extern __shared__ float sm[];
   float* sQ = sm;
   float* sX = sQ + BT * Pitch<HD>::v;  // K, then V
@@ -198,9 +202,11 @@ __global__ void __launch_bounds__(NT_) win_fwd_simt_kernel(SimtParams p) {
     }
     auto tok_of = [&](int r) { return PAGED ? r / per_tok : r; };
     auto head_of = [&](int r) { return PAGED ? head0 + r % per_tok : head0; };
-    load_rows<T, HD>(sQ, [&](int r) -> const T* {
-      return r < nrows ? row_ptr<T>(p.q, PAGED ? 0 : b, head_of(r), q0row + tok_of(r)) : nullptr;
+    TileRegs<HD, NT_> regs;
+    regs.fetch([&](int r) -> const float* {
+      return r < nrows ? row_ptr<float>(p.q, PAGED ? 0 : b, head_of(r), q0row + tok_of(r)) : nullptr;
     });
+    regs.put(sQ);
 
     float acc[4][HD / 16], m[4], l[4];
     int pos[4];
@@ -214,19 +220,25 @@ __global__ void __launch_bounds__(NT_) win_fwd_simt_kernel(SimtParams p) {
     }
     const int pmax = p0 + tok_of(nrows - 1), lo_min = p0 - p.window + 1;
 
-    for (int j = at.off; j < at.off + take && j < kt.count; ++j) {
+    // A key that no row of the item sees is not read (its memory may hold anything).
+    auto keys = [&](const TensorRef& t, int j) {
       const int u0 = kt.tile(j) * BT;
-      // A key that no row of the item sees is not read (its memory may hold anything).
-      auto key_row = [&](const TensorRef& t, int r) -> const T* {
+      return [&, t, u0](int r) -> const float* {
         const int u = u0 + r;
         if (u > pmax || u >= len || (u < lo_min && u >= p.sinks)) return nullptr;
-        if (!PAGED) return row_ptr<T>(t, b, kvh, u);
+        if (!PAGED) return row_ptr<float>(t, b, kvh, u);
         const int pg = p.table[(int64_t)b * p.max_pages + u / p.page];
-        return (unsigned)pg < (unsigned)p.num_pages ? row_ptr<T>(t, pg, kvh, u % p.page) : nullptr;
+        return (unsigned)pg < (unsigned)p.num_pages ? row_ptr<float>(t, pg, kvh, u % p.page) : nullptr;
       };
+    };
+    const int end = min(at.off + take, kt.count);
+    if (at.off < end) regs.fetch(keys(p.k, at.off));
+    for (int j = at.off; j < end; ++j) {
+      const int u0 = kt.tile(j) * BT;
       __syncthreads();
-      load_rows<T, HD>(sX, [&](int r) { return key_row(p.k, r); });
+      regs.put(sX);
       __syncthreads();
+      regs.fetch(keys(p.v, j));
       float x[4][4];
       dots<HD>(sQ, sX, tx, ty, x);
       bool held[4];
@@ -268,8 +280,9 @@ __global__ void __launch_bounds__(NT_) win_fwd_simt_kernel(SimtParams p) {
         for (int c = 0; c < HD / 16; ++c) acc[i][c] *= f;
       }
       __syncthreads();
-      load_rows<T, HD>(sX, [&](int r) { return key_row(p.v, r); });
+      regs.put(sX);
       __syncthreads();
+      if (j + 1 < end) regs.fetch(keys(p.k, j + 1));
       weighted<HD>(sP, sX, tx, ty, acc);
     }
 
@@ -291,7 +304,7 @@ __global__ void __launch_bounds__(NT_) win_fwd_simt_kernel(SimtParams p) {
         continue;
       }
       const float inv = l[i] == 0.f ? 0.f : 1.0f / l[i];
-      store_row<T, HD>(row_ptr_w<T>(p.h, PAGED ? 0 : b, head_of(r), q0row + tok_of(r)), acc[i], tx, inv);
+      store_row<HD>(row_ptr_w<float>(p.h, PAGED ? 0 : b, head_of(r), q0row + tok_of(r)), acc[i], tx, inv);
       if (tx == 0) {
         const int64_t o = PAGED ? (int64_t)head_of(r) * p.T + q0row + tok_of(r)
                                 : ((int64_t)b * p.Hq + head0) * p.N + q0row + r;
@@ -369,134 +382,219 @@ struct SimtBwd {
   float c, scale;
 };
 
+// 512 threads in two groups of 256: the first forms the weights, the second dP, side by side (twice the warps
+// for the same tiles; one group of 256 took 165 us for dkv and 77 us for dq at N = 1000, 8 heads, d = 128).
+// The next step's tiles are fetched into registers while this one is computed.
+constexpr int BWD_THREADS = 512;
+
 template <int HD>
 constexpr size_t bwd_smem() {
-  return (size_t)(4 * BT * Pitch<HD>::v + BT * SP) * 4;
+  return (size_t)(4 * BT * Pitch<HD>::v + 2 * BT * SP) * 4;
 }
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(NT_) win_bwd_dq_simt_kernel(SimtBwd p) {
+__device__ __forceinline__ void put4x4(float* P, const float (&x)[4][4], int tx, int ty) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj) P[(4 * ty + i) * SP + tx + 16 * jj] = x[i][jj];
+}
+
+template <int HD>
+__global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dq_simt_kernel(SimtBwd p) {
   extern __shared__ float sm[];
   float* sQ = sm;
   float* sG = sQ + BT * Pitch<HD>::v;
   float* sK = sG + BT * Pitch<HD>::v;
   float* sV = sK + BT * Pitch<HD>::v;
-  float* sS = sV + BT * Pitch<HD>::v;
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  float* sP = sV + BT * Pitch<HD>::v;
+  float* sS = sP + BT * SP;
+  const int grp = threadIdx.x >> 8, tid = threadIdx.x & 255, tx = tid & 15, ty = tid >> 4;
   const int planes = (int)(gridDim.x / p.NT);
   const int plane = (int)blockIdx.x % planes, qt = p.NT - 1 - (int)blockIdx.x / planes;
   const int b = plane / p.Hq, h = plane % p.Hq, kvh = h / p.grp;
   const int q0 = qt * BT, nrows = min(BT, p.N - q0);
   const KeyTiles kt = key_tiles<BT>(q0, q0 + nrows - 1, p.window, p.sinks);
-  load_rows<T, HD>(sQ, [&](int r) -> const T* { return r < nrows ? row_ptr<T>(p.q, b, h, q0 + r) : nullptr; });
-  load_rows<T, HD>(sG, [&](int r) -> const T* { return r < nrows ? row_ptr<T>(p.g, b, h, q0 + r) : nullptr; });
-  float ls[4], ds[4], acc[4][HD / 16];  // -lse2, -D
+  TileRegs<HD, BWD_THREADS> ra, rb;
+  auto query = [&](const TensorRef& t) {
+    return [&, t](int r) -> const float* { return r < nrows ? row_ptr<float>(t, b, h, q0 + r) : nullptr; };
+  };
+  auto key = [&](const TensorRef& t, int j) {
+    const int u0 = kt.tile(j) * BT;
+    return [&, t, u0](int r) -> const float* { return u0 + r < p.N ? row_ptr<float>(t, b, kvh, u0 + r) : nullptr; };
+  };
+  ra.fetch(query(p.q));
+  rb.fetch(query(p.g));
+  ra.put(sQ);
+  rb.put(sG);
+  ra.fetch(key(p.k, 0));
+  rb.fetch(key(p.v, 0));
+  constexpr int CT = HD / 32;  // columns of a thread: CT tx + HD/2 grp ..
+  const int col = CT * tx + HD / 2 * grp;
+  float st[4], acc[4][CT];  // st: -lse2 (first group), -D (second)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t o = ((int64_t)b * p.Hq + h) * p.Npad + q0 + 4 * ty + i;
-    ls[i] = p.lse2[o];
-    ds[i] = p.dsum[o];
+    st[i] = grp ? p.dsum[o] : p.lse2[o];
 #pragma unroll
-    for (int c = 0; c < HD / 16; ++c) acc[i][c] = 0.f;
+    for (int c = 0; c < CT; ++c) acc[i][c] = 0.f;
   }
   for (int j = 0; j < kt.count; ++j) {
     const int u0 = kt.tile(j) * BT;
     __syncthreads();
-    load_rows<T, HD>(sK, [&](int r) -> const T* { return u0 + r < p.N ? row_ptr<T>(p.k, b, kvh, u0 + r) : nullptr; });
-    load_rows<T, HD>(sV, [&](int r) -> const T* { return u0 + r < p.N ? row_ptr<T>(p.v, b, kvh, u0 + r) : nullptr; });
+    ra.put(sK);
+    rb.put(sV);
     __syncthreads();
-    float x[4][4], y[4][4];
-    dots<HD>(sQ, sK, tx, ty, x);
-    dots<HD>(sG, sV, tx, ty, y);
+    if (j + 1 < kt.count) {
+      ra.fetch(key(p.k, j + 1));
+      rb.fetch(key(p.v, j + 1));
+    }
+    float x[4][4];
+    dots<HD>(grp ? sG : sQ, grp ? sV : sK, tx, ty, x);
+    if (grp == 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int jj = 0; jj < 4; ++jj) {
-        const int u = u0 + tx + 16 * jj, t = q0 + 4 * ty + i;
-        const bool see = u <= t && (t - u < p.window || u < p.sinks);
-        sS[(4 * ty + i) * SP + tx + 16 * jj] = see ? exp2f(fmaf(x[i][jj], p.c, ls[i])) * (y[i][jj] + ds[i]) : 0.f;
+        for (int jj = 0; jj < 4; ++jj) {
+          const int u = u0 + tx + 16 * jj, t = q0 + 4 * ty + i;
+          const bool see = u <= t && (t - u < p.window || u < p.sinks);
+          x[i][jj] = see ? exp2f(fmaf(x[i][jj], p.c, st[i])) : 0.f;
+        }
+      put4x4(sP, x, tx, ty);
+    }
+    __syncthreads();
+    if (grp == 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+          const float pv = sP[(4 * ty + i) * SP + tx + 16 * jj];
+          x[i][jj] = pv != 0.f ? pv * (x[i][jj] + st[i]) : 0.f;
+        }
+      put4x4(sS, x, tx, ty);
+    }
+    __syncthreads();
+#pragma unroll 2
+    for (int u = 0; u < BT; u += 4) {
+      float w[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 t = *reinterpret_cast<const float4*>(sS + (4 * ty + i) * SP + u);
+        w[i][0] = t.x;
+        w[i][1] = t.y;
+        w[i][2] = t.z;
+        w[i][3] = t.w;
       }
-    __syncthreads();
-    weighted<HD>(sS, sK, tx, ty, acc);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float* kr = sK + (u + e) * Pitch<HD>::v + col;
+#pragma unroll
+        for (int c = 0; c < CT; c += 2) {
+          const float2 k2 = *reinterpret_cast<const float2*>(kr + c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            acc[i][c] = fmaf(w[i][e], k2.x, acc[i][c]);
+            acc[i][c + 1] = fmaf(w[i][e], k2.y, acc[i][c + 1]);
+          }
+        }
+      }
+    }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (4 * ty + i < nrows) store_row<T, HD>(row_ptr_w<T>(p.dq, b, h, q0 + 4 * ty + i), acc[i], tx, p.scale);
+    if (4 * ty + i < nrows) {
+      float* dst = row_ptr_w<float>(p.dq, b, h, q0 + 4 * ty + i) + col;
+#pragma unroll
+      for (int c = 0; c < CT; c += 2) *reinterpret_cast<float2*>(dst + c) = make_float2(acc[i][c] * p.scale, acc[i][c + 1] * p.scale);
+    }
 }
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(NT_) win_bwd_dkv_simt_kernel(SimtBwd p) {
+template <int HD>
+__global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dkv_simt_kernel(SimtBwd p) {
   extern __shared__ float sm[];
   float* sK = sm;
   float* sV = sK + BT * Pitch<HD>::v;
   float* sQ = sV + BT * Pitch<HD>::v;
   float* sG = sQ + BT * Pitch<HD>::v;
-  float* sS = sG + BT * Pitch<HD>::v;
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  float* sP = sG + BT * Pitch<HD>::v;
+  float* sS = sP + BT * SP;
+  const int grp = threadIdx.x >> 8, tid = threadIdx.x & 255, tx = tid & 15, ty = tid >> 4;
   const int plane = (int)blockIdx.x % p.Hkv + (int)blockIdx.y * p.Hkv;
   const Chunk ch = find_chunk<BT>((int)blockIdx.x / p.Hkv, p.NT, p.L, p.grp, p.N, p.window, p.sinks);
   const int b = plane / p.Hkv, kvh = plane % p.Hkv;
   const int u0 = ch.kt * BT, nq = query_tiles_of<BT>(ch.kt, p.N, p.window, p.sinks);
   const int first = ch.idx * p.L, last = min(first + p.L, nq * p.grp);
-  load_rows<T, HD>(sK, [&](int r) -> const T* { return u0 + r < p.N ? row_ptr<T>(p.k, b, kvh, u0 + r) : nullptr; });
-  load_rows<T, HD>(sV, [&](int r) -> const T* { return u0 + r < p.N ? row_ptr<T>(p.v, b, kvh, u0 + r) : nullptr; });
-  float dk[4][HD / 16], dv[4][HD / 16];
+  TileRegs<HD, BWD_THREADS> ra, rb;
+  float nx[4];  // -lse2 (first group) or -D (second) of the next step
+  auto key = [&](const TensorRef& t) {
+    return [&, t](int r) -> const float* { return u0 + r < p.N ? row_ptr<float>(t, b, kvh, u0 + r) : nullptr; };
+  };
+  auto fetch = [&](int s) {
+    const int h = kvh * p.grp + s / nq, q0 = (ch.kt + s % nq) * BT;
+    ra.fetch([&](int r) -> const float* { return q0 + r < p.N ? row_ptr<float>(p.q, b, h, q0 + r) : nullptr; });
+    rb.fetch([&](int r) -> const float* { return q0 + r < p.N ? row_ptr<float>(p.g, b, h, q0 + r) : nullptr; });
+    const float* row = (grp ? p.dsum : p.lse2) + ((int64_t)b * p.Hq + h) * p.Npad + q0 + tx;
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj) nx[jj] = row[16 * jj];
+  };
+  ra.fetch(key(p.k));
+  rb.fetch(key(p.v));
+  ra.put(sK);
+  rb.put(sV);
+  fetch(first);
+  float acc[4][HD / 16];  // dV (first group) or dK (second)
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int c = 0; c < HD / 16; ++c) dk[i][c] = dv[i][c] = 0.f;
-  for (int st = first; st < last; ++st) {
-    const int h = kvh * p.grp + st / nq, q0 = (ch.kt + st % nq) * BT;
-    __syncthreads();
-    load_rows<T, HD>(sQ, [&](int r) -> const T* { return q0 + r < p.N ? row_ptr<T>(p.q, b, h, q0 + r) : nullptr; });
-    load_rows<T, HD>(sG, [&](int r) -> const T* { return q0 + r < p.N ? row_ptr<T>(p.g, b, h, q0 + r) : nullptr; });
-    float ls[4], ds[4];  // -lse2, -D
+    for (int c = 0; c < HD / 16; ++c) acc[i][c] = 0.f;
+  for (int s = first; s < last; ++s) {
+    const int q0 = (ch.kt + s % nq) * BT;
+    float st[4];
 #pragma unroll
-    for (int jj = 0; jj < 4; ++jj) {
-      const int64_t o = ((int64_t)b * p.Hq + h) * p.Npad + q0 + tx + 16 * jj;
-      ls[jj] = p.lse2[o];
-      ds[jj] = p.dsum[o];
+    for (int jj = 0; jj < 4; ++jj) st[jj] = nx[jj];
+    __syncthreads();
+    ra.put(sQ);
+    rb.put(sG);
+    __syncthreads();
+    if (s + 1 < last) fetch(s + 1);
+    float x[4][4];
+    dots<HD>(grp ? sV : sK, grp ? sG : sQ, tx, ty, x);
+    if (grp == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+          const int u = u0 + 4 * ty + i, t = q0 + tx + 16 * jj;
+          const bool see = u <= t && (t - u < p.window || u < p.sinks);
+          x[i][jj] = see ? exp2f(fmaf(x[i][jj], p.c, st[jj])) : 0.f;
+        }
+      put4x4(sP, x, tx, ty);
     }
     __syncthreads();
-    float x[4][4], y[4][4];
-    dots<HD>(sK, sQ, tx, ty, x);
-    dots<HD>(sV, sG, tx, ty, y);
+    if (grp == 1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int jj = 0; jj < 4; ++jj) {
-        const int u = u0 + 4 * ty + i, t = q0 + tx + 16 * jj;
-        const bool see = u <= t && (t - u < p.window || u < p.sinks);
-        const float pv = see ? exp2f(fmaf(x[i][jj], p.c, ls[jj])) : 0.f;
-        sS[(4 * ty + i) * SP + tx + 16 * jj] = pv;
-        y[i][jj] = see ? pv * (y[i][jj] + ds[jj]) : 0.f;
-      }
-    __syncthreads();
-    weighted<HD>(sS, sG, tx, ty, dv);
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int jj = 0; jj < 4; ++jj) sS[(4 * ty + i) * SP + tx + 16 * jj] = y[i][jj];
-    __syncthreads();
-    weighted<HD>(sS, sQ, tx, ty, dk);
+        for (int jj = 0; jj < 4; ++jj) {
+          const float pv = sP[(4 * ty + i) * SP + tx + 16 * jj];
+          x[i][jj] = pv != 0.f ? pv * (x[i][jj] + st[jj]) : 0.f;
+        }
+      put4x4(sS, x, tx, ty);
+      asm volatile("bar.sync 1, 256;" ::: "memory");  // the second group's own tile
+    }
+    weighted<HD>(grp ? sS : sP, grp ? sQ : sG, tx, ty, acc);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int u = u0 + 4 * ty + i;
     if (u >= p.N) continue;
     if (ch.n == 1) {
-      store_row<T, HD>(row_ptr_w<T>(p.dk, b, kvh, u), dk[i], tx, p.scale);
-      store_row<T, HD>(row_ptr_w<T>(p.dv, b, kvh, u), dv[i], tx, 1.0f);
+      store_row<HD>(row_ptr_w<float>(grp ? p.dk : p.dv, b, kvh, u), acc[i], tx, grp ? p.scale : 1.0f);
     } else {
-      float* base = p.part + ((size_t)plane * p.partials + ch.slot + ch.idx) * (2 * BT * HD) + (4 * ty + i) * HD;
+      float* base = p.part + ((size_t)plane * p.partials + ch.slot + ch.idx) * (2 * BT * HD) + (grp ? 0 : BT * HD) + (4 * ty + i) * HD;
 #pragma unroll
-      for (int q = 0; q < HD / 64; ++q) {
+      for (int q = 0; q < HD / 64; ++q)
         *reinterpret_cast<float4*>(base + 64 * q + 4 * tx) =
-            make_float4(dk[i][4 * q], dk[i][4 * q + 1], dk[i][4 * q + 2], dk[i][4 * q + 3]);
-        *reinterpret_cast<float4*>(base + BT * HD + 64 * q + 4 * tx) =
-            make_float4(dv[i][4 * q], dv[i][4 * q + 1], dv[i][4 * q + 2], dv[i][4 * q + 3]);
-      }
+            make_float4(acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]);
     }
   }
 }
@@ -556,7 +654,7 @@ cudaError_t set_smem(K kern, size_t bytes) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <typename T, int HD>
+template <int HD>
 cudaError_t fwd_t(const WinDims& D, const WinFwdArgs& a, cudaStream_t st) {
   SimtParams p{};
   p.q = a.q;
@@ -571,7 +669,7 @@ cudaError_t fwd_t(const WinDims& D, const WinFwdArgs& a, cudaStream_t st) {
   p.sinks = D.sinks;
   p.NT = (D.N + BT - 1) / BT;
   p.c = D.scale * kLog2e;
-  auto kern = win_fwd_simt_kernel<T, HD, false>;
+  auto kern = win_fwd_simt_kernel<HD, false>;
   cudaError_t e = set_smem(kern, fwd_smem<HD>());
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)((int64_t)p.NT * D.B * D.Hq), NT_, fwd_smem<HD>(), st>>>(p);
@@ -579,7 +677,7 @@ cudaError_t fwd_t(const WinDims& D, const WinFwdArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <typename T, int HD>
+template <int HD>
 cudaError_t bwd_t(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
   cudaError_t e = launch_win_bwd_pre(D, a, st);
   if (e != cudaSuccess) return e;
@@ -609,15 +707,15 @@ cudaError_t bwd_t(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
   p.partials = cp.partials;
   p.c = D.scale * kLog2e;
   p.scale = D.scale;
-  auto dkv = win_bwd_dkv_simt_kernel<T, HD>;
+  auto dkv = win_bwd_dkv_simt_kernel<HD>;
   if ((e = set_smem(dkv, bwd_smem<HD>())) != cudaSuccess) return e;
-  dkv<<<dim3(cp.chunks * D.Hkv, D.B), NT_, bwd_smem<HD>(), st>>>(p);
+  dkv<<<dim3(cp.chunks * D.Hkv, D.B), BWD_THREADS, bwd_smem<HD>(), st>>>(p);
   count_launches(1);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if ((e = launch_win_kvjoin<BT>(D, a, cp, p.part, st)) != cudaSuccess) return e;
-  auto dq = win_bwd_dq_simt_kernel<T, HD>;
+  auto dq = win_bwd_dq_simt_kernel<HD>;
   if ((e = set_smem(dq, bwd_smem<HD>())) != cudaSuccess) return e;
-  dq<<<(unsigned)((int64_t)cp.NT * D.B * D.Hq), NT_, bwd_smem<HD>(), st>>>(p);
+  dq<<<(unsigned)((int64_t)cp.NT * D.B * D.Hq), BWD_THREADS, bwd_smem<HD>(), st>>>(p);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -641,7 +739,7 @@ cudaError_t join_t(const WinDims& D, const WinBwdArgs& a, const ChunkPlan& p, co
   return cudaGetLastError();
 }
 
-template <typename T, int HD>
+template <int HD>
 cudaError_t paged_t(const PagedDims& D, const PagedArgs& a, cudaStream_t st) {
   SimtParams p{};
   p.q = a.q;
@@ -662,7 +760,7 @@ cudaError_t paged_t(const PagedDims& D, const PagedArgs& a, cudaStream_t st) {
   const int TI = BT / D.g;
   p.batch = Batch{a.q_start, a.kv_len, D.seqs, D.T, D.max_pages * D.page, TI, D.window, D.sinks, D.Hkv};
   p.part = static_cast<float*>(a.ws);
-  auto kern = win_fwd_simt_kernel<T, HD, true>;
+  auto kern = win_fwd_simt_kernel<HD, true>;
   cudaError_t e = set_smem(kern, fwd_smem<HD>());
   if (e != cudaSuccess) return e;
   kern<<<kPagedCtas, NT_, fwd_smem<HD>(), st>>>(p);
@@ -674,17 +772,17 @@ cudaError_t paged_t(const PagedDims& D, const PagedArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_win_fwd_simt(const WinDims& D, const WinFwdArgs& a, cudaStream_t st) {
-  return D.d == 64 ? fwd_t<float, 64>(D, a, st) : fwd_t<float, 128>(D, a, st);
+  return D.d == 64 ? fwd_t<64>(D, a, st) : fwd_t<128>(D, a, st);
 }
 cudaError_t launch_win_bwd_pre(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
   if (D.dtype == SSA_BF16) return D.d == 64 ? pre_t<__nv_bfloat16, 64>(D, a, st) : pre_t<__nv_bfloat16, 128>(D, a, st);
   return D.d == 64 ? pre_t<float, 64>(D, a, st) : pre_t<float, 128>(D, a, st);
 }
 cudaError_t launch_win_bwd_simt(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
-  return D.d == 64 ? bwd_t<float, 64>(D, a, st) : bwd_t<float, 128>(D, a, st);
+  return D.d == 64 ? bwd_t<64>(D, a, st) : bwd_t<128>(D, a, st);
 }
 cudaError_t launch_paged_simt(const PagedDims& D, const PagedArgs& a, cudaStream_t st) {
-  return D.d == 64 ? paged_t<float, 64>(D, a, st) : paged_t<float, 128>(D, a, st);
+  return D.d == 64 ? paged_t<64>(D, a, st) : paged_t<128>(D, a, st);
 }
 
 template <int BTJ>

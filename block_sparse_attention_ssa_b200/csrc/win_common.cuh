@@ -274,6 +274,11 @@ cudaError_t launch_paged_simt(const PagedDims& D, const PagedArgs& a, cudaStream
 template <int KT, int ROWS>
 cudaError_t launch_paged_join(const PagedDims& D, const PagedArgs& a, int ctas, int TI, int min_units, cudaStream_t st);
 
+// Whether rows of a bf16 tensor can be written in 32-byte pieces.
+inline bool wide_rows(const TensorRef& t) {
+  return reinterpret_cast<uintptr_t>(t.p) % 32 == 0 && t.sb % 16 == 0 && t.sh % 16 == 0 && t.sn % 16 == 0;
+}
+
 // TMA maps over bf16 tensors of any length with broadcast batch or head dimensions.
 bool tma_map_4d(CUtensorMap* map, const void* p, int d, int64_t n1, int64_t n2, int64_t n3, int64_t s1, int64_t s2,
                 int64_t s3, int b1, int b2);
