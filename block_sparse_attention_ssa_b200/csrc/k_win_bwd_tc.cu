@@ -662,7 +662,7 @@ cudaError_t launch(const WinDims& D, const WinBwdArgs& a, int32_t* status, cudaS
   cudaError_t e = launch_win_bwd_pre(D, a, st);
   if (e != cudaSuccess) return e;
   const WinBwdLayout L = win_bwd_layout(D);
-  const ChunkPlan cp = chunk_plan<TILE>(D, kBwdChunks);
+  const ChunkPlan cp = chunk_plan<TILE>(D, kBwdChunks, kTcMinSteps);
   char* ws = static_cast<char*>(a.ws);
   p.dq = a.dq;
   p.dk = a.dk;

@@ -17,13 +17,16 @@ namespace ssa {
 namespace {
 
 constexpr int BT = 64;
-constexpr int NT_ = 256;
+constexpr int GROUP = 256;          // threads on one 64 x 64 tile
+constexpr int THREADS = 2 * GROUP;  // two groups in a CTA
 constexpr int SP = BT + 4;  // row pitch of the P tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// CTAs of one paged call, a multiple of the SMs; units are worth a CTA from two on.
-constexpr int kPagedCtas = 296;
+// CTAs of one paged call, one per SM; units are worth a CTA from two on.
+constexpr int kPagedCtas = 148;
 constexpr int kMinUnits = 2;
+// Steps of a backward chunk at least: a 64 x 64 step takes some 9 us of a CTA, a partial's round trip less.
+constexpr int kMinSteps = 2;
 
 template <int HD>
 struct Pitch {
@@ -44,15 +47,15 @@ struct SimtParams {
 
 // A 64-row tile on its way through registers, so that its loads are in flight while the tile before is used; a
 // null row pointer gives zeros.
-template <int HD, int THREADS>
-struct TileRegs {
-  static constexpr int PER = HD / 4, N = BT * PER / THREADS;
+template <int HD, int TH>
+struct TileRegs {  // by the TH threads of a group or of the CTA
+  static constexpr int PER = HD / 4, N = BT * PER / TH;
   float4 v[N];
   template <typename F>
   __device__ __forceinline__ void fetch(F row) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int e = threadIdx.x + i * THREADS;
+      const int e = threadIdx.x % TH + i * TH;
       const float* p = row(e / PER);
       v[i] = p != nullptr ? *reinterpret_cast<const float4*>(p + (e % PER) * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
@@ -60,7 +63,7 @@ struct TileRegs {
   __device__ __forceinline__ void put(float* dst) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int e = threadIdx.x + i * THREADS;
+      const int e = threadIdx.x % TH + i * TH;
       *reinterpret_cast<float4*>(dst + (e / PER) * Pitch<HD>::v + (e % PER) * 4) = v[i];
     }
   }
@@ -131,32 +134,40 @@ __device__ __forceinline__ void store_row(float* dst, const float* acc, int tx, 
         make_float4(acc[4 * q] * mul, acc[4 * q + 1] * mul, acc[4 * q + 2] * mul, acc[4 * q + 3] * mul);
 }
 
+// Q, then each group's tile (K, then V) and weights.
 template <int HD>
 constexpr size_t fwd_smem() {
-  return (size_t)(2 * BT * Pitch<HD>::v + BT * SP) * 4;
+  return (size_t)(3 * BT * Pitch<HD>::v + 2 * BT * SP) * 4;
+}
+
+__device__ __forceinline__ void group_sync(int grp) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(GROUP) : "memory");
 }
 
 // ================================================================ forward
+// The two groups of a CTA take its key tiles in turn, each with its own online softmax, and join them at the end:
+// few rows fill the GPU's warps too (one group took 37 us at N = 1021, 8 heads and sequences, window 200).
 template <int HD, bool PAGED>
-__global__ void __launch_bounds__(NT_, 2) win_fwd_simt_kernel(SimtParams p) {
+__global__ void __launch_bounds__(THREADS, 1) win_fwd_simt_kernel(SimtParams p) {
   extern __shared__ float sm[];
   float* sQ = sm;
-  float* sX = sQ + BT * Pitch<HD>::v;  // K, then V
-  float* sP = sX + BT * Pitch<HD>::v;
+  const int grp = threadIdx.x / GROUP, tid = threadIdx.x % GROUP, tx = tid & 15, ty = tid >> 4;
+  float* sX = sQ + (1 + grp) * BT * Pitch<HD>::v;  // K, then V
+  float* sP = sQ + 3 * BT * Pitch<HD>::v + grp * BT * SP;
   __shared__ Place sh_place;
   __shared__ int sh_left;
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  __shared__ float sh_m[BT], sh_l[BT];
 
   Place at{0, 0, 0, 0};
   int left = 1;
   if (PAGED) {
-    if (tid < 32) {
+    if (threadIdx.x < 32) {
       const long long U = p.batch.total<BT>();
       const long long per = share(U, (int)gridDim.x, kMinUnits);
       const long long u0 = per * blockIdx.x;
       const long long n = u0 < U ? min(per, U - u0) : 0;
       if (n > 0) at = p.batch.locate<BT>(u0);
-      if (tid == 0) {
+      if (threadIdx.x == 0) {
         sh_place = at;
         sh_left = (int)n;
       }
@@ -202,11 +213,13 @@ __global__ void __launch_bounds__(NT_, 2) win_fwd_simt_kernel(SimtParams p) {
     }
     auto tok_of = [&](int r) { return PAGED ? r / per_tok : r; };
     auto head_of = [&](int r) { return PAGED ? head0 + r % per_tok : head0; };
-    TileRegs<HD, NT_> regs;
-    regs.fetch([&](int r) -> const float* {
-      return r < nrows ? row_ptr<float>(p.q, PAGED ? 0 : b, head_of(r), q0row + tok_of(r)) : nullptr;
-    });
-    regs.put(sQ);
+    TileRegs<HD, GROUP> regs;
+    if (grp == 0) {
+      regs.fetch([&](int r) -> const float* {
+        return r < nrows ? row_ptr<float>(p.q, PAGED ? 0 : b, head_of(r), q0row + tok_of(r)) : nullptr;
+      });
+      regs.put(sQ);
+    }
 
     float acc[4][HD / 16], m[4], l[4];
     int pos[4];
@@ -232,12 +245,13 @@ __global__ void __launch_bounds__(NT_, 2) win_fwd_simt_kernel(SimtParams p) {
       };
     };
     const int end = min(at.off + take, kt.count);
-    if (at.off < end) regs.fetch(keys(p.k, at.off));
-    for (int j = at.off; j < end; ++j) {
+    if (at.off + grp < end) regs.fetch(keys(p.k, at.off + grp));
+    __syncthreads();  // Q is there
+    for (int j = at.off + grp; j < end; j += 2) {
       const int u0 = kt.tile(j) * BT;
-      __syncthreads();
+      group_sync(grp);
       regs.put(sX);
-      __syncthreads();
+      group_sync(grp);
       regs.fetch(keys(p.v, j));
       float x[4][4];
       dots<HD>(sQ, sX, tx, ty, x);
@@ -279,18 +293,50 @@ __global__ void __launch_bounds__(NT_, 2) win_fwd_simt_kernel(SimtParams p) {
 #pragma unroll
         for (int c = 0; c < HD / 16; ++c) acc[i][c] *= f;
       }
-      __syncthreads();
+      group_sync(grp);
       regs.put(sX);
-      __syncthreads();
-      if (j + 1 < end) regs.fetch(keys(p.k, j + 1));
+      group_sync(grp);
+      if (j + 2 < end) regs.fetch(keys(p.k, j + 2));
       weighted<HD>(sP, sX, tx, ty, acc);
     }
 
+    // ---- join of the groups' softmaxes
+    if (grp == 1) {
+      group_sync(1);  // sX is read to the end
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        store_row<HD>(sX + (4 * ty + i) * Pitch<HD>::v, acc[i], tx, 1.0f);
+        if (tx == 0) {
+          sh_m[4 * ty + i] = m[i];
+          sh_l[4 * ty + i] = l[i];
+        }
+      }
+    }
+    __syncthreads();
+    if (grp == 0) {
+      const float* other = sX + BT * Pitch<HD>::v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i;
+        const float m1 = sh_m[r], mn = fmaxf(m[i], m1), ref = mn == kNegInf ? 0.f : mn;
+        const float f0 = exp2f(m[i] - ref), f1 = exp2f(m1 - ref);
+        l[i] = l[i] * f0 + sh_l[r] * f1;
+        m[i] = mn;
+#pragma unroll
+        for (int q = 0; q < HD / 64; ++q) {
+          const float4 o = *reinterpret_cast<const float4*>(other + r * Pitch<HD>::v + 64 * q + 4 * tx);
+          acc[i][4 * q] = acc[i][4 * q] * f0 + o.x * f1;
+          acc[i][4 * q + 1] = acc[i][4 * q + 1] * f0 + o.y * f1;
+          acc[i][4 * q + 2] = acc[i][4 * q + 2] * f0 + o.z * f1;
+          acc[i][4 * q + 3] = acc[i][4 * q + 3] * f0 + o.w * f1;
+        }
+      }
+    }
     // ---- epilogue
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 4 * ty + i;
-      if (r >= nrows) continue;
+      if (r >= nrows || grp == 1) continue;
       if (PAGED && part_rows) {
         float* base = p.part + (size_t)(2 * blockIdx.x + (seg ? 1 : 0)) * partial_floats(BT, HD);
 #pragma unroll
@@ -382,11 +428,9 @@ struct SimtBwd {
   float c, scale;
 };
 
-// 512 threads in two groups of 256: the first forms the weights, the second dP, side by side (twice the warps
+// The first group forms the weights, the second dP, side by side (twice the warps
 // for the same tiles; one group of 256 took 165 us for dkv and 77 us for dq at N = 1000, 8 heads, d = 128).
 // The next step's tiles are fetched into registers while this one is computed.
-constexpr int BWD_THREADS = 512;
-
 template <int HD>
 constexpr size_t bwd_smem() {
   return (size_t)(4 * BT * Pitch<HD>::v + 2 * BT * SP) * 4;
@@ -400,7 +444,7 @@ __device__ __forceinline__ void put4x4(float* P, const float (&x)[4][4], int tx,
 }
 
 template <int HD>
-__global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dq_simt_kernel(SimtBwd p) {
+__global__ void __launch_bounds__(THREADS, 1) win_bwd_dq_simt_kernel(SimtBwd p) {
   extern __shared__ float sm[];
   float* sQ = sm;
   float* sG = sQ + BT * Pitch<HD>::v;
@@ -414,7 +458,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dq_simt_kernel(SimtBwd
   const int b = plane / p.Hq, h = plane % p.Hq, kvh = h / p.grp;
   const int q0 = qt * BT, nrows = min(BT, p.N - q0);
   const KeyTiles kt = key_tiles<BT>(q0, q0 + nrows - 1, p.window, p.sinks);
-  TileRegs<HD, BWD_THREADS> ra, rb;
+  TileRegs<HD, THREADS> ra, rb;
   auto query = [&](const TensorRef& t) {
     return [&, t](int r) -> const float* { return r < nrows ? row_ptr<float>(t, b, h, q0 + r) : nullptr; };
   };
@@ -509,7 +553,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dq_simt_kernel(SimtBwd
 }
 
 template <int HD>
-__global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dkv_simt_kernel(SimtBwd p) {
+__global__ void __launch_bounds__(THREADS, 1) win_bwd_dkv_simt_kernel(SimtBwd p) {
   extern __shared__ float sm[];
   float* sK = sm;
   float* sV = sK + BT * Pitch<HD>::v;
@@ -523,7 +567,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dkv_simt_kernel(SimtBw
   const int b = plane / p.Hkv, kvh = plane % p.Hkv;
   const int u0 = ch.kt * BT, nq = query_tiles_of<BT>(ch.kt, p.N, p.window, p.sinks);
   const int first = ch.idx * p.L, last = min(first + p.L, nq * p.grp);
-  TileRegs<HD, BWD_THREADS> ra, rb;
+  TileRegs<HD, THREADS> ra, rb;
   float nx[4];  // -lse2 (first group) or -D (second) of the next step
   auto key = [&](const TensorRef& t) {
     return [&, t](int r) -> const float* { return u0 + r < p.N ? row_ptr<float>(t, b, kvh, u0 + r) : nullptr; };
@@ -672,7 +716,7 @@ cudaError_t fwd_t(const WinDims& D, const WinFwdArgs& a, cudaStream_t st) {
   auto kern = win_fwd_simt_kernel<HD, false>;
   cudaError_t e = set_smem(kern, fwd_smem<HD>());
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)((int64_t)p.NT * D.B * D.Hq), NT_, fwd_smem<HD>(), st>>>(p);
+  kern<<<(unsigned)((int64_t)p.NT * D.B * D.Hq), THREADS, fwd_smem<HD>(), st>>>(p);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -682,7 +726,7 @@ cudaError_t bwd_t(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
   cudaError_t e = launch_win_bwd_pre(D, a, st);
   if (e != cudaSuccess) return e;
   const WinBwdLayout L = win_bwd_layout(D);
-  const ChunkPlan cp = chunk_plan<BT>(D, kBwdChunks);
+  const ChunkPlan cp = chunk_plan<BT>(D, kBwdChunks, kMinSteps);
   char* ws = static_cast<char*>(a.ws);
   SimtBwd p{};
   p.q = a.q;
@@ -709,13 +753,13 @@ cudaError_t bwd_t(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
   p.scale = D.scale;
   auto dkv = win_bwd_dkv_simt_kernel<HD>;
   if ((e = set_smem(dkv, bwd_smem<HD>())) != cudaSuccess) return e;
-  dkv<<<dim3(cp.chunks * D.Hkv, D.B), BWD_THREADS, bwd_smem<HD>(), st>>>(p);
+  dkv<<<dim3(cp.chunks * D.Hkv, D.B), THREADS, bwd_smem<HD>(), st>>>(p);
   count_launches(1);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if ((e = launch_win_kvjoin<BT>(D, a, cp, p.part, st)) != cudaSuccess) return e;
   auto dq = win_bwd_dq_simt_kernel<HD>;
   if ((e = set_smem(dq, bwd_smem<HD>())) != cudaSuccess) return e;
-  dq<<<(unsigned)((int64_t)cp.NT * D.B * D.Hq), BWD_THREADS, bwd_smem<HD>(), st>>>(p);
+  dq<<<(unsigned)((int64_t)cp.NT * D.B * D.Hq), THREADS, bwd_smem<HD>(), st>>>(p);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -763,7 +807,7 @@ cudaError_t paged_t(const PagedDims& D, const PagedArgs& a, cudaStream_t st) {
   auto kern = win_fwd_simt_kernel<HD, true>;
   cudaError_t e = set_smem(kern, fwd_smem<HD>());
   if (e != cudaSuccess) return e;
-  kern<<<kPagedCtas, NT_, fwd_smem<HD>(), st>>>(p);
+  kern<<<kPagedCtas, THREADS, fwd_smem<HD>(), st>>>(p);
   count_launches(1);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_paged_join<BT, BT>(D, a, kPagedCtas, TI, kMinUnits, st);
@@ -807,7 +851,7 @@ WinBwdLayout win_bwd_layout(const WinDims& D) {
   o = up(o + rows * 4);
   L.part = o;
   const int tile = D.dtype == SSA_BF16 ? 128 : BT;
-  const ChunkPlan p = D.dtype == SSA_BF16 ? chunk_plan<128>(D, kBwdChunks) : chunk_plan<BT>(D, kBwdChunks);
+  const ChunkPlan p = D.dtype == SSA_BF16 ? chunk_plan<128>(D, kBwdChunks, kTcMinSteps) : chunk_plan<BT>(D, kBwdChunks, kMinSteps);
   o = up(o + (size_t)D.B * D.Hkv * p.partials * 2 * tile * D.d * 4);
   L.bytes = o;
   return L;

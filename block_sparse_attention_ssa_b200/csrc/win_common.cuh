@@ -190,19 +190,21 @@ __host__ __device__ __forceinline__ int query_tiles_of(int kt, int N, int window
 }
 
 constexpr int kBwdChunks = 296;  // chunks to aim for, two per SM
+constexpr int kTcMinSteps = 8;   // steps of a chunk at least on the tensor cores (1.5 us each)
 
 struct ChunkPlan {
   int L, NT, chunks, partials;  // per (batch, kv head)
 };
 
 template <int BT>
-inline ChunkPlan chunk_plan(const WinDims& D, int ctas) {
+inline ChunkPlan chunk_plan(const WinDims& D, int ctas, int min_steps) {
   ChunkPlan p{};
   p.NT = (D.N + BT - 1) / BT;
   long long steps = 0;
   for (int kt = 0; kt < p.NT; ++kt) steps += (long long)query_tiles_of<BT>(kt, D.N, D.window, D.sinks) * D.g;
   const long long all = steps * D.B * D.Hkv;
-  p.L = (int)((all + ctas - 1) / ctas < 8 ? 8 : (all + ctas - 1) / ctas);
+  const long long even = (all + ctas - 1) / ctas;
+  p.L = (int)(even < min_steps ? min_steps : even);
   for (int kt = 0; kt < p.NT; ++kt) {
     const int n = (int)(((long long)query_tiles_of<BT>(kt, D.N, D.window, D.sinks) * D.g + p.L - 1) / p.L);
     p.chunks += n;
