@@ -13,8 +13,12 @@
 
 #include <type_traits>
 
+#include "sm100_ptx.cuh"
+
 namespace ssa {
 namespace {
+
+using sm100::fma2;
 
 constexpr int BT = 64;
 constexpr int GROUP = 256;          // threads on one 64 x 64 tile
@@ -69,14 +73,15 @@ struct TileRegs {  // by the TH threads of a group or of the CTA
   }
 };
 
-// s[i][j] = A[4 ty + i] . B[tx + 16 j]
+// s[i][j] = A[4 ty + i] . B[tx + 16 j], even and odd head dims in the two halves of a packed multiply-add.
 template <int HD>
 __device__ __forceinline__ void dots(const float* A, const float* B, int tx, int ty, float (&s)[4][4]) {
   constexpr int P = Pitch<HD>::v;
+  float2 t[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) t[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
   for (int k = 0; k < HD; k += 4) {
     float4 a[4], b[4];
@@ -88,12 +93,14 @@ __device__ __forceinline__ void dots(const float* A, const float* B, int tx, int
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
-        s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
-        s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
-        s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+        t[i][j] = fma2(make_float2(a[i].x, a[i].y), make_float2(b[j].x, b[j].y), t[i][j]);
+        t[i][j] = fma2(make_float2(a[i].z, a[i].w), make_float2(b[j].z, b[j].w), t[i][j]);
       }
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = t[i][j].x + t[i][j].y;
 }
 
 // acc[i][.] += sum_u W[4 ty + i][u] X[u][.]; columns 4 tx + 64 q + 0..3.
@@ -117,10 +124,13 @@ __device__ __forceinline__ void weighted(const float* W, const float* X, int tx,
         const float4 x = *reinterpret_cast<const float4*>(X + (u + e) * Pitch<HD>::v + 64 * q + 4 * tx);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          acc[i][4 * q] = fmaf(w[i][e], x.x, acc[i][4 * q]);
-          acc[i][4 * q + 1] = fmaf(w[i][e], x.y, acc[i][4 * q + 1]);
-          acc[i][4 * q + 2] = fmaf(w[i][e], x.z, acc[i][4 * q + 2]);
-          acc[i][4 * q + 3] = fmaf(w[i][e], x.w, acc[i][4 * q + 3]);
+          const float2 ww = make_float2(w[i][e], w[i][e]);
+          const float2 lo = fma2(ww, make_float2(x.x, x.y), make_float2(acc[i][4 * q], acc[i][4 * q + 1]));
+          const float2 hi = fma2(ww, make_float2(x.z, x.w), make_float2(acc[i][4 * q + 2], acc[i][4 * q + 3]));
+          acc[i][4 * q] = lo.x;
+          acc[i][4 * q + 1] = lo.y;
+          acc[i][4 * q + 2] = hi.x;
+          acc[i][4 * q + 3] = hi.y;
         }
       }
   }
@@ -536,8 +546,9 @@ __global__ void __launch_bounds__(THREADS, 1) win_bwd_dq_simt_kernel(SimtBwd p) 
           const float2 k2 = *reinterpret_cast<const float2*>(kr + c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            acc[i][c] = fmaf(w[i][e], k2.x, acc[i][c]);
-            acc[i][c + 1] = fmaf(w[i][e], k2.y, acc[i][c + 1]);
+            const float2 a2 = fma2(make_float2(w[i][e], w[i][e]), k2, make_float2(acc[i][c], acc[i][c + 1]));
+            acc[i][c] = a2.x;
+            acc[i][c + 1] = a2.y;
           }
         }
       }
