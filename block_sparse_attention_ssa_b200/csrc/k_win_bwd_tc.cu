@@ -278,8 +278,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       tc_fence_after();
       const bool all = t0 >= ub && (t0 + COLS - 1 - ua < p.window || ub < p.sinks);
-      // queries c with lo <= c < hi see the key (c >= lo alone where it is a sink)
-      const int lo = u - t0, hi = u < p.sinks ? COLS : u + p.window - t0;
+      const uint32_t vis = visible_queries(u, t0, p.window, p.sinks);
       float x[COLS];
       tmem_ld32(aS, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
       tmem_wait_ld();
@@ -296,8 +295,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       if (!all) {
 #pragma unroll
-        for (int c = 0; c < COLS; ++c)
-          if (c < lo || c >= hi) x[c] = 0.f;
+        for (int c = 0; c < COLS; ++c) x[c] = keep(vis, c, x[c], 0.f);
       }
 #pragma unroll
       for (int c = 0; c < COLS; c += 2) pk[c / 2] = pack_bf16(x[c], x[c + 1]);
@@ -329,8 +327,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       if (!all) {  // zero times a NaN or an infinity of a hidden pair
 #pragma unroll
-        for (int c = 0; c < COLS; ++c)
-          if (c < lo || c >= hi) x[c] = 0.f;
+        for (int c = 0; c < COLS; ++c) x[c] = keep(vis, c, x[c], 0.f);
       }
 #pragma unroll
       for (int c = 0; c < COLS; c += 2) pk[c / 2] = pack_bf16(x[c], x[c + 1]);
@@ -567,7 +564,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const uint32_t aS = cS + lane_base + TILE * (k & 1) + COLS * cg;
         const int u0 = I.kt.tile((int)(k - n)) * TILE + COLS * cg;  // this warp's first key
         const bool all = u0 + COLS - 1 <= ta && (tb - u0 < p.window || u0 + COLS <= p.sinks);
-        const int hi = t - u0, lo = t - p.window - u0, sk = p.sinks - u0;  // sees lo < c <= hi, or c < sk
         float x[COLS];
         tmem_ld32(aS, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
         tmem_wait_ld();
@@ -592,9 +588,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           x[c + 1] = z.y;
         }
         if (!all) {
+          const uint32_t vis = visible_keys(t, u0, p.window, p.sinks);
 #pragma unroll
-          for (int c = 0; c < COLS; ++c)
-            if (c > hi || (c <= lo && c >= sk)) x[c] = 0.f;
+          for (int c = 0; c < COLS; ++c) x[c] = keep(vis, c, x[c], 0.f);
         }
 #pragma unroll
         for (int c = 0; c < COLS; c += 2) pk[c / 2] = pack_bf16(x[c], x[c + 1]);

@@ -495,12 +495,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     };
     auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u, abort)) != 0; };
     uint32_t tc = 0, mc = 0, outs = 0, joins = 0;  // tiles; the warp's tiles and items with rows; joined items
-    // Paged form: the next item's coordinates (loads and divisions) are formed before the epilogue, while the
-    // last product runs: 77 against 85 us for one token over 65536 keys.  In the window form the same step
-    // lets the slots fall into step with each other: 0.91 against 0.71 ms at N = 32768, window 1024.
-    constexpr bool kAhead = PAGED;
-    bool ok = true, more = kAhead && walk.next(I);
-    while (kAhead ? more : ok && walk.next(I)) {
+    bool ok = true, more = walk.next(I);
+    while (more) {
       const int g = I.g;
       const int shift = s && I.two ? I.toks0 : 0;  // the slot's first token within the item
       const int nrows = (s && I.two ? I.toks - I.toks0 : I.toks0) * g;
@@ -527,12 +523,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tmem_ld32(s_addr + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
             tmem_wait_ld();
             if (!all) {
-              const int v0 = u0 + 32 * q;
-              const int hi = pos - v0, lo = pos - p.window - v0, sk = p.sinks - v0;  // sees lo < c <= hi, or c < sk
-              const uint32_t gone = bad >> (2 * q);
+              uint32_t vis = visible_keys(pos, u0 + 32 * q, p.window, p.sinks);
+              if (PAGED) {
+                const uint32_t gone = bad >> (2 * q);
+                vis &= ~((gone & 1u ? 0xffffu : 0u) | (gone & 2u ? 0xffff0000u : 0u));
+              }
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (c > hi || (c <= lo && c >= sk) || ((gone >> (c >> 4)) & 1u)) x[c] = kNegInf;
+              for (int c = 0; c < 32; ++c) x[c] = keep(vis, c, x[c], kNegInf);
             }
           };
           float a0 = kNegInf, a1 = kNegInf, a2 = kNegInf, a3 = kNegInf;
@@ -642,9 +639,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         ++outs;
       }
-      // ---- epilogue of the item: each half's warps take half of O's columns
+      // ---- epilogue of the item: each half's warps take half of O's columns.  The next item's coordinates
+      // (loads and divisions) are formed while the last product runs.
       Item J;
-      if (kAhead) more = walk.next(J);
+      more = walk.next(J);
       if (any) {
         if (!(ok = wait(&M.pv_done[s][1], tc - 1))) break;
         tc_fence_after();
@@ -737,7 +735,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&M.o_free[s]);
       }
-      if (kAhead) I = J;
+      I = J;
     }
   }
 

@@ -64,6 +64,26 @@ __host__ __device__ __forceinline__ KeyTiles key_tiles(int pmin, int pmax, int w
   return k;
 }
 
+// Bits c < n of a word.  A row's visible columns are formed as one word and applied by selects: compared one by
+// one they became a branch a column, and a partly visible tile took six times a whole one.
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
+
+// Keys u0 .. u0 + 31 that the query at position t sees.
+__device__ __forceinline__ uint32_t visible_keys(int t, int u0, int window, int sinks) {
+  return bits_below(t - u0 + 1) & (~bits_below(t - window - u0 + 1) | bits_below(sinks - u0));
+}
+// Queries t0 .. t0 + 31 that see key u.
+__device__ __forceinline__ uint32_t visible_queries(int u, int t0, int window, int sinks) {
+  return ~bits_below(u - t0) & (u < sinks ? ~0u : bits_below(u + window - t0));
+}
+__device__ __forceinline__ float keep(uint32_t vis, int c, float x, float other) {
+  float r;
+  asm("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\tselp.f32 %0, %2, %3, p;\n\t}"
+      : "=f"(r)
+      : "r"(vis & (1u << c)), "f"(x), "f"(other));
+  return r;
+}
+
 // ---------------------------------------------------------------- shares of a ragged batch
 // Work items of one paged call: (sequence b, run of TI new tokens, kv head).
 // An item is as many units as its queries see key tiles (one, to write its empty
