@@ -70,6 +70,7 @@ __global__ void __launch_bounds__(256) paged_append_kernel(PagedArgs a, PagedDim
 //   m = max m_i, h = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i, a warp per row.
 template <typename T, int HD, int KT, int ROWS>
 __global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, Batch batch, int T_, int g, int ctas, int min_units) {
+  // Launched while the attention kernel still runs: only the partials wait for its end.
   __shared__ Place sh;
   __shared__ long long sh_unit[3];
   if (threadIdx.x < 32) {
@@ -86,6 +87,8 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, Batch batc
     }
   }
   __syncthreads();
+  // Every CTA waits, those without work too: what follows in the stream waits for this kernel alone.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Place at = sh;
   if (at.b >= batch.seqs) return;
   const long long u0 = sh_unit[0], u1 = sh_unit[1], per = sh_unit[2];
@@ -110,13 +113,17 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, Batch batc
     float l = 0.f, o[V];
 #pragma unroll
     for (int c = 0; c < V; ++c) o[c] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = 0; i < parts; ++i) {
       const float* q = slot(i);
       const float f = exp2f(q[ROWS * HD + r] - ref);
       l = fmaf(f, q[ROWS * HD + ROWS + r], l);
 #pragma unroll
-      for (int c = 0; c < V; ++c) o[c] = fmaf(f, q[r * HD + lane * V + c], o[c]);
+      for (int c = 0; c < V; c += 2) {
+        const float2 x = *reinterpret_cast<const float2*>(q + r * HD + lane * V + c);
+        o[c] = fmaf(f, x.x, o[c]);
+        o[c + 1] = fmaf(f, x.y, o[c + 1]);
+      }
     }
     const float inv = l == 0.f ? 0.f : 1.0f / l;
     const int h = at.kvh * g + r % g, row = s.q0 + i0 + r / g;
@@ -139,14 +146,23 @@ cudaError_t launch_paged_append(const PagedDims& D, const PagedArgs& a, cudaStre
 template <int KT, int ROWS>
 cudaError_t launch_paged_join(const PagedDims& D, const PagedArgs& a, int ctas, int TI, int min_units, cudaStream_t st) {
   const Batch batch{a.q_start, a.kv_len, D.seqs, D.T, D.max_pages * D.page, TI, D.window, D.sinks, D.Hkv};
-  const dim3 grid(ctas, 4);
+  // Programmatic launch: the kernel's start (its launch and the search of its item) overlaps the attention
+  // kernel's last CTAs; it waits for that kernel before it reads a partial.
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, 4);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   using T = std::conditional_t<KT == 128, __nv_bfloat16, float>;  // units of 128 keys are the bf16 kernel's
-  if (D.d == 64)
-    paged_join_kernel<T, 64, KT, ROWS><<<grid, 256, 0, st>>>(a, batch, D.T, D.g, ctas, min_units);
-  else
-    paged_join_kernel<T, 128, KT, ROWS><<<grid, 256, 0, st>>>(a, batch, D.T, D.g, ctas, min_units);
+  const cudaError_t e = D.d == 64
+      ? cudaLaunchKernelEx(&cfg, paged_join_kernel<T, 64, KT, ROWS>, a, batch, D.T, D.g, ctas, min_units)
+      : cudaLaunchKernelEx(&cfg, paged_join_kernel<T, 128, KT, ROWS>, a, batch, D.T, D.g, ctas, min_units);
   count_launches(1);
-  return cudaGetLastError();
+  return e;
 }
 template cudaError_t launch_paged_join<128, 256>(const PagedDims&, const PagedArgs&, int, int, int, cudaStream_t);
 template cudaError_t launch_paged_join<64, 64>(const PagedDims&, const PagedArgs&, int, int, int, cudaStream_t);

@@ -58,7 +58,7 @@ struct BwdParams {
   const float* dsum;
   float* part;
   int32_t* status;
-  int B, Hq, Hkv, g, N, Npad, NT, window, sinks, L, partials;
+  int B, Hq, Hkv, g, N, Npad, NT, window, sinks, L, partials, cut;
   int zq, zk, zv, zg;  // broadcast dimensions: bit 0 batch, bit 1 head
   float c, scale;      // c = scale * log2(e)
   bool wide_q, wide_kv;  // gradients in 32-byte pieces
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tmem_alloc(&M.tmem_base, 512);
     tmem_relinquish();
   }
-  const Chunk ch = find_chunk<TILE>((int)blockIdx.x / p.Hkv, p.NT, p.L, p.g, p.N, p.window, p.sinks);
+  const Chunk ch = find_chunk<TILE>((int)blockIdx.x / p.Hkv, p.cut, p.L, p.g, p.N, p.window, p.sinks);
   const int u0 = ch.kt * TILE, nq = query_tiles_of<TILE>(ch.kt, p.N, p.window, p.sinks);
   const int first = ch.idx * p.L, T = 2 * min(p.L, nq * p.g - first);  // units: step (head, query tile), half
   tc_fence_before();
@@ -678,6 +678,7 @@ cudaError_t launch(const WinDims& D, const WinBwdArgs& a, int32_t* status, cudaS
   p.sinks = D.sinks;
   p.L = cp.L;
   p.partials = cp.partials;
+  p.cut = cp.cut;
   p.c = D.scale * kLog2e;
   p.scale = D.scale;
   p.wide_q = wide_rows(a.dq);

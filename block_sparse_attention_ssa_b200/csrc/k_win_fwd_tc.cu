@@ -9,8 +9,9 @@
 //
 // A persistent CTA per SM walks work items of up to 256 query rows in two slots of 128
 // (TMEM lanes).  Key tiles of 128 keys are shared by both slots; a step is half a tile, 64
-// keys.  Warps 4 (2 s + h) .. + 3 hold the softmax of half h of slot s's tiles, warp 16 loads
-// by TMA, one thread of warps 17 and 18 issues the products of slot 0 and slot 1 (one issuer
+// keys.  Warps 4 (2 s + h) .. + 3 hold the softmax of half h of slot s's tiles, warps 16 and 19
+// load Q with K and V by TMA (a tile of 16-token pages is 32 copies, more than one warp issues
+// in a tile's time at full memory rate), one thread of warps 17 and 18 issues the products of slot 0 and slot 1 (one issuer
 // for both spent more cycles on its control flow than the products take).  TMEM: O of slot s
 // at HD s, its two S buffers of 64 columns at 256 + 128 s; P (bf16 pairs) overwrites the second
 // half of its S buffer and feeds P V from TMEM.  The next tile's logits are issued behind P V
@@ -41,7 +42,7 @@ using bf16 = __nv_bfloat16;
 constexpr int TILE = 128;
 constexpr int UNIT = 64;  // keys of a step
 constexpr int NTHREADS = 640;
-constexpr int WARP_TMA = 16, WARP_MMA = 17;  // and WARP_MMA + 1 for slot 1; the last warp only fills its group
+constexpr int WARP_TMA = 16, WARP_MMA = 17, WARP_TMA_V = 19;  // and WARP_MMA + 1 for slot 1
 
 constexpr int kCtas = 148;     // one per SM
 constexpr int kMinUnits = 4;   // key tiles worth a CTA of their own
@@ -273,6 +274,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (PAGED) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be brought up
   const uint32_t tmem = M.tmem_base;
   uint8_t* sQ = smem;
   uint8_t* sK = smem + C::OFF_K;
@@ -281,99 +283,96 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   Item I;
   uint32_t base = 0;  // key tiles before this item
 
-  if (warp == WARP_TMA) {
-    // ================================================================ producer
+  if (warp == WARP_TMA || warp == WARP_TMA_V) {
+    // ================================================================ producers: Q and K, and V
+    const bool is_k = warp == WARP_TMA;
+    const CUtensorMap* map = is_k ? &tmK : &tmV;
+    const int zero = is_k ? p.zk : p.zv, stages = is_k ? C::NSK : C::NSV;
+    uint64_t* full = is_k ? M.k_full : M.v_full;
+    uint64_t* empty = is_k ? M.k_empty : M.v_empty;
+    uint8_t* ring = is_k ? sK : sV;
     if (lane == 0) {
-      prefetch_tensormap(&tmQ);
-      prefetch_tensormap(&tmK);
-      prefetch_tensormap(&tmV);
+      prefetch_tensormap(map);
+      if (is_k) prefetch_tensormap(&tmQ);
     }
-    uint32_t q_issued = 0, k_issued = 0, v_issued = 0;
+    uint32_t q_issued = 0, issued = 0;
     bool ok = true;
     while (ok && walk.next(I)) {
       if (I.T == 0) continue;
-      if (q_issued > 0 && !__all_sync(0xffffffffu, mbar_wait(&M.q_empty, (q_issued - 1) & 1u, abort))) break;
-      if (lane == 0) {
-        const int slots = I.two ? 2 : 1;
-        const uint32_t bytes = PAGED ? (uint32_t)(p.TQ * p.g * HD * 2) : (uint32_t)C::TB;
-        mbar_expect_tx(&M.q_full, bytes * slots);
-        for (int s = 0; s < slots; ++s)
-          for (int f = 0; f < HD / 64; ++f) {
-            uint8_t* dst = sQ + s * C::TB + f * C::HALF;
-            if (PAGED)
-              tma_load_4d(dst, &tmQ, &M.q_full, 64 * f, I.head0, I.row0 + s * p.TQ, 0);
-            else
-              tma_load_4d(dst, &tmQ, &M.q_full, 64 * f, I.row0 + s * TILE, p.zq & 2 ? 0 : I.head0, p.zq & 1 ? 0 : I.b);
-          }
-      }
-      ++q_issued;
-      const int pmax = I.p0 + I.toks - 1, lo_min = I.p0 - p.window + 1;
-      // One key tile: its pages, a copy per lane (a page, or its half of the columns).
-      auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int t, int zero, uint32_t* bad) {
-        if (!PAGED) {
-          if (lane == 0) {
-            mbar_expect_tx(bar, C::TB);
-            for (int f = 0; f < HD / 64; ++f)
-              tma_load_4d(dst + f * C::HALF, map, bar, 64 * f, t * TILE, zero & 2 ? 0 : I.kvh, zero & 1 ? 0 : I.b);
-          }
-          return;
-        }
-        const int rows = min(p.page, TILE), copies = TILE / rows * (HD / 64);
-        const int u = t * TILE + (lane / (HD / 64)) * rows;
-        int pg = p.num_pages;  // past the end: zeros, and nothing read
-        const bool seen = u <= pmax && (u + rows > lo_min || u < p.sinks);
-        if (lane < copies && seen) {
-          const int id = p.table[(int64_t)I.b * p.max_pages + u / p.page];
-          if ((unsigned)id < (unsigned)p.num_pages) pg = id;
-        }
-        if (bad != nullptr) {
-          const unsigned gone = __ballot_sync(0xffffffffu, lane < copies && seen && pg == p.num_pages);
-          if (lane == 0) {
-            uint32_t bits = 0;
-            for (unsigned m = gone; m; m &= m - 1) {
-              const int r = ((__ffs(m) - 1) / (HD / 64)) * rows;
-              bits |= ((1u << (rows / 16)) - 1u) << (r / 16);
+      if (is_k) {
+        if (q_issued > 0 && !__all_sync(0xffffffffu, mbar_wait(&M.q_empty, (q_issued - 1) & 1u, abort))) break;
+        if (lane == 0) {
+          const int slots = I.two ? 2 : 1;
+          const uint32_t bytes = PAGED ? (uint32_t)(p.TQ * p.g * HD * 2) : (uint32_t)C::TB;
+          mbar_expect_tx(&M.q_full, bytes * slots);
+          for (int s = 0; s < slots; ++s)
+            for (int f = 0; f < HD / 64; ++f) {
+              uint8_t* dst = sQ + s * C::TB + f * C::HALF;
+              if (PAGED)
+                tma_load_4d(dst, &tmQ, &M.q_full, 64 * f, I.head0, I.row0 + s * p.TQ, 0);
+              else
+                tma_load_4d(dst, &tmQ, &M.q_full, 64 * f, I.row0 + s * TILE, p.zq & 2 ? 0 : I.head0, p.zq & 1 ? 0 : I.b);
             }
-            *bad = bits;
-          }
         }
-        if (lane == 0) mbar_expect_tx(bar, C::TB);
-        __syncwarp();
-        if (lane < copies) {
-          const int f = lane % (HD / 64), r = (lane / (HD / 64)) * rows;
-          tma_load_4d(dst + f * C::HALF + r * 128, map, bar, 64 * f, u % p.page, zero & 2 ? 0 : I.kvh,
-                      (zero & 1) && pg < p.num_pages ? 0 : pg);
-        }
-        __syncwarp();
-      };
+        ++q_issued;
+      }
+      const int pmax = I.p0 + I.toks - 1, lo_min = I.p0 - p.window + 1;
       for (int j = 0; j < I.T; ++j) {
         const uint32_t n = base + j;
-        const int t = I.tile(j), sk = (int)(n % C::NSK), sv = (int)(n % C::NSV);
-        if (n >= C::NSK && !__all_sync(0xffffffffu, mbar_wait(&M.k_empty[sk], (n / C::NSK - 1) & 1u, abort))) {
+        const int t = I.tile(j), st = (int)(n % stages);
+        const uint32_t use = n / stages;
+        // Pages of the tile: a copy a lane (a page, or its half of the columns).  Ids are read before the wait.
+        const int rows = PAGED ? min(p.page, TILE) : TILE, copies = TILE / rows * (HD / 64);
+        const int u = t * TILE + (lane / (HD / 64)) * rows;
+        int pg = p.num_pages;  // past the end: zeros, and nothing read
+        bool seen = false;
+        if (PAGED && lane < copies) {
+          seen = u <= pmax && (u + rows > lo_min || u < p.sinks);
+          if (seen) {
+            const int id = p.table[(int64_t)I.b * p.max_pages + u / p.page];
+            if ((unsigned)id < (unsigned)p.num_pages) pg = id;
+          }
+        }
+        if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(&empty[st], (use - 1) & 1u, abort))) {
           ok = false;
           break;
         }
-        load(&tmK, sK + sk * C::TB, &M.k_full[sk], t, p.zk, &M.bad[n & 7]);
-        k_issued = n + 1;
-        if (n >= C::NSV && !__all_sync(0xffffffffu, mbar_wait(&M.v_empty[sv], (n / C::NSV - 1) & 1u, abort))) {
-          ok = false;
-          break;
+        uint8_t* dst = ring + st * C::TB;
+        if (PAGED) {
+          if (is_k) {
+            const unsigned gone = __ballot_sync(0xffffffffu, seen && pg == p.num_pages);
+            if (lane == 0) {
+              uint32_t bits = 0;
+              for (unsigned m = gone; m; m &= m - 1) {
+                const int r = ((__ffs(m) - 1) / (HD / 64)) * rows;
+                bits |= ((1u << (rows / 16)) - 1u) << (r / 16);
+              }
+              M.bad[n & 7] = bits;
+            }
+          }
+          if (lane == 0) mbar_expect_tx(&full[st], C::TB);
+          __syncwarp();
+          if (lane < copies) {
+            const int f = lane % (HD / 64), r = (lane / (HD / 64)) * rows;
+            tma_load_4d(dst + f * C::HALF + r * 128, map, &full[st], 64 * f, u % p.page, zero & 2 ? 0 : I.kvh,
+                        (zero & 1) && pg < p.num_pages ? 0 : pg);
+          }
+          __syncwarp();
+        } else if (lane == 0) {
+          mbar_expect_tx(&full[st], C::TB);
+          for (int f = 0; f < HD / 64; ++f)
+            tma_load_4d(dst + f * C::HALF, map, &full[st], 64 * f, t * TILE, zero & 2 ? 0 : I.kvh, zero & 1 ? 0 : I.b);
         }
-        load(&tmV, sV + sv * C::TB, &M.v_full[sv], t, p.zv, nullptr);
-        v_issued = n + 1;
+        issued = n + 1;
       }
       base += I.T;
     }
     // every copy must have landed before the CTA ends
     int dummy = 0;
     if (q_issued) mbar_wait(&M.q_full, (q_issued - 1) & 1u, &dummy);
-    for (uint32_t n = k_issued > C::NSK ? k_issued - C::NSK : 0; n < k_issued; ++n) {
+    for (uint32_t n = issued > (uint32_t)stages ? issued - stages : 0; n < issued; ++n) {
       dummy = 0;
-      mbar_wait(&M.k_full[n % C::NSK], (n / C::NSK) & 1u, &dummy);
-    }
-    for (uint32_t n = v_issued > C::NSV ? v_issued - C::NSV : 0; n < v_issued; ++n) {
-      dummy = 0;
-      mbar_wait(&M.v_full[n % C::NSV], (n / C::NSV) & 1u, &dummy);
+      mbar_wait(&full[n % stages], (n / stages) & 1u, &dummy);
     }
   } else if (warp == WARP_MMA || warp == WARP_MMA + 1) {
     // ================================================================ MMA issuer of slot s

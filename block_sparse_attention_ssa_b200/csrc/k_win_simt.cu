@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(THREADS, 1) win_fwd_simt_kernel(SimtParams p) 
       }
     }
     __syncthreads();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be brought up
     at = sh_place;
     left = sh_left;
   }
@@ -434,7 +435,7 @@ struct SimtBwd {
   const float* lse2;
   const float* dsum;
   float* part;
-  int Hq, Hkv, grp, N, Npad, window, sinks, NT, L, partials;
+  int Hq, Hkv, grp, N, Npad, window, sinks, NT, L, partials, cut;
   float c, scale;
 };
 
@@ -574,7 +575,7 @@ __global__ void __launch_bounds__(THREADS, 1) win_bwd_dkv_simt_kernel(SimtBwd p)
   float* sS = sP + BT * SP;
   const int grp = threadIdx.x >> 8, tid = threadIdx.x & 255, tx = tid & 15, ty = tid >> 4;
   const int plane = (int)blockIdx.x % p.Hkv + (int)blockIdx.y * p.Hkv;
-  const Chunk ch = find_chunk<BT>((int)blockIdx.x / p.Hkv, p.NT, p.L, p.grp, p.N, p.window, p.sinks);
+  const Chunk ch = find_chunk<BT>((int)blockIdx.x / p.Hkv, p.cut, p.L, p.grp, p.N, p.window, p.sinks);
   const int b = plane / p.Hkv, kvh = plane % p.Hkv;
   const int u0 = ch.kt * BT, nq = query_tiles_of<BT>(ch.kt, p.N, p.window, p.sinks);
   const int first = ch.idx * p.L, last = min(first + p.L, nq * p.grp);
@@ -654,11 +655,11 @@ __global__ void __launch_bounds__(THREADS, 1) win_bwd_dkv_simt_kernel(SimtBwd p)
   }
 }
 
-// Joins the chunks of one key tile in order: grid (key tiles, planes).
+// Joins the chunks of one key tile in order: grid (key tiles that may be cut, planes, parts of a tile's rows).
 template <typename T, int HD, int BTJ>
 __global__ void __launch_bounds__(256)
-    win_kvjoin_kernel(const float* part, TensorRef dk, TensorRef dv, int Hkv, int grp, int N, int NT, int L,
-                      int partials, int window, int sinks, float scale) {
+    win_kvjoin_kernel(const float* part, TensorRef dk, TensorRef dv, int Hkv, int grp, int N, int L, int partials,
+                      int window, int sinks, float scale) {
   const int kt = blockIdx.x, plane = blockIdx.y, b = plane / Hkv, kvh = plane % Hkv;
   auto chunks_of = [&](int k) {
     return (int)(((long long)query_tiles_of<BTJ>(k, N, window, sinks) * grp + L - 1) / L);
@@ -760,6 +761,7 @@ cudaError_t bwd_t(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
   p.NT = cp.NT;
   p.L = cp.L;
   p.partials = cp.partials;
+  p.cut = cp.cut;
   p.c = D.scale * kLog2e;
   p.scale = D.scale;
   auto dkv = win_bwd_dkv_simt_kernel<HD>;
@@ -788,8 +790,8 @@ cudaError_t pre_t(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
 
 template <typename T, int HD, int BTJ>
 cudaError_t join_t(const WinDims& D, const WinBwdArgs& a, const ChunkPlan& p, const float* part, cudaStream_t st) {
-  win_kvjoin_kernel<T, HD, BTJ><<<dim3(p.NT, D.B * D.Hkv, 8), 256, 0, st>>>(
-      part, a.dk, a.dv, D.Hkv, D.g, D.N, p.NT, p.L, p.partials, D.window, D.sinks, D.scale);
+  win_kvjoin_kernel<T, HD, BTJ><<<dim3(p.cut, D.B * D.Hkv, 8), 256, 0, st>>>(
+      part, a.dk, a.dv, D.Hkv, D.g, D.N, p.L, p.partials, D.window, D.sinks, D.scale);
   count_launches(1);
   return cudaGetLastError();
 }

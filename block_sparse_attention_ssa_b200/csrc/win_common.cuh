@@ -214,6 +214,7 @@ constexpr int kTcMinSteps = 8;   // steps of a chunk at least on the tensor core
 
 struct ChunkPlan {
   int L, NT, chunks, partials;  // per (batch, kv head)
+  int cut;                      // tiles from this one on are one chunk each
 };
 
 template <int BT>
@@ -228,7 +229,10 @@ inline ChunkPlan chunk_plan(const WinDims& D, int ctas, int min_steps) {
   for (int kt = 0; kt < p.NT; ++kt) {
     const int n = (int)(((long long)query_tiles_of<BT>(kt, D.N, D.window, D.sinks) * D.g + p.L - 1) / p.L);
     p.chunks += n;
-    if (n > 1) p.partials += n;
+    if (n > 1) {
+      p.partials += n;
+      p.cut = kt + 1;
+    }
   }
   return p;
 }
@@ -238,15 +242,16 @@ struct Chunk {
   int slot;        // first partial slot of the tile within its plane (n > 1)
 };
 
-// The chunk with number ci of a plane; warp-wide.
+// The chunk with number ci of a plane; warp-wide.  Only the first `cut` tiles are searched: behind them chunks
+// and tiles go together.
 template <int BT>
-__device__ __forceinline__ Chunk find_chunk(int ci, int NT, int L, int g, int N, int window, int sinks) {
+__device__ __forceinline__ Chunk find_chunk(int ci, int cut, int L, int g, int N, int window, int sinks) {
   const int lane = threadIdx.x & 31;
   int before = 0, slots = 0;
   Chunk r{0, 0, 1, 0};
-  for (int k0 = 0; k0 < NT; k0 += 32) {
+  for (int k0 = 0; k0 < cut; k0 += 32) {
     const int kt = k0 + lane;
-    const int n = kt < NT ? (int)(((long long)query_tiles_of<BT>(kt, N, window, sinks) * g + L - 1) / L) : 0;
+    const int n = kt < cut ? (int)(((long long)query_tiles_of<BT>(kt, N, window, sinks) * g + L - 1) / L) : 0;
     const int sl = n > 1 ? n : 0;
     int incl = n, incs = sl;
 #pragma unroll
@@ -269,6 +274,7 @@ __device__ __forceinline__ Chunk find_chunk(int ci, int NT, int L, int g, int N,
     before += __shfl_sync(0xffffffffu, incl, 31);
     slots += __shfl_sync(0xffffffffu, incs, 31);
   }
+  r.kt = cut + ci - before;
   return r;
 }
 

@@ -387,8 +387,11 @@ SSA_API size_t ssa_window_workspace_bytes(const ssa_window_dims_t* dims);
  *     [B, Hq, N] fp32, dense.  Inputs may broadcast batches and heads (stride 0);
  *     rows, and the slices of an output, may not lie over one another
  *     (SSA_ERR_INVALID_ARG).
- *   A NaN or an infinity in the V row of a token may reach rows of other
- *     tokens up to 127 positions earlier (a weight of zero times it). */
+ *   What a hidden key holds does not matter.  A NaN or an infinity in the V
+ *     row of token u may also reach tokens that do not see u but share a tile
+ *     with one that does (a weight of zero times it): up to 127 positions
+ *     before u, or behind the end of u's window.  The same holds for the
+ *     gradients and NaN or infinities in Q, K, g. */
 SSA_API ssa_status_t ssa_fwd_window(const ssa_window_dims_t* dims, const ssa_tensor_t* Q, const ssa_tensor_t* K,
                                     const ssa_tensor_t* V, const ssa_tensor_t* h, float* lse,
                                     ssa_stream_t stream);
@@ -450,7 +453,7 @@ SSA_API size_t ssa_paged_workspace_bytes(const ssa_paged_dims_t* dims);
  *   k, v: packed [1, Hkv, total_q, d] strided (in).
  *   K, V: the caches (in/out); only the new tokens' rows are written.
  * New tokens at negative positions and rows behind q_start[num_seqs] are
- * skipped.  Two sequences that write the same page row race. */
+ * skipped.  Two new tokens that write the same page row race. */
 SSA_API ssa_status_t ssa_paged_append(const ssa_paged_dims_t* dims, const ssa_tensor_t* k, const ssa_tensor_t* v,
                                       const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table,
                                       const ssa_tensor_t* K, const ssa_tensor_t* V, ssa_stream_t stream);

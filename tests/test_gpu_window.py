@@ -34,6 +34,13 @@ SHAPES = {
     "everything_d128": (1, 8, 1, 450, 128, EVERYTHING, 9),
     "three_to_one": (1, 3, 1, 700, 128, 256, 16),
     "group_of_sixteen": (1, 16, 1, 257, 64, 70, 4),
+    # enough heads for the form that holds two 128-row tiles at once
+    "two_tiles": (1, 64, 8, 600, 64, 130, 70),
+    "two_tiles_everything": (1, 50, 10, 641, 128, EVERYTHING, 0),
+    "two_tiles_second_short": (1, 150, 50, 140, 64, 33, 3),
+    "two_tiles_narrow": (2, 40, 8, 450, 128, 1, 1),
+    # key tiles cut into chunks
+    "cut_tiles": (1, 8, 1, 1400, 64, 65, 64),
 }
 
 
