@@ -16,6 +16,7 @@ import ctypes
 import math
 import os
 import re
+from array import array
 
 import torch
 
@@ -124,14 +125,12 @@ _SIGS = {
     "ssa_launch_count": (ctypes.c_uint64, []),
     "ssa_selftest_timeout": (ctypes.c_int, [ctypes.c_void_p]),
     "ssa_window_workspace_bytes": (ctypes.c_size_t, [_P(ssa_window_dims_t)]),
-    "ssa_fwd_window": (ctypes.c_int, [_P(ssa_window_dims_t)] + [_P(ssa_tensor_t)] * 4 + [ctypes.c_void_p] * 2),
-    "ssa_bwd_window": (ctypes.c_int, [_P(ssa_window_dims_t)] + [_P(ssa_tensor_t)] * 4 + [ctypes.c_void_p]
-                       + [_P(ssa_tensor_t)] * 4 + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    # tensors by address: ssa_tensor_t is four 64-bit words, and a call's are built in one array
+    "ssa_fwd_window": (ctypes.c_int, [ctypes.c_void_p] * 7),
+    "ssa_bwd_window": (ctypes.c_int, [ctypes.c_void_p] * 11 + [ctypes.c_size_t, ctypes.c_void_p]),
     "ssa_paged_workspace_bytes": (ctypes.c_size_t, [_P(ssa_paged_dims_t)]),
-    "ssa_paged_append": (ctypes.c_int, [_P(ssa_paged_dims_t)] + [_P(ssa_tensor_t)] * 2 + [ctypes.c_void_p] * 3
-                         + [_P(ssa_tensor_t)] * 2 + [ctypes.c_void_p]),
-    "ssa_paged_attention": (ctypes.c_int, [_P(ssa_paged_dims_t)] + [_P(ssa_tensor_t)] * 3 + [ctypes.c_void_p] * 3
-                            + [_P(ssa_tensor_t), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "ssa_paged_append": (ctypes.c_int, [ctypes.c_void_p] * 9),
+    "ssa_paged_attention": (ctypes.c_int, [ctypes.c_void_p] * 10 + [ctypes.c_size_t, ctypes.c_void_p]),
     "ssa_block_scores_noalloc": (ctypes.c_int, [_P(ssa_dims_t), _P(ssa_tensor_t), _P(ssa_tensor_t),
                                                  ctypes.c_void_p, ctypes.c_void_p]),
 }
@@ -306,16 +305,16 @@ def _wrong(name: str, x: torch.Tensor, shape: tuple, dtype: torch.dtype, device:
                       f"device ({device}), got {x.dtype} {tuple(x.shape)} on {x.device}")
 
 
-def _arg(name: str, x: torch.Tensor, shape: tuple, dtype: torch.dtype, device: torch.device, b: int, h: int, n: int):
-    """ssa_tensor_t of a checked tensor whose dimensions b, h, n are the C ABI's batch, head and row (b = -1: none)."""
+def _arg(name: str, x: torch.Tensor, shape: tuple, dtype: torch.dtype, device: torch.device, b: int, h: int, n: int) -> tuple:
+    """The words of a checked tensor's ssa_tensor_t; b, h, n: the C ABI's batch, head and row among its dimensions
+    (b = -1: none)."""
     if x.shape != shape or x.dtype is not dtype or x.device != device or not x.is_cuda:
         raise _wrong(name, x, shape, dtype, device)
     st, d = x.stride(), shape[-1]
     if st[-1] != 1:
         raise _wrong(name, x, shape, dtype, device)
     # a dimension of length one has no stride of its own: one that fits
-    return ctypes.byref(ssa_tensor_t(x.data_ptr(), st[b] if b >= 0 and shape[b] > 1 else d, st[h] if shape[h] > 1 else d,
-                                     st[n] if shape[n] > 1 else d))
+    return (x.data_ptr(), st[b] if b >= 0 and shape[b] > 1 else d, st[h] if shape[h] > 1 else d, st[n] if shape[n] > 1 else d)
 
 
 def _array(name: str, x: torch.Tensor, shape: tuple, dtype: torch.dtype, device: torch.device) -> int:
@@ -357,18 +356,24 @@ def ssa_fwd_window(dims, Q, K, V, h, lse, stream=None) -> None:
     """Window attention with sinks: Q, h [B, Hq, N, d], K, V [B, Hkv, N, d], lse [B, Hq, N] fp32."""
     dt, dev, N, d = dims.torch_dtype, Q.device, dims.N, dims.d
     q, kv = (dims.B, dims.Hq, N, d), (dims.B, dims.Hkv, N, d)
-    _call("ssa_fwd_window", dev, stream, ctypes.byref(dims), _arg("Q", Q, q, dt, dev, 0, 1, 2), _arg("K", K, kv, dt, dev, 0, 1, 2),
-          _arg("V", V, kv, dt, dev, 0, 1, 2), _arg("h", h, q, dt, dev, 0, 1, 2), _array("lse", lse, q[:3], torch.float32, dev))
+    words = array("q", (*_arg("Q", Q, q, dt, dev, 0, 1, 2), *_arg("K", K, kv, dt, dev, 0, 1, 2),
+                        *_arg("V", V, kv, dt, dev, 0, 1, 2), *_arg("h", h, q, dt, dev, 0, 1, 2)))
+    t = words.buffer_info()[0]
+    _call("ssa_fwd_window", dev, stream, ctypes.byref(dims), t, t + 32, t + 64, t + 96,
+          _array("lse", lse, q[:3], torch.float32, dev))
 
 
 def ssa_bwd_window(dims, Q, K, V, h, lse, g, dQ, dK, dV, ws, stream=None) -> None:
     """Gradients of <g, h> for what ssa_fwd_window computed."""
     dt, dev, N, d = dims.torch_dtype, Q.device, dims.N, dims.d
     q, kv = (dims.B, dims.Hq, N, d), (dims.B, dims.Hkv, N, d)
-    _call("ssa_bwd_window", dev, stream, ctypes.byref(dims), _arg("Q", Q, q, dt, dev, 0, 1, 2), _arg("K", K, kv, dt, dev, 0, 1, 2),
-          _arg("V", V, kv, dt, dev, 0, 1, 2), _arg("h", h, q, dt, dev, 0, 1, 2), _array("lse", lse, q[:3], torch.float32, dev),
-          _arg("g", g, q, dt, dev, 0, 1, 2), _arg("dQ", dQ, q, dt, dev, 0, 1, 2), _arg("dK", dK, kv, dt, dev, 0, 1, 2),
-          _arg("dV", dV, kv, dt, dev, 0, 1, 2), *_scratch(ws, dev))
+    words = array("q", (*_arg("Q", Q, q, dt, dev, 0, 1, 2), *_arg("K", K, kv, dt, dev, 0, 1, 2),
+                        *_arg("V", V, kv, dt, dev, 0, 1, 2), *_arg("h", h, q, dt, dev, 0, 1, 2),
+                        *_arg("g", g, q, dt, dev, 0, 1, 2), *_arg("dQ", dQ, q, dt, dev, 0, 1, 2),
+                        *_arg("dK", dK, kv, dt, dev, 0, 1, 2), *_arg("dV", dV, kv, dt, dev, 0, 1, 2)))
+    t = words.buffer_info()[0]
+    _call("ssa_bwd_window", dev, stream, ctypes.byref(dims), t, t + 32, t + 64, t + 96,
+          _array("lse", lse, q[:3], torch.float32, dev), t + 128, t + 160, t + 192, t + 224, *_scratch(ws, dev))
 
 
 def _batch(q_start, kv_len, page_table, dims, dev) -> tuple[int, int, int]:
@@ -381,19 +386,23 @@ def ssa_paged_append(dims, k, v, q_start, kv_len, page_table, K, V, stream=None)
     """Writes the new rows k, v [total_q, Hkv, d] into the caches K, V [num_pages, page, Hkv, d] (any strides)."""
     dt, dev, Hkv, d = dims.torch_dtype, k.device, dims.Hkv, dims.d
     new, cache = (dims.total_q, Hkv, d), (dims.num_pages, dims.page, Hkv, d)
-    _call("ssa_paged_append", dev, stream, ctypes.byref(dims), _arg("k", k, new, dt, dev, -1, 1, 0),
-          _arg("v", v, new, dt, dev, -1, 1, 0), *_batch(q_start, kv_len, page_table, dims, dev),
-          _arg("K", K, cache, dt, dev, 0, 2, 1), _arg("V", V, cache, dt, dev, 0, 2, 1))
+    words = array("q", (*_arg("k", k, new, dt, dev, -1, 1, 0), *_arg("v", v, new, dt, dev, -1, 1, 0),
+                        *_arg("K", K, cache, dt, dev, 0, 2, 1), *_arg("V", V, cache, dt, dev, 0, 2, 1)))
+    t = words.buffer_info()[0]
+    _call("ssa_paged_append", dev, stream, ctypes.byref(dims), t, t + 32, *_batch(q_start, kv_len, page_table, dims, dev),
+          t + 64, t + 96)
 
 
 def ssa_paged_attention(dims, q, K, V, q_start, kv_len, page_table, h, lse, ws, stream=None) -> None:
     """Attention of the new rows q [total_q, Hq, d] over the caches: h [total_q, Hq, d], lse [Hq, total_q] fp32."""
     dt, dev, T, Hq, d = dims.torch_dtype, q.device, dims.total_q, dims.Hq, dims.d
     rows, cache = (T, Hq, d), (dims.num_pages, dims.page, dims.Hkv, d)
-    _call("ssa_paged_attention", dev, stream, ctypes.byref(dims), _arg("q", q, rows, dt, dev, -1, 1, 0),
-          _arg("K", K, cache, dt, dev, 0, 2, 1), _arg("V", V, cache, dt, dev, 0, 2, 1),
-          *_batch(q_start, kv_len, page_table, dims, dev), _arg("h", h, rows, dt, dev, -1, 1, 0),
-          _array("lse", lse, (Hq, T), torch.float32, dev), *_scratch(ws, dev))
+    words = array("q", (*_arg("q", q, rows, dt, dev, -1, 1, 0), *_arg("K", K, cache, dt, dev, 0, 2, 1),
+                        *_arg("V", V, cache, dt, dev, 0, 2, 1), *_arg("h", h, rows, dt, dev, -1, 1, 0)))
+    t = words.buffer_info()[0]
+    _call("ssa_paged_attention", dev, stream, ctypes.byref(dims), t, t + 32, t + 64,
+          *_batch(q_start, kv_len, page_table, dims, dev), t + 96, _array("lse", lse, (Hq, T), torch.float32, dev),
+          *_scratch(ws, dev))
 
 
 def ssa_launch_count() -> int:
