@@ -1,0 +1,844 @@
+// Window attention with sinks and paged attention in fp32, and the preprocess and the join
+// of the backward for both types.
+//
+// Mathematics: the online softmax over the visible keys (base 2, scale folded in) and,
+// backward, p = 2^(x c - lse2), dx = p (g.v - D), dQ = scale dx K, dK = scale dx^T Q,
+// dV = p^T g.  Products run on the warp-level tensor cores in TF32, each fp32 operand as the
+// sum of two TF32 values (11 bits each) and each product as three: a_lo b_hi + a_hi b_lo +
+// a_hi b_hi, fp32 accumulation.  What is left out, a_lo b_lo and the low part's own last
+// bits, is below 2^-21 of the product: nearer than an fp32 dot product of 64 terms needs to
+// be.  On the FMA pipe the same tiles were bound by shared memory (a 4 x 4 thread tile reads
+// twice what the pipe can take): 178 against FIXME us for the training step below.
+//
+// Tiles: 64 queries by 64 keys, a warp 16 rows by all columns, so that a row's statistics
+// need no exchange between warps and the weights go from the accumulators of one product to
+// the operand of the next in registers.  Groups of four warps take a CTA's tiles in turn and
+// join at the end, so that few rows fill an SM's warps too, and one group's copies
+// (cp.async, zeros for hidden rows) run under another's products.
+//
+// Fragments of mma.m16n8k8 (g = lane / 4, t = lane % 4): A holds rows g, g + 8 and reduction
+// t, t + 4; B reduction t, t + 4 and column g; C rows g, g + 8 and columns 2t, 2t + 1.  The
+// order of the reduction is free: t and t + 4 stand for elements 2t and 2t + 1 of each eight,
+// so an accumulator is the next product's A as it is, and A and B of the logits are 8-byte
+// loads.
+#include "win_common.cuh"
+
+#include <type_traits>
+
+#include "mma_sync.cuh"
+
+namespace ssa {
+namespace {
+
+constexpr int BT = 64;
+constexpr int GROUP = 128;  // threads on one 64 x 64 tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// CTAs of one paged call, one per SM; units are worth a CTA from two on.
+constexpr int kPagedCtas = 148;
+constexpr int kMinUnits = 2;
+// Steps of a backward chunk at least: a 64 x 64 step takes microseconds of a CTA, a partial's round trip less.
+constexpr int kMinSteps = 2;
+
+// Row pitches in shared memory, by the fragments' 32 banks: rows read as 8-byte pairs of a row (logits) want a
+// pitch of 8 mod 32, rows read down a column (weighted sums) 4 mod 32.  A tile read both ways takes the latter.
+template <int HD>
+struct Pitch {
+  static constexpr int along = HD + 8, down = HD + 4;
+};
+
+struct F32Params {
+  TensorRef q, k, v, h;
+  float* lse;
+  int Hq, g, N, window, sinks, NT;
+  float c;
+  // paged
+  const int32_t* table;
+  Batch batch;
+  int page, num_pages, max_pages, T;
+  float* part;
+};
+
+// ---------------------------------------------------------------- TF32 in pairs
+struct Pair {
+  uint32_t hi, lo;
+};
+// x = hi + lo: hi rounded to 11 bits, lo the exact rest (the tensor core reads its upper 11 bits).
+__device__ __forceinline__ Pair split(float x) {
+  Pair p;
+  p.hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+  p.lo = __float_as_uint(x - __uint_as_float(p.hi));
+  return p;
+}
+
+__device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// c += a b to fp32 accuracy, the small terms first.
+__device__ __forceinline__ void mma_pairs(float (&c)[4], const Pair (&a)[4], const Pair (&b)[2]) {
+  mma_tf32(c, a[0].lo, a[1].lo, a[2].lo, a[3].lo, b[0].hi, b[1].hi);
+  mma_tf32(c, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[0].lo, b[1].lo);
+  mma_tf32(c, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[0].hi, b[1].hi);
+}
+
+// c[n] = (16 rows of A) . (rows 8 n .. 8 n + 7 of B) over HD; A: row g of the warp's sixteen at A + g PA.
+template <int HD, int NT, int PA, int PB>
+__device__ __forceinline__ void logits(float (&c)[NT][4], const float* A, const float* B, int g, int t) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[n][i] = 0.f;
+#pragma unroll 2
+  for (int k = 0; k < HD; k += 8) {
+    const float2 x = *reinterpret_cast<const float2*>(A + g * PA + k + 2 * t);
+    const float2 y = *reinterpret_cast<const float2*>(A + (g + 8) * PA + k + 2 * t);
+    const Pair a[4] = {split(x.x), split(y.x), split(x.y), split(y.y)};
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float2 z = *reinterpret_cast<const float2*>(B + (8 * n + g) * PB + k + 2 * t);
+      const Pair b[2] = {split(z.x), split(z.y)};
+      mma_pairs(c[n], a, b);
+    }
+  }
+}
+
+// acc[n] += W X for the weights W (16 x 8 KT, accumulator layout) and the rows of X, columns 8 n ...
+template <int HD, int KT, int PX>
+__device__ __forceinline__ void weighted(float (&acc)[HD / 8][4], const float (&w)[KT][4], const float* X, int g, int t) {
+#pragma unroll
+  for (int k = 0; k < KT; ++k) {
+    const Pair a[4] = {split(w[k][0]), split(w[k][2]), split(w[k][1]), split(w[k][3])};
+    const float* r0 = X + (8 * k + 2 * t) * PX + g;
+#pragma unroll
+    for (int n = 0; n < HD / 8; ++n) {
+      const Pair b[2] = {split(r0[8 * n]), split(r0[PX + 8 * n])};
+      mma_pairs(acc[n], a, b);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- shared memory
+// 64 rows of HD values by the `n` threads tid = 0 ..; a null row gives zeros (and a copy of no bytes from `any`).
+// Asynchronous: copies_done() below.
+template <int HD, int P, typename F>
+__device__ __forceinline__ void copy_rows(float* dst, const void* any, int tid, int n, F row) {
+  constexpr int PER = HD / 4;
+  for (int e = tid; e < BT * PER; e += n) {
+    const float* r = row(e / PER);
+    warp_mma::cp_async16(dst + (e / PER) * P + (e % PER) * 4, r != nullptr ? r + (e % PER) * 4 : any, r != nullptr ? 16 : 0);
+  }
+  warp_mma::cp_async_commit();
+}
+__device__ __forceinline__ void copies_done() { warp_mma::cp_async_wait<0>(); }
+__device__ __forceinline__ void group_sync(int grp) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(GROUP) : "memory");
+}
+
+// ================================================================ forward
+template <int HD>
+struct Fwd {
+  static constexpr int GROUPS = HD == 128 ? 3 : 4;  // registers: 168 and 128 a thread
+  static constexpr int THREADS = GROUPS * GROUP;
+  static constexpr int TILEF = BT * Pitch<HD>::along;
+  static constexpr size_t SMEM = (size_t)(1 + GROUPS) * TILEF * 4;  // Q, then each group's K or V
+};
+
+template <int HD, bool PAGED>
+__global__ void __launch_bounds__(Fwd<HD>::THREADS, 1) win_fwd_f32_kernel(F32Params p) {
+  using C = Fwd<HD>;
+  constexpr int PA = Pitch<HD>::along, PD = Pitch<HD>::down;
+  extern __shared__ float sm[];
+  float* sQ = sm;
+  const int grp = threadIdx.x / GROUP, tid = threadIdx.x % GROUP, warp = tid >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  float* sX = sQ + (1 + grp) * C::TILEF;  // K, then V, at the end the group's accumulators
+  __shared__ Place sh_place;
+  __shared__ int sh_left;
+  __shared__ float sh_m[C::GROUPS][BT], sh_l[C::GROUPS][BT];
+
+  Place at{0, 0, 0, 0};
+  int left = 1;
+  if (PAGED) {
+    if (threadIdx.x < 32) {
+      const long long U = p.batch.total<BT>();
+      const long long per = share(U, (int)gridDim.x, kMinUnits);
+      const long long u0 = per * blockIdx.x;
+      const long long n = u0 < U ? min(per, U - u0) : 0;
+      if (n > 0) at = p.batch.locate<BT>(u0);
+      if (threadIdx.x == 0) {
+        sh_place = at;
+        sh_left = (int)n;
+      }
+    }
+    __syncthreads();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be brought up
+    at = sh_place;
+    left = sh_left;
+  }
+
+  for (int seg = 0; left > 0; ++seg) {
+    // ---- the item
+    int b, head0, q0row, kvh, nrows, p0, per_tok, i0 = 0, units, take, len;
+    Seq s{};
+    KeyTiles kt;
+    if (PAGED) {
+      b = at.b;
+      s = load_seq(p.batch.q_start, p.batch.kv_len, b, p.T, p.batch.cap);
+      i0 = at.run * p.batch.TI;
+      const int toks = min(p.batch.TI, s.n - i0);
+      kvh = at.kvh;
+      head0 = kvh * p.g;
+      per_tok = p.g;
+      nrows = toks * p.g;
+      q0row = s.q0 + i0;
+      p0 = s.len - s.n + i0;
+      len = s.len;
+      kt = run_tiles<BT>(s, i0, p.batch.TI, p.window, p.sinks);
+      units = max(1, kt.count);
+      take = min(left, units - at.off);
+    } else {
+      const int planes = (int)(gridDim.x / p.NT);
+      const int plane = (int)blockIdx.x % planes, qt = p.NT - 1 - (int)blockIdx.x / planes;
+      b = plane / p.Hq;
+      head0 = plane % p.Hq;
+      kvh = head0 / p.g;
+      per_tok = 1;
+      q0row = p0 = qt * BT;
+      nrows = min(BT, p.N - p0);
+      len = p.N;
+      kt = key_tiles<BT>(p0, p0 + nrows - 1, p.window, p.sinks);
+      units = take = kt.count;
+    }
+    const bool cut = PAGED && take < units;
+    auto tok_of = [&](int r) { return PAGED ? r / per_tok : r; };
+    auto head_of = [&](int r) { return PAGED ? head0 + r % per_tok : head0; };
+    copy_rows<HD, PA>(sQ, p.q.p, threadIdx.x, C::THREADS, [&](int r) -> const float* {
+      return r < nrows ? row_ptr<float>(p.q, PAGED ? 0 : b, head_of(r), q0row + tok_of(r)) : nullptr;
+    });
+
+    // rows r and r + 8 of the tile
+    const int r0 = 16 * warp + g;
+    float acc[HD / 8][4], m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
+    int pos[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) pos[i] = r0 + 8 * i < nrows ? p0 + tok_of(r0 + 8 * i) : -1;
+#pragma unroll
+    for (int n = 0; n < HD / 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+    const int pmax = p0 + tok_of(nrows - 1), lo_min = p0 - p.window + 1;
+
+    const int end = min(at.off + take, kt.count);
+    copies_done();
+    __syncthreads();  // Q is there
+    for (int j = at.off + grp; j < end; j += C::GROUPS) {
+      const int u0 = kt.tile(j) * BT;
+      // A key that no row of the item sees is not read (its memory may hold anything).
+      auto keys = [&](const TensorRef& x) {
+        return [&, x](int r) -> const float* {
+          const int u = u0 + r;
+          if (u > pmax || u >= len || (u < lo_min && u >= p.sinks)) return nullptr;
+          if (!PAGED) return row_ptr<float>(x, b, kvh, u);
+          const int pg = p.table[(int64_t)b * p.max_pages + u / p.page];
+          return (unsigned)pg < (unsigned)p.num_pages ? row_ptr<float>(x, pg, kvh, u % p.page) : nullptr;
+        };
+      };
+      copy_rows<HD, PA>(sX, p.q.p, tid, GROUP, keys(p.k));
+      uint32_t gone[2] = {0u, 0u};  // keys whose page is missing
+      if (PAGED)
+        for (int c = 0; c < BT; c += 16) {  // a page holds 16 tokens at least
+          const int u = u0 + c;
+          if (u < len && (unsigned)p.table[(int64_t)b * p.max_pages + u / p.page] >= (unsigned)p.num_pages)
+            gone[c >> 5] |= 0xffffu << (c & 16);
+        }
+      copies_done();
+      group_sync(grp);
+      float x[8][4];
+      logits<HD, 8, PA, PA>(x, sQ + 16 * warp * PA, sX, g, t);
+      group_sync(grp);  // K is read
+      copy_rows<HD, PD>(sX, p.q.p, tid, GROUP, keys(p.v));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t v0 = visible_keys(pos[i], u0, p.window, p.sinks) & ~gone[0];
+        const uint32_t v1 = visible_keys(pos[i], u0 + 32, p.window, p.sinks) & ~gone[1];
+        float mx = kNegInf;
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t vis = (n < 4 ? v0 : v1) >> (2 * t);
+            x[n][2 * i + e] = keep(vis, 8 * (n & 3) + e, x[n][2 * i + e] * p.c, kNegInf);
+            mx = fmaxf(mx, x[n][2 * i + e]);
+          }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[i], mx), ref = mn == kNegInf ? 0.f : mn, f = exp2f(m[i] - ref);
+        m[i] = mn;
+        l[i] *= f;
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            x[n][2 * i + e] = exp2f(x[n][2 * i + e] - ref);
+            l[i] += x[n][2 * i + e];
+          }
+#pragma unroll
+        for (int n = 0; n < HD / 8; ++n) {
+          acc[n][2 * i] *= f;
+          acc[n][2 * i + 1] *= f;
+        }
+      }
+      copies_done();
+      group_sync(grp);
+      weighted<HD, 8, PD>(acc, x, sX, g, t);
+      group_sync(grp);  // V is read
+    }
+
+    // ---- the groups' softmaxes, joined by the first one
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      const int r = r0 + 8 * i;
+      if (grp > 0) {
+        if (t == 0) {
+          sh_m[grp][r] = m[i];
+          sh_l[grp][r] = l[i];
+        }
+#pragma unroll
+        for (int n = 0; n < HD / 8; ++n)
+          *reinterpret_cast<float2*>(sX + r * PA + 8 * n + 2 * t) = make_float2(acc[n][2 * i], acc[n][2 * i + 1]);
+      }
+    }
+    __syncthreads();
+    if (grp == 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = r0 + 8 * i;
+#pragma unroll 1
+        for (int o = 1; o < C::GROUPS; ++o) {
+          const float m1 = sh_m[o][r], mn = fmaxf(m[i], m1), ref = mn == kNegInf ? 0.f : mn;
+          const float f0 = exp2f(m[i] - ref), f1 = exp2f(m1 - ref);
+          l[i] = l[i] * f0 + sh_l[o][r] * f1;
+          m[i] = mn;
+          const float* other = sQ + (1 + o) * C::TILEF + r * PA + 2 * t;
+#pragma unroll
+          for (int n = 0; n < HD / 8; ++n) {
+            const float2 y = *reinterpret_cast<const float2*>(other + 8 * n);
+            acc[n][2 * i] = acc[n][2 * i] * f0 + y.x * f1;
+            acc[n][2 * i + 1] = acc[n][2 * i + 1] * f0 + y.y * f1;
+          }
+        }
+        // ---- epilogue
+        if (r >= nrows) continue;
+        float* dst;
+        float mul = 1.f;
+        if (cut) {
+          float* base = p.part + (size_t)(2 * blockIdx.x + (seg ? 1 : 0)) * partial_floats(BT, HD);
+          dst = base + r * HD;
+          if (t == 0) {
+            base[BT * HD + r] = m[i];
+            base[BT * HD + BT + r] = l[i];
+          }
+        } else {
+          mul = l[i] == 0.f ? 0.f : 1.0f / l[i];
+          dst = row_ptr_w<float>(p.h, PAGED ? 0 : b, head_of(r), q0row + tok_of(r));
+          if (t == 0) {
+            const int64_t o = PAGED ? (int64_t)head_of(r) * p.T + q0row + tok_of(r)
+                                    : ((int64_t)b * p.Hq + head0) * p.N + q0row + r;
+            p.lse[o] = l[i] == 0.f ? kNegInf : (m[i] + log2f(l[i])) * kLn2;
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < HD / 8; ++n)
+          *reinterpret_cast<float2*>(dst + 8 * n + 2 * t) = make_float2(acc[n][2 * i] * mul, acc[n][2 * i + 1] * mul);
+      }
+    }
+    if (!PAGED) break;
+    // ---- the next item
+    left -= take;
+    if (left <= 0) break;
+    at.off = 0;
+    if (++at.kvh == p.batch.Hkv) {
+      at.kvh = 0;
+      ++at.run;
+      while (at.b < p.batch.seqs) {
+        s = load_seq(p.batch.q_start, p.batch.kv_len, at.b, p.T, p.batch.cap);
+        if (at.run * p.batch.TI < s.n) break;
+        at.run = 0;
+        ++at.b;
+      }
+      if (at.b >= p.batch.seqs) break;
+    }
+    __syncthreads();  // shared memory is read to the end
+  }
+}
+
+// ================================================================ backward
+// -D_t = -(g_t . h_t) and -lse in base 2, rows padded to 128 tokens.  Bound by reading h and g: a row is LPR
+// lanes of 16 bytes, and a warp has four rows' loads of each in flight per lane group.
+template <typename T, int HD>
+__global__ void __launch_bounds__(256) win_bwd_pre_kernel(TensorRef h, TensorRef g, const float* lse, float* lse2,
+                                                          float* dsum, int Hq, int N, int Npad) {
+  constexpr int V = Vec16<T>::kN, LPR = HD / V, RPW = 32 / LPR, U = 4;
+  const int lane = threadIdx.x & 31, c = lane % LPR * V;
+  const int bh = blockIdx.y, b = bh / Hq, hd = bh % Hq;
+  const int t0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * (RPW * U) + lane / LPR;
+  uint4 x[U], y[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int t = t0 + i * RPW;
+    x[i] = y[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (t < N) {
+      x[i] = *reinterpret_cast<const uint4*>(row_ptr<T>(h, b, hd, t) + c);
+      y[i] = *reinterpret_cast<const uint4*>(row_ptr<T>(g, b, hd, t) + c);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int t = t0 + i * RPW;
+    float u[V], v[V], s = 0.f;
+    Vec16<T>::load(reinterpret_cast<const T*>(&x[i]), u);
+    Vec16<T>::load(reinterpret_cast<const T*>(&y[i]), v);
+#pragma unroll
+    for (int e = 0; e < V; ++e) s = fmaf(u[e], v[e], s);
+#pragma unroll
+    for (int o = LPR / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane % LPR == 0 && t < Npad) {
+      float ls = kNegInf;  // 2^(x - inf) = 0 in the padding and in rows without weight
+      if (t < N) {
+        const float l = lse[(int64_t)bh * N + t] * kLog2e;
+        if (l != kNegInf) ls = -l;
+      }
+      lse2[(int64_t)bh * Npad + t] = ls;
+      dsum[(int64_t)bh * Npad + t] = -s;
+    }
+  }
+}
+
+struct F32Bwd {
+  TensorRef q, k, v, g, dq, dk, dv;
+  const float* lse2;
+  const float* dsum;
+  float* part;
+  int Hq, Hkv, grp, N, Npad, window, sinks, NT, L, partials, cut;
+  float c, scale;
+};
+
+// Two groups of four warps, up to 255 registers a thread: the accumulators of a warp's sixteen rows stay in them
+// (128 in dkv at d = 128), logits and dP are formed 32 columns at a time.
+constexpr int BWD_THREADS = 2 * GROUP;
+
+// dq: Q, g, then each group's K, V.  dkv: K, V, then each group's Q, g.
+template <int HD>
+constexpr size_t bwd_smem() {
+  return (size_t)(2 * BT * Pitch<HD>::along + 2 * BT * (Pitch<HD>::down + Pitch<HD>::along)) * 4;
+}
+
+// The second group's accumulators are added to the first's through shared memory (the group's own tiles).
+template <int HD>
+__device__ __forceinline__ void add_groups(float (&acc)[HD / 8][4], float* buf, int grp, int r0, int t) {
+  constexpr int P = Pitch<HD>::down;
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < HD / 8; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float2* q = reinterpret_cast<float2*>(buf + (r0 + 8 * i) * P + 8 * n + 2 * t);
+      if (grp == 1) *q = make_float2(acc[n][2 * i], acc[n][2 * i + 1]);
+    }
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < HD / 8; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 y = *reinterpret_cast<const float2*>(buf + (r0 + 8 * i) * P + 8 * n + 2 * t);
+      if (grp == 0) {
+        acc[n][2 * i] += y.x;
+        acc[n][2 * i + 1] += y.y;
+      }
+    }
+}
+
+template <int HD>
+__device__ __forceinline__ void store_rows(float* row, const float (&acc)[HD / 8][4], int i, int t, float mul) {
+#pragma unroll
+  for (int n = 0; n < HD / 8; ++n)
+    *reinterpret_cast<float2*>(row + 8 * n + 2 * t) = make_float2(acc[n][2 * i] * mul, acc[n][2 * i + 1] * mul);
+}
+
+template <int HD>
+__global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dq_f32_kernel(F32Bwd p) {
+  constexpr int PA = Pitch<HD>::along, PD = Pitch<HD>::down;
+  extern __shared__ float sm[];
+  const int grp = threadIdx.x / GROUP, tid = threadIdx.x % GROUP, warp = tid >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3, r0 = 16 * warp + g;
+  float* sQ = sm;
+  float* sG = sQ + BT * PA;
+  float* sK = sG + BT * PA + grp * BT * (PD + PA);  // read along (logits) and down (dQ)
+  float* sV = sK + BT * PD;
+  const int planes = (int)(gridDim.x / p.NT);
+  const int plane = (int)blockIdx.x % planes, qt = p.NT - 1 - (int)blockIdx.x / planes;
+  const int b = plane / p.Hq, h = plane % p.Hq, kvh = h / p.grp;
+  const int q0 = qt * BT, nrows = min(BT, p.N - q0);
+  const KeyTiles kt = key_tiles<BT>(q0, q0 + nrows - 1, p.window, p.sinks);
+  auto query = [&](const TensorRef& x) {
+    return [&, x](int r) -> const float* { return r < nrows ? row_ptr<float>(x, b, h, q0 + r) : nullptr; };
+  };
+  copy_rows<HD, PA>(sQ, p.q.p, threadIdx.x, BWD_THREADS, query(p.q));
+  copy_rows<HD, PA>(sG, p.q.p, threadIdx.x, BWD_THREADS, query(p.g));
+  float nl[2], nd[2], acc[HD / 8][4];  // -lse2, -D
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t o = ((int64_t)b * p.Hq + h) * p.Npad + q0 + r0 + 8 * i;
+    nl[i] = p.lse2[o];
+    nd[i] = p.dsum[o];
+  }
+#pragma unroll
+  for (int n = 0; n < HD / 8; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+  copies_done();
+  __syncthreads();
+  for (int j = grp; j < kt.count; j += 2) {
+    const int u0 = kt.tile(j) * BT;
+    auto key = [&](const TensorRef& x) {
+      return [&, x](int r) -> const float* { return u0 + r < p.N ? row_ptr<float>(x, b, kvh, u0 + r) : nullptr; };
+    };
+    copy_rows<HD, PD>(sK, p.q.p, tid, GROUP, key(p.k));
+    copy_rows<HD, PA>(sV, p.q.p, tid, GROUP, key(p.v));
+    copies_done();
+    group_sync(grp);
+#pragma unroll 1
+    for (int c0 = 0; c0 < BT; c0 += 32) {
+      float x[4][4], y[4][4];
+      logits<HD, 4, PA, PD>(x, sQ + 16 * warp * PA, sK + c0 * PD, g, t);
+      logits<HD, 4, PA, PA>(y, sG + 16 * warp * PA, sV + c0 * PA, g, t);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t vis = visible_keys(q0 + r0 + 8 * i, u0 + c0, p.window, p.sinks) >> (2 * t);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int k = 2 * i + e;
+            x[n][k] = keep(vis, 8 * n + e, exp2f(fmaf(x[n][k], p.c, nl[i])) * (y[n][k] + nd[i]), 0.f);
+          }
+      }
+      weighted<HD, 4, PD>(acc, x, sK + c0 * PD, g, t);
+    }
+    group_sync(grp);  // K and V are read
+  }
+  add_groups<HD>(acc, sG + BT * PA, grp, r0, t);
+  if (grp == 0)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (r0 + 8 * i < nrows) store_rows<HD>(row_ptr_w<float>(p.dq, b, h, q0 + r0 + 8 * i), acc, i, t, p.scale);
+}
+
+template <int HD>
+__global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dkv_f32_kernel(F32Bwd p) {
+  constexpr int PA = Pitch<HD>::along, PD = Pitch<HD>::down;
+  extern __shared__ float sm[];
+  const int grp = threadIdx.x / GROUP, tid = threadIdx.x % GROUP, warp = tid >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3, r0 = 16 * warp + g;
+  float* sK = sm;
+  float* sV = sK + BT * PA;
+  float* sQ = sV + BT * PA + grp * 2 * BT * PD;  // read along (logits) and down (dK, dV)
+  float* sG = sQ + BT * PD;
+  const int plane = (int)blockIdx.x % p.Hkv + (int)blockIdx.y * p.Hkv;
+  const Chunk ch = find_chunk<BT>((int)blockIdx.x / p.Hkv, p.cut, p.L, p.grp, p.N, p.window, p.sinks);
+  const int b = plane / p.Hkv, kvh = plane % p.Hkv;
+  const int u0 = ch.kt * BT, nq = query_tiles_of<BT>(ch.kt, p.N, p.window, p.sinks);
+  const int first = ch.idx * p.L, last = min(first + p.L, nq * p.grp);
+  auto key = [&](const TensorRef& x) {
+    return [&, x](int r) -> const float* { return u0 + r < p.N ? row_ptr<float>(x, b, kvh, u0 + r) : nullptr; };
+  };
+  copy_rows<HD, PA>(sK, p.q.p, threadIdx.x, BWD_THREADS, key(p.k));
+  copy_rows<HD, PA>(sV, p.q.p, threadIdx.x, BWD_THREADS, key(p.v));
+  float dk[HD / 8][4], dv[HD / 8][4];
+#pragma unroll
+  for (int n = 0; n < HD / 8; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dk[n][i] = dv[n][i] = 0.f;
+  copies_done();
+  __syncthreads();
+  for (int s = first + grp; s < last; s += 2) {
+    const int h = kvh * p.grp + s / nq, q0 = (ch.kt + s % nq) * BT;
+    auto query = [&](const TensorRef& x) {
+      return [&, x](int r) -> const float* { return q0 + r < p.N ? row_ptr<float>(x, b, h, q0 + r) : nullptr; };
+    };
+    copy_rows<HD, PD>(sQ, p.q.p, tid, GROUP, query(p.q));
+    copy_rows<HD, PD>(sG, p.q.p, tid, GROUP, query(p.g));
+    const float* nl = p.lse2 + ((int64_t)b * p.Hq + h) * p.Npad + q0 + 2 * t;  // -lse2, -D of columns 2t, 2t + 1
+    const float* nd = p.dsum + ((int64_t)b * p.Hq + h) * p.Npad + q0 + 2 * t;
+    copies_done();
+    group_sync(grp);
+#pragma unroll 1
+    for (int c0 = 0; c0 < BT; c0 += 32) {
+      float x[4][4], y[4][4];
+      logits<HD, 4, PA, PD>(x, sK + 16 * warp * PA, sQ + c0 * PD, g, t);
+      logits<HD, 4, PA, PD>(y, sV + 16 * warp * PA, sG + c0 * PD, g, t);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const float2 l2 = *reinterpret_cast<const float2*>(nl + c0 + 8 * n), d2 = *reinterpret_cast<const float2*>(nd + c0 + 8 * n);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t vis = visible_queries(u0 + r0 + 8 * i, q0 + c0, p.window, p.sinks) >> (2 * t);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int k = 2 * i + e;
+            const float pv = keep(vis, 8 * n + e, exp2f(fmaf(x[n][k], p.c, e ? l2.y : l2.x)), 0.f);
+            x[n][k] = pv;
+            y[n][k] = keep(vis, 8 * n + e, pv * (y[n][k] + (e ? d2.y : d2.x)), 0.f);
+          }
+        }
+      }
+      weighted<HD, 4, PD>(dv, x, sG + c0 * PD, g, t);
+      weighted<HD, 4, PD>(dk, y, sQ + c0 * PD, g, t);
+    }
+    group_sync(grp);  // Q and g are read
+  }
+  add_groups<HD>(dk, sV + BT * PA, grp, r0, t);
+  add_groups<HD>(dv, sV + BT * PA, grp, r0, t);
+  if (grp == 0)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int u = u0 + r0 + 8 * i;
+      if (u >= p.N) continue;
+      if (ch.n == 1) {
+        store_rows<HD>(row_ptr_w<float>(p.dk, b, kvh, u), dk, i, t, p.scale);
+        store_rows<HD>(row_ptr_w<float>(p.dv, b, kvh, u), dv, i, t, 1.0f);
+      } else {
+        float* base = p.part + ((size_t)plane * p.partials + ch.slot + ch.idx) * (2 * BT * HD) + (r0 + 8 * i) * HD;
+        store_rows<HD>(base, dk, i, t, 1.0f);
+        store_rows<HD>(base + BT * HD, dv, i, t, 1.0f);
+      }
+    }
+}
+
+// Joins the chunks of one key tile in order: grid (key tiles that may be cut, planes, parts of a tile's rows).
+template <typename T, int HD, int BTJ>
+__global__ void __launch_bounds__(256)
+    win_kvjoin_kernel(const float* part, TensorRef dk, TensorRef dv, int Hkv, int grp, int N, int L, int partials,
+                      int window, int sinks, float scale) {
+  const int kt = blockIdx.x, plane = blockIdx.y, b = plane / Hkv, kvh = plane % Hkv;
+  auto chunks_of = [&](int k) {
+    return (int)(((long long)query_tiles_of<BTJ>(k, N, window, sinks) * grp + L - 1) / L);
+  };
+  const int n = chunks_of(kt);
+  if (n == 1) return;
+  __shared__ int slot_sh;
+  if (threadIdx.x < 32) {
+    int s = 0;
+    for (int k = threadIdx.x; k < kt; k += 32) {
+      const int c = chunks_of(k);
+      s += c > 1 ? c : 0;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (threadIdx.x == 0) slot_sh = s;
+  }
+  __syncthreads();
+  const float* base = part + ((size_t)plane * partials + slot_sh) * (2 * BTJ * HD);
+  // blockIdx.z cuts the tile's rows
+  const int rows = BTJ / gridDim.z, r0 = blockIdx.z * rows;
+  for (int e = threadIdx.x; e < rows * HD / 4; e += 256) {
+    const int r = r0 + e / (HD / 4), c = (e % (HD / 4)) * 4, u = kt * BTJ + r;
+    if (u >= N) continue;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), v = a;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float* q = base + (size_t)i * (2 * BTJ * HD) + r * HD + c;
+      const float4 x = *reinterpret_cast<const float4*>(q), y = *reinterpret_cast<const float4*>(q + BTJ * HD);
+      a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+      v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+    }
+    T* ok = row_ptr_w<T>(dk, b, kvh, u) + c;
+    T* ov = row_ptr_w<T>(dv, b, kvh, u) + c;
+    ok[0] = from_f32<T>(a.x * scale);
+    ok[1] = from_f32<T>(a.y * scale);
+    ok[2] = from_f32<T>(a.z * scale);
+    ok[3] = from_f32<T>(a.w * scale);
+    ov[0] = from_f32<T>(v.x);
+    ov[1] = from_f32<T>(v.y);
+    ov[2] = from_f32<T>(v.z);
+    ov[3] = from_f32<T>(v.w);
+  }
+}
+
+template <typename K>
+cudaError_t set_smem(K kern, size_t bytes) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <int HD>
+cudaError_t fwd_t(const WinDims& D, const WinFwdArgs& a, cudaStream_t st) {
+  F32Params p{};
+  p.q = a.q;
+  p.k = a.k;
+  p.v = a.v;
+  p.h = a.h;
+  p.lse = a.lse;
+  p.Hq = D.Hq;
+  p.g = D.g;
+  p.N = D.N;
+  p.window = D.window;
+  p.sinks = D.sinks;
+  p.NT = (D.N + BT - 1) / BT;
+  p.c = D.scale * kLog2e;
+  auto kern = win_fwd_f32_kernel<HD, false>;
+  cudaError_t e = set_smem(kern, Fwd<HD>::SMEM);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)((int64_t)p.NT * D.B * D.Hq), Fwd<HD>::THREADS, Fwd<HD>::SMEM, st>>>(p);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+template <int HD>
+cudaError_t bwd_t(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
+  cudaError_t e = launch_win_bwd_pre(D, a, st);
+  if (e != cudaSuccess) return e;
+  const WinBwdLayout L = win_bwd_layout(D);
+  const ChunkPlan cp = chunk_plan<BT>(D, kBwdChunks, kMinSteps);
+  char* ws = static_cast<char*>(a.ws);
+  F32Bwd p{};
+  p.q = a.q;
+  p.k = a.k;
+  p.v = a.v;
+  p.g = a.g;
+  p.dq = a.dq;
+  p.dk = a.dk;
+  p.dv = a.dv;
+  p.lse2 = reinterpret_cast<const float*>(ws + L.lse2);
+  p.dsum = reinterpret_cast<const float*>(ws + L.dsum);
+  p.part = reinterpret_cast<float*>(ws + L.part);
+  p.Hq = D.Hq;
+  p.Hkv = D.Hkv;
+  p.grp = D.g;
+  p.N = D.N;
+  p.Npad = L.Npad;
+  p.window = D.window;
+  p.sinks = D.sinks;
+  p.NT = cp.NT;
+  p.L = cp.L;
+  p.partials = cp.partials;
+  p.cut = cp.cut;
+  p.c = D.scale * kLog2e;
+  p.scale = D.scale;
+  auto dkv = win_bwd_dkv_f32_kernel<HD>;
+  if ((e = set_smem(dkv, bwd_smem<HD>())) != cudaSuccess) return e;
+  dkv<<<dim3(cp.chunks * D.Hkv, D.B), BWD_THREADS, bwd_smem<HD>(), st>>>(p);
+  count_launches(1);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_win_kvjoin<BT>(D, a, cp, p.part, st)) != cudaSuccess) return e;
+  auto dq = win_bwd_dq_f32_kernel<HD>;
+  if ((e = set_smem(dq, bwd_smem<HD>())) != cudaSuccess) return e;
+  dq<<<(unsigned)((int64_t)cp.NT * D.B * D.Hq), BWD_THREADS, bwd_smem<HD>(), st>>>(p);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+template <typename T, int HD>
+cudaError_t pre_t(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
+  const WinBwdLayout L = win_bwd_layout(D);
+  char* ws = static_cast<char*>(a.ws);
+  constexpr int per = 8 * 4 * (32 / (HD / Vec16<T>::kN));  // rows of a CTA
+  win_bwd_pre_kernel<T, HD><<<dim3((L.Npad + per - 1) / per, D.B * D.Hq), 256, 0, st>>>(
+      a.h, a.g, a.lse, reinterpret_cast<float*>(ws + L.lse2), reinterpret_cast<float*>(ws + L.dsum), D.Hq, D.N, L.Npad);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+template <typename T, int HD, int BTJ>
+cudaError_t join_t(const WinDims& D, const WinBwdArgs& a, const ChunkPlan& p, const float* part, cudaStream_t st) {
+  win_kvjoin_kernel<T, HD, BTJ><<<dim3(p.cut, D.B * D.Hkv, 8), 256, 0, st>>>(
+      part, a.dk, a.dv, D.Hkv, D.g, D.N, p.L, p.partials, D.window, D.sinks, D.scale);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+template <int HD>
+cudaError_t paged_t(const PagedDims& D, const PagedArgs& a, cudaStream_t st) {
+  F32Params p{};
+  p.q = a.q;
+  p.k = a.k;
+  p.v = a.v;
+  p.h = a.h;
+  p.lse = a.lse;
+  p.Hq = D.Hq;
+  p.g = D.g;
+  p.window = D.window;
+  p.sinks = D.sinks;
+  p.c = D.scale * kLog2e;
+  p.table = a.table;
+  p.page = D.page;
+  p.num_pages = D.num_pages;
+  p.max_pages = D.max_pages;
+  p.T = D.T;
+  const int TI = BT / D.g;
+  p.batch = Batch{a.q_start, a.kv_len, D.seqs, D.T, D.max_pages * D.page, TI, D.window, D.sinks, D.Hkv};
+  p.part = static_cast<float*>(a.ws);
+  auto kern = win_fwd_f32_kernel<HD, true>;
+  cudaError_t e = set_smem(kern, Fwd<HD>::SMEM);
+  if (e != cudaSuccess) return e;
+  kern<<<kPagedCtas, Fwd<HD>::THREADS, Fwd<HD>::SMEM, st>>>(p);
+  count_launches(1);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_paged_join<BT, BT>(D, a, kPagedCtas, TI, kMinUnits, st);
+}
+
+}  // namespace
+
+cudaError_t launch_win_fwd_f32(const WinDims& D, const WinFwdArgs& a, cudaStream_t st) {
+  return D.d == 64 ? fwd_t<64>(D, a, st) : fwd_t<128>(D, a, st);
+}
+cudaError_t launch_win_bwd_pre(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
+  if (D.dtype == SSA_BF16) return D.d == 64 ? pre_t<__nv_bfloat16, 64>(D, a, st) : pre_t<__nv_bfloat16, 128>(D, a, st);
+  return D.d == 64 ? pre_t<float, 64>(D, a, st) : pre_t<float, 128>(D, a, st);
+}
+cudaError_t launch_win_bwd_f32(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
+  return D.d == 64 ? bwd_t<64>(D, a, st) : bwd_t<128>(D, a, st);
+}
+cudaError_t launch_paged_f32(const PagedDims& D, const PagedArgs& a, cudaStream_t st) {
+  return D.d == 64 ? paged_t<64>(D, a, st) : paged_t<128>(D, a, st);
+}
+
+template <int BTJ>
+cudaError_t launch_win_kvjoin(const WinDims& D, const WinBwdArgs& a, const ChunkPlan& p, const float* part,
+                              cudaStream_t st) {
+  if (p.partials == 0) return cudaSuccess;
+  using T = std::conditional_t<BTJ == 128, __nv_bfloat16, float>;  // tiles of 128 tokens are the bf16 kernels'
+  return D.d == 64 ? join_t<T, 64, BTJ>(D, a, p, part, st) : join_t<T, 128, BTJ>(D, a, p, part, st);
+}
+template cudaError_t launch_win_kvjoin<64>(const WinDims&, const WinBwdArgs&, const ChunkPlan&, const float*, cudaStream_t);
+template cudaError_t launch_win_kvjoin<128>(const WinDims&, const WinBwdArgs&, const ChunkPlan&, const float*, cudaStream_t);
+
+WinBwdLayout win_bwd_layout(const WinDims& D) {
+  WinBwdLayout L{};
+  L.Npad = (D.N + 127) / 128 * 128;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t rows = (size_t)D.B * D.Hq * L.Npad;
+  size_t o = 0;
+  L.lse2 = o;
+  o = up(o + rows * 4);
+  L.dsum = o;
+  o = up(o + rows * 4);
+  L.part = o;
+  const int tile = D.dtype == SSA_BF16 ? 128 : BT;
+  const ChunkPlan p = D.dtype == SSA_BF16 ? chunk_plan<128>(D, kBwdChunks, kTcMinSteps) : chunk_plan<BT>(D, kBwdChunks, kMinSteps);
+  o = up(o + (size_t)D.B * D.Hkv * p.partials * 2 * tile * D.d * 4);
+  L.bytes = o;
+  return L;
+}
+
+size_t paged_ws_bytes(const PagedDims& D) {
+  return ((size_t)2 * kPagedCtas * partial_floats(BT, D.d) * 4 + 255) / 256 * 256;
+}
+
+}  // namespace ssa

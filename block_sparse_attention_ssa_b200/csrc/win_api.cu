@@ -111,7 +111,7 @@ ssa_status_t ssa_fwd_window(const ssa_window_dims_t* dims, const ssa_tensor_t* Q
   if ((s = require_sm100()) != SSA_OK) return s;
   a.lse = lse;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (D.dtype == SSA_F32) return from_cuda(launch_win_fwd_simt(D, a, st));
+  if (D.dtype == SSA_F32) return from_cuda(launch_win_fwd_f32(D, a, st));
   int32_t* status = status_word();
   if (status == nullptr) return SSA_ERR_CUDA;
   return from_cuda(launch_win_fwd_tc(D, a, status, st));
@@ -142,7 +142,7 @@ ssa_status_t ssa_bwd_window(const ssa_window_dims_t* dims, const ssa_tensor_t* Q
   a.lse = lse;
   a.ws = ws;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (D.dtype == SSA_F32) return from_cuda(launch_win_bwd_simt(D, a, st));
+  if (D.dtype == SSA_F32) return from_cuda(launch_win_bwd_f32(D, a, st));
   int32_t* status = status_word();
   if (status == nullptr) return SSA_ERR_CUDA;
   return from_cuda(launch_win_bwd_tc(D, a, status, st));
@@ -203,7 +203,7 @@ ssa_status_t ssa_paged_attention(const ssa_paged_dims_t* dims, const ssa_tensor_
   a.lse = lse;
   a.ws = ws;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (D.dtype == SSA_F32) return from_cuda(launch_paged_simt(D, a, st));
+  if (D.dtype == SSA_F32) return from_cuda(launch_paged_f32(D, a, st));
   int32_t* status = status_word();
   if (status == nullptr) return SSA_ERR_CUDA;
   return from_cuda(launch_paged_tc(D, a, status, st));

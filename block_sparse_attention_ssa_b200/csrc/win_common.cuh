@@ -279,7 +279,7 @@ __device__ __forceinline__ Chunk find_chunk(int ci, int cut, int L, int g, int N
 }
 
 // ---------------------------------------------------------------- launchers
-cudaError_t launch_win_fwd_simt(const WinDims& D, const WinFwdArgs& a, cudaStream_t st);
+cudaError_t launch_win_fwd_f32(const WinDims& D, const WinFwdArgs& a, cudaStream_t st);
 
 // Workspace of the backward: -lse (base 2) and -D_t in rows padded to 128 tokens, then partials.
 struct WinBwdLayout {
@@ -289,7 +289,7 @@ struct WinBwdLayout {
 WinBwdLayout win_bwd_layout(const WinDims& D);
 // Fills lse2 (-infinity in padding rows) and dsum.
 cudaError_t launch_win_bwd_pre(const WinDims& D, const WinBwdArgs& a, cudaStream_t st);
-cudaError_t launch_win_bwd_simt(const WinDims& D, const WinBwdArgs& a, cudaStream_t st);
+cudaError_t launch_win_bwd_f32(const WinDims& D, const WinBwdArgs& a, cudaStream_t st);
 // Adds the chunks' partials of key tiles of BT tokens into dK, dV.
 template <int BT>
 cudaError_t launch_win_kvjoin(const WinDims& D, const WinBwdArgs& a, const ChunkPlan& p, const float* part,
@@ -297,7 +297,7 @@ cudaError_t launch_win_kvjoin(const WinDims& D, const WinBwdArgs& a, const Chunk
 
 cudaError_t launch_paged_append(const PagedDims& D, const PagedArgs& a, cudaStream_t st);
 size_t paged_ws_bytes(const PagedDims& D);
-cudaError_t launch_paged_simt(const PagedDims& D, const PagedArgs& a, cudaStream_t st);
+cudaError_t launch_paged_f32(const PagedDims& D, const PagedArgs& a, cudaStream_t st);
 // Joins the partials of cut items (ROWS rows of G per token of a run of TI tokens, KT keys per unit).
 template <int KT, int ROWS>
 cudaError_t launch_paged_join(const PagedDims& D, const PagedArgs& a, int ctas, int TI, int min_units, cudaStream_t st);
