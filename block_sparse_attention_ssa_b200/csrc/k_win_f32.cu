@@ -8,7 +8,8 @@
 // a_hi b_hi, fp32 accumulation.  What is left out, a_lo b_lo and the low part's own last
 // bits, is below 2^-21 of the product: nearer than an fp32 dot product of 64 terms needs to
 // be.  On the FMA pipe the same tiles were bound by shared memory (a 4 x 4 thread tile reads
-// twice what the pipe can take): 178 against FIXME us for the training step below.
+// twice what the pipe can take): 178 against 128 us for a training
+// step of 8 heads, 1000 tokens, d = 128, window 128.
 //
 // Tiles: 64 queries by 64 keys, a warp 16 rows by all columns, so that a row's statistics
 // need no exchange between warps and the weights go from the accumulators of one product to
@@ -73,22 +74,27 @@ __device__ __forceinline__ Pair split(float x) {
 
 __device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// c += a b to fp32 accuracy, the small terms first.
-__device__ __forceinline__ void mma_pairs(float (&c)[4], const Pair (&a)[4], const Pair (&b)[2]) {
-  mma_tf32(c, a[0].lo, a[1].lo, a[2].lo, a[3].lo, b[0].hi, b[1].hi);
-  mma_tf32(c, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[0].lo, b[1].lo);
-  mma_tf32(c, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[0].hi, b[1].hi);
+// c[n] += a b[n] to fp32 accuracy, the small terms first; the accumulators in turn, so that no product waits for
+// the one before.
+template <int N>
+__device__ __forceinline__ void mma_pairs(float (*c)[4], const Pair (&a)[4], const Pair (&b)[N][2]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) mma_tf32(c[n], a[0].lo, a[1].lo, a[2].lo, a[3].lo, b[n][0].hi, b[n][1].hi);
+#pragma unroll
+  for (int n = 0; n < N; ++n) mma_tf32(c[n], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[n][0].lo, b[n][1].lo);
+#pragma unroll
+  for (int n = 0; n < N; ++n) mma_tf32(c[n], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[n][0].hi, b[n][1].hi);
 }
 
 // c[n] = (16 rows of A) . (rows 8 n .. 8 n + 7 of B) over HD; A: row g of the warp's sixteen at A + g PA.
 template <int HD, int NT, int PA, int PB>
-__device__ __forceinline__ void logits(float (&c)[NT][4], const float* A, const float* B, int g, int t) {
+__device__ __forceinline__ void logits(float (*c)[4], const float* A, const float* B, int g, int t) {
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -99,27 +105,42 @@ __device__ __forceinline__ void logits(float (&c)[NT][4], const float* A, const 
     const float2 y = *reinterpret_cast<const float2*>(A + (g + 8) * PA + k + 2 * t);
     const Pair a[4] = {split(x.x), split(y.x), split(x.y), split(y.y)};
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const float2 z = *reinterpret_cast<const float2*>(B + (8 * n + g) * PB + k + 2 * t);
-      const Pair b[2] = {split(z.x), split(z.y)};
-      mma_pairs(c[n], a, b);
+    for (int n0 = 0; n0 < NT; n0 += 4) {
+      Pair b[4][2];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const float2 z = *reinterpret_cast<const float2*>(B + (8 * (n0 + n) + g) * PB + k + 2 * t);
+        b[n][0] = split(z.x);
+        b[n][1] = split(z.y);
+      }
+      mma_pairs<4>(c + n0, a, b);
     }
   }
 }
 
 // acc[n] += W X for the weights W (16 x 8 KT, accumulator layout) and the rows of X, columns 8 n ...
 template <int HD, int KT, int PX>
-__device__ __forceinline__ void weighted(float (&acc)[HD / 8][4], const float (&w)[KT][4], const float* X, int g, int t) {
+__device__ __forceinline__ void weighted(float (&acc)[HD / 8][4], const float (*w)[4], const float* X, int g, int t) {
 #pragma unroll
   for (int k = 0; k < KT; ++k) {
     const Pair a[4] = {split(w[k][0]), split(w[k][2]), split(w[k][1]), split(w[k][3])};
     const float* r0 = X + (8 * k + 2 * t) * PX + g;
 #pragma unroll
-    for (int n = 0; n < HD / 8; ++n) {
-      const Pair b[2] = {split(r0[8 * n]), split(r0[PX + 8 * n])};
-      mma_pairs(acc[n], a, b);
+    for (int n0 = 0; n0 < HD / 8; n0 += 4) {
+      Pair b[4][2];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        b[n][0] = split(r0[8 * (n0 + n)]);
+        b[n][1] = split(r0[PX + 8 * (n0 + n)]);
+      }
+      mma_pairs<4>(acc + n0, a, b);
     }
   }
+}
+
+// Whether a query at positions t0 .. t1 sees a key of u0 .. u0 + 31: warps leave out the others.
+__device__ __forceinline__ bool any_sees(int t0, int t1, int u0, int window, int sinks) {
+  return u0 <= t1 && (u0 + 31 > t0 - window || u0 < sinks);
 }
 
 // ---------------------------------------------------------------- shared memory
@@ -232,6 +253,7 @@ __global__ void __launch_bounds__(Fwd<HD>::THREADS, 1) win_fwd_f32_kernel(F32Par
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
     const int pmax = p0 + tok_of(nrows - 1), lo_min = p0 - p.window + 1;
+    const int w0 = p0 + tok_of(16 * warp), w1 = p0 + tok_of(min(16 * warp + 15, nrows - 1));  // the warp's positions
 
     const int end = min(at.off + take, kt.count);
     copies_done();
@@ -259,7 +281,19 @@ __global__ void __launch_bounds__(Fwd<HD>::THREADS, 1) win_fwd_f32_kernel(F32Par
       copies_done();
       group_sync(grp);
       float x[8][4];
-      logits<HD, 8, PA, PA>(x, sQ + 16 * warp * PA, sX, g, t);
+      bool some[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        some[c] = any_sees(w0, w1, u0 + 32 * c, p.window, p.sinks);
+        if (some[c]) {
+          logits<HD, 4, PA, PA>(x + 4 * c, sQ + 16 * warp * PA, sX + 32 * c * PA, g, t);
+        } else {
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[4 * c + n][e] = 0.f;  // masked below
+        }
+      }
       group_sync(grp);  // K is read
       copy_rows<HD, PD>(sX, p.q.p, tid, GROUP, keys(p.v));
 #pragma unroll
@@ -295,7 +329,9 @@ __global__ void __launch_bounds__(Fwd<HD>::THREADS, 1) win_fwd_f32_kernel(F32Par
       }
       copies_done();
       group_sync(grp);
-      weighted<HD, 8, PD>(acc, x, sX, g, t);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (some[c]) weighted<HD, 4, PD>(acc, x + 4 * c, sX + 32 * c * PD, g, t);
       group_sync(grp);  // V is read
     }
 
@@ -517,6 +553,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dq_f32_kernel(F32Bwd p
 #pragma unroll 1
     for (int c0 = 0; c0 < BT; c0 += 32) {
       float x[4][4], y[4][4];
+      if (!any_sees(q0 + 16 * warp, q0 + 16 * warp + 15, u0 + c0, p.window, p.sinks)) continue;
       logits<HD, 4, PA, PD>(x, sQ + 16 * warp * PA, sK + c0 * PD, g, t);
       logits<HD, 4, PA, PA>(y, sG + 16 * warp * PA, sV + c0 * PA, g, t);
 #pragma unroll
@@ -582,6 +619,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dkv_f32_kernel(F32Bwd 
 #pragma unroll 1
     for (int c0 = 0; c0 < BT; c0 += 32) {
       float x[4][4], y[4][4];
+      const int k0 = u0 + 16 * warp, t0 = q0 + c0;  // 16 keys, 32 queries
+      if (k0 > t0 + 31 || (k0 + 15 <= t0 - p.window && k0 >= p.sinks)) continue;
       logits<HD, 4, PA, PD>(x, sK + 16 * warp * PA, sQ + c0 * PD, g, t);
       logits<HD, 4, PA, PD>(y, sV + 16 * warp * PA, sG + c0 * PD, g, t);
 #pragma unroll
