@@ -8,7 +8,7 @@
 // a_hi b_hi, fp32 accumulation.  What is left out, a_lo b_lo and the low part's own last
 // bits, is below 2^-21 of the product: nearer than an fp32 dot product of 64 terms needs to
 // be.  On the FMA pipe the same tiles were bound by shared memory (a 4 x 4 thread tile reads
-// twice what the pipe can take): 178 against 128 us for a training
+// twice what the pipe can take): 178 against 142 us for a training
 // step of 8 heads, 1000 tokens, d = 128, window 128.
 //
 // Tiles: 64 queries by 64 keys, a warp 16 rows by all columns, so that a row's statistics
@@ -80,60 +80,87 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// c[n] += a b[n] to fp32 accuracy, the small terms first; the accumulators in turn, so that no product waits for
-// the one before.
+// c[n] += a b[n] over 16 terms to fp32 accuracy, the small terms first; the accumulators in turn, so that no
+// product waits for the one before.  The tensor core cuts off what it adds to its accumulator, so sixteen terms are
+// summed there and added here, rounded: running sums in the tensor core left a training step's gradients 2e-6 off
+// (norms), this leaves 3e-7 to 6e-7.
 template <int N>
-__device__ __forceinline__ void mma_pairs(float (*c)[4], const Pair (&a)[4], const Pair (&b)[N][2]) {
+__device__ __forceinline__ void mma_pairs(float (*c)[4], const Pair (&a)[2][4], const Pair (&b)[2][N][2]) {
+  float s[N][4];
 #pragma unroll
-  for (int n = 0; n < N; ++n) mma_tf32(c[n], a[0].lo, a[1].lo, a[2].lo, a[3].lo, b[n][0].hi, b[n][1].hi);
+  for (int n = 0; n < N; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
 #pragma unroll
-  for (int n = 0; n < N; ++n) mma_tf32(c[n], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[n][0].lo, b[n][1].lo);
+  for (int k = 0; k < 2; ++k)
 #pragma unroll
-  for (int n = 0; n < N; ++n) mma_tf32(c[n], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[n][0].hi, b[n][1].hi);
+    for (int n = 0; n < N; ++n) mma_tf32(s[n], a[k][0].lo, a[k][1].lo, a[k][2].lo, a[k][3].lo, b[k][n][0].hi, b[k][n][1].hi);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int n = 0; n < N; ++n) mma_tf32(s[n], a[k][0].hi, a[k][1].hi, a[k][2].hi, a[k][3].hi, b[k][n][0].lo, b[k][n][1].lo);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int n = 0; n < N; ++n) mma_tf32(s[n], a[k][0].hi, a[k][1].hi, a[k][2].hi, a[k][3].hi, b[k][n][0].hi, b[k][n][1].hi);
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[n][i] += s[n][i];
 }
 
-// c[n] = (16 rows of A) . (rows 8 n .. 8 n + 7 of B) over HD; A: row g of the warp's sixteen at A + g PA.
-template <int HD, int NT, int PA, int PB>
+// c[n] = (16 rows of A) . (rows 8 n .. 8 n + 7 of B) over HD, n < 4; A: row g of the warp's sixteen at A + g PA.
+template <int HD, int PA, int PB>
 __device__ __forceinline__ void logits(float (*c)[4], const float* A, const float* B, int g, int t) {
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int n = 0; n < 4; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[n][i] = 0.f;
-#pragma unroll 2
-  for (int k = 0; k < HD; k += 8) {
-    const float2 x = *reinterpret_cast<const float2*>(A + g * PA + k + 2 * t);
-    const float2 y = *reinterpret_cast<const float2*>(A + (g + 8) * PA + k + 2 * t);
-    const Pair a[4] = {split(x.x), split(y.x), split(x.y), split(y.y)};
+#pragma unroll 1
+  for (int k0 = 0; k0 < HD; k0 += 16) {
+    Pair a[2][4], b[2][4][2];
 #pragma unroll
-    for (int n0 = 0; n0 < NT; n0 += 4) {
-      Pair b[4][2];
+    for (int k = 0; k < 2; ++k) {
+      const float2 x = *reinterpret_cast<const float2*>(A + g * PA + k0 + 8 * k + 2 * t);
+      const float2 y = *reinterpret_cast<const float2*>(A + (g + 8) * PA + k0 + 8 * k + 2 * t);
+      a[k][0] = split(x.x);
+      a[k][1] = split(y.x);
+      a[k][2] = split(x.y);
+      a[k][3] = split(y.y);
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        const float2 z = *reinterpret_cast<const float2*>(B + (8 * (n0 + n) + g) * PB + k + 2 * t);
-        b[n][0] = split(z.x);
-        b[n][1] = split(z.y);
+        const float2 z = *reinterpret_cast<const float2*>(B + (8 * n + g) * PB + k0 + 8 * k + 2 * t);
+        b[k][n][0] = split(z.x);
+        b[k][n][1] = split(z.y);
       }
-      mma_pairs<4>(c + n0, a, b);
     }
+    mma_pairs<4>(c, a, b);
   }
 }
 
-// acc[n] += W X for the weights W (16 x 8 KT, accumulator layout) and the rows of X, columns 8 n ...
-template <int HD, int KT, int PX>
+// acc[n] += W X for the weights W (16 x 32, accumulator layout) and 32 rows of X, columns 8 n ...
+template <int HD, int PX>
 __device__ __forceinline__ void weighted(float (&acc)[HD / 8][4], const float (*w)[4], const float* X, int g, int t) {
 #pragma unroll
-  for (int k = 0; k < KT; ++k) {
-    const Pair a[4] = {split(w[k][0]), split(w[k][2]), split(w[k][1]), split(w[k][3])};
-    const float* r0 = X + (8 * k + 2 * t) * PX + g;
+  for (int k0 = 0; k0 < 4; k0 += 2) {
+    Pair a[2][4];
 #pragma unroll
-    for (int n0 = 0; n0 < HD / 8; n0 += 4) {
-      Pair b[4][2];
+    for (int k = 0; k < 2; ++k) {
+      a[k][0] = split(w[k0 + k][0]);
+      a[k][1] = split(w[k0 + k][2]);
+      a[k][2] = split(w[k0 + k][1]);
+      a[k][3] = split(w[k0 + k][3]);
+    }
+    const float* r0 = X + (8 * k0 + 2 * t) * PX + g;
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        b[n][0] = split(r0[8 * (n0 + n)]);
-        b[n][1] = split(r0[PX + 8 * (n0 + n)]);
-      }
-      mma_pairs<4>(acc + n0, a, b);
+    for (int n0 = 0; n0 < HD / 8; n0 += 2) {
+      Pair b[2][2][2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          b[k][n][0] = split(r0[8 * k * PX + 8 * (n0 + n)]);
+          b[k][n][1] = split(r0[(8 * k + 1) * PX + 8 * (n0 + n)]);
+        }
+      mma_pairs<2>(acc + n0, a, b);
     }
   }
 }
@@ -286,7 +313,7 @@ __global__ void __launch_bounds__(Fwd<HD>::THREADS, 1) win_fwd_f32_kernel(F32Par
       for (int c = 0; c < 2; ++c) {
         some[c] = any_sees(w0, w1, u0 + 32 * c, p.window, p.sinks);
         if (some[c]) {
-          logits<HD, 4, PA, PA>(x + 4 * c, sQ + 16 * warp * PA, sX + 32 * c * PA, g, t);
+          logits<HD, PA, PA>(x + 4 * c, sQ + 16 * warp * PA, sX + 32 * c * PA, g, t);
         } else {
 #pragma unroll
           for (int n = 0; n < 4; ++n)
@@ -331,7 +358,7 @@ __global__ void __launch_bounds__(Fwd<HD>::THREADS, 1) win_fwd_f32_kernel(F32Par
       group_sync(grp);
 #pragma unroll
       for (int c = 0; c < 2; ++c)
-        if (some[c]) weighted<HD, 4, PD>(acc, x + 4 * c, sX + 32 * c * PD, g, t);
+        if (some[c]) weighted<HD, PD>(acc, x + 4 * c, sX + 32 * c * PD, g, t);
       group_sync(grp);  // V is read
     }
 
@@ -554,8 +581,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dq_f32_kernel(F32Bwd p
     for (int c0 = 0; c0 < BT; c0 += 32) {
       float x[4][4], y[4][4];
       if (!any_sees(q0 + 16 * warp, q0 + 16 * warp + 15, u0 + c0, p.window, p.sinks)) continue;
-      logits<HD, 4, PA, PD>(x, sQ + 16 * warp * PA, sK + c0 * PD, g, t);
-      logits<HD, 4, PA, PA>(y, sG + 16 * warp * PA, sV + c0 * PA, g, t);
+      logits<HD, PA, PD>(x, sQ + 16 * warp * PA, sK + c0 * PD, g, t);
+      logits<HD, PA, PA>(y, sG + 16 * warp * PA, sV + c0 * PA, g, t);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t vis = visible_keys(q0 + r0 + 8 * i, u0 + c0, p.window, p.sinks) >> (2 * t);
@@ -567,7 +594,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dq_f32_kernel(F32Bwd p
             x[n][k] = keep(vis, 8 * n + e, exp2f(fmaf(x[n][k], p.c, nl[i])) * (y[n][k] + nd[i]), 0.f);
           }
       }
-      weighted<HD, 4, PD>(acc, x, sK + c0 * PD, g, t);
+      weighted<HD, PD>(acc, x, sK + c0 * PD, g, t);
     }
     group_sync(grp);  // K and V are read
   }
@@ -621,8 +648,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dkv_f32_kernel(F32Bwd 
       float x[4][4], y[4][4];
       const int k0 = u0 + 16 * warp, t0 = q0 + c0;  // 16 keys, 32 queries
       if (k0 > t0 + 31 || (k0 + 15 <= t0 - p.window && k0 >= p.sinks)) continue;
-      logits<HD, 4, PA, PD>(x, sK + 16 * warp * PA, sQ + c0 * PD, g, t);
-      logits<HD, 4, PA, PD>(y, sV + 16 * warp * PA, sG + c0 * PD, g, t);
+      logits<HD, PA, PD>(x, sK + 16 * warp * PA, sQ + c0 * PD, g, t);
+      logits<HD, PA, PD>(y, sV + 16 * warp * PA, sG + c0 * PD, g, t);
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         const float2 l2 = *reinterpret_cast<const float2*>(nl + c0 + 8 * n), d2 = *reinterpret_cast<const float2*>(nd + c0 + 8 * n);
@@ -638,8 +665,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dkv_f32_kernel(F32Bwd 
           }
         }
       }
-      weighted<HD, 4, PD>(dv, x, sG + c0 * PD, g, t);
-      weighted<HD, 4, PD>(dk, y, sQ + c0 * PD, g, t);
+      weighted<HD, PD>(dv, x, sG + c0 * PD, g, t);
+      weighted<HD, PD>(dk, y, sQ + c0 * PD, g, t);
     }
     group_sync(grp);  // Q and g are read
   }
