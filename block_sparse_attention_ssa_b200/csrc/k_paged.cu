@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, Batch batc
   }
   __syncthreads();
   // Every CTA waits, those without work too: what follows in the stream waits for this kernel alone.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  ahead_wait();
   const Place at = sh;
   if (at.b >= batch.seqs) return;
   const long long u0 = sh_unit[0], u1 = sh_unit[1], per = sh_unit[2];
@@ -146,23 +146,11 @@ cudaError_t launch_paged_append(const PagedDims& D, const PagedArgs& a, cudaStre
 template <int KT, int ROWS>
 cudaError_t launch_paged_join(const PagedDims& D, const PagedArgs& a, int ctas, int TI, int min_units, cudaStream_t st) {
   const Batch batch{a.q_start, a.kv_len, D.seqs, D.T, D.max_pages * D.page, TI, D.window, D.sinks, D.Hkv};
-  // Programmatic launch: the kernel's start (its launch and the search of its item) overlaps the attention
-  // kernel's last CTAs; it waits for that kernel before it reads a partial.
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, 4);
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  // The launch and the search of the items overlap the attention kernel's last CTAs.
   using T = std::conditional_t<KT == 128, __nv_bfloat16, float>;  // units of 128 keys are the bf16 kernel's
-  const cudaError_t e = D.d == 64
-      ? cudaLaunchKernelEx(&cfg, paged_join_kernel<T, 64, KT, ROWS>, a, batch, D.T, D.g, ctas, min_units)
-      : cudaLaunchKernelEx(&cfg, paged_join_kernel<T, 128, KT, ROWS>, a, batch, D.T, D.g, ctas, min_units);
-  count_launches(1);
-  return e;
+  const dim3 grid(ctas, 4);
+  return D.d == 64 ? launch_ahead(paged_join_kernel<T, 64, KT, ROWS>, grid, 256, 0, st, a, batch, D.T, D.g, ctas, min_units)
+                   : launch_ahead(paged_join_kernel<T, 128, KT, ROWS>, grid, 256, 0, st, a, batch, D.T, D.g, ctas, min_units);
 }
 template cudaError_t launch_paged_join<128, 256>(const PagedDims&, const PagedArgs&, int, int, int, cudaStream_t);
 template cudaError_t launch_paged_join<64, 64>(const PagedDims&, const PagedArgs&, int, int, int, cudaStream_t);

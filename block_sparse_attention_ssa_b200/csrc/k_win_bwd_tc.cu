@@ -163,6 +163,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  allow_ahead();
+  ahead_wait();
   const uint32_t tmem = M.tmem_base;
   const uint32_t cK = tmem, cV = tmem + HD, cS = tmem + 256, cP = tmem + 384;
   uint8_t* sK = smem;
@@ -432,6 +434,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  ahead_wait();
   const uint32_t tmem = M.tmem_base;
   const uint32_t cQ = tmem, cS = tmem + 128, cP = tmem + 384;
   uint8_t* sQ = smem;
@@ -685,16 +688,12 @@ cudaError_t launch(const WinDims& D, const WinBwdArgs& a, int32_t* status, cudaS
   p.wide_kv = wide_rows(a.dk) && wide_rows(a.dv);
   auto dkv = win_bwd_dkv_tc_kernel<HD>;
   if ((e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, dkv_smem<HD>())) != cudaSuccess) return e;
-  dkv<<<dim3(cp.chunks * D.Hkv, D.B), NTHREADS, dkv_smem<HD>(), st>>>(qu, k, v, gu, p);
-  count_launches(1);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_ahead(dkv, dim3(cp.chunks * D.Hkv, D.B), NTHREADS, dkv_smem<HD>(), st, qu, k, v, gu, p)) != cudaSuccess) return e;
   if ((e = launch_win_kvjoin<TILE>(D, a, cp, p.part, st)) != cudaSuccess) return e;
   auto dq = win_bwd_dq_tc_kernel<HD>;
   if ((e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, dq_smem<HD>())) != cudaSuccess) return e;
   const int64_t items = (int64_t)D.B * D.Hq * cp.NT;
-  dq<<<(unsigned)(items < kCtas ? items : kCtas), NTHREADS, dq_smem<HD>(), st>>>(q, k, v, g, p);
-  count_launches(1);
-  return cudaGetLastError();
+  return launch_ahead(dq, dim3((unsigned)(items < kCtas ? items : kCtas)), NTHREADS, dq_smem<HD>(), st, q, k, v, g, p);
 }
 
 }  // namespace

@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(Fwd<HD>::THREADS, 1) win_fwd_f32_kernel(F32Par
       }
     }
     __syncthreads();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be brought up
+    allow_ahead();  // the join
     at = sh_place;
     left = sh_left;
   }
@@ -452,6 +452,7 @@ __global__ void __launch_bounds__(256) win_bwd_pre_kernel(TensorRef h, TensorRef
   const int lane = threadIdx.x & 31, c = lane % LPR * V;
   const int bh = blockIdx.y, b = bh / Hq, hd = bh % Hq;
   const int t0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * (RPW * U) + lane / LPR;
+  allow_ahead();
   uint4 x[U], y[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
@@ -555,6 +556,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dq_f32_kernel(F32Bwd p
   };
   copy_rows<HD, PA>(sQ, p.q.p, threadIdx.x, BWD_THREADS, query(p.q));
   copy_rows<HD, PA>(sG, p.q.p, threadIdx.x, BWD_THREADS, query(p.g));
+  allow_ahead();
+  ahead_wait();
   float nl[2], nd[2], acc[HD / 8][4];  // -lse2, -D
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -625,6 +628,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dkv_f32_kernel(F32Bwd 
   };
   copy_rows<HD, PA>(sK, p.q.p, threadIdx.x, BWD_THREADS, key(p.k));
   copy_rows<HD, PA>(sV, p.q.p, threadIdx.x, BWD_THREADS, key(p.v));
+  allow_ahead();
+  ahead_wait();
   float dk[HD / 8][4], dv[HD / 8][4];
 #pragma unroll
   for (int n = 0; n < HD / 8; ++n)
@@ -698,6 +703,8 @@ __global__ void __launch_bounds__(256)
     return (int)(((long long)query_tiles_of<BTJ>(k, N, window, sinks) * grp + L - 1) / L);
   };
   const int n = chunks_of(kt);
+  allow_ahead();
+  ahead_wait();
   if (n == 1) return;
   __shared__ int slot_sh;
   if (threadIdx.x < 32) {
@@ -799,15 +806,11 @@ cudaError_t bwd_t(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
   p.scale = D.scale;
   auto dkv = win_bwd_dkv_f32_kernel<HD>;
   if ((e = set_smem(dkv, bwd_smem<HD>())) != cudaSuccess) return e;
-  dkv<<<dim3(cp.chunks * D.Hkv, D.B), BWD_THREADS, bwd_smem<HD>(), st>>>(p);
-  count_launches(1);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_ahead(dkv, dim3(cp.chunks * D.Hkv, D.B), BWD_THREADS, bwd_smem<HD>(), st, p)) != cudaSuccess) return e;
   if ((e = launch_win_kvjoin<BT>(D, a, cp, p.part, st)) != cudaSuccess) return e;
   auto dq = win_bwd_dq_f32_kernel<HD>;
   if ((e = set_smem(dq, bwd_smem<HD>())) != cudaSuccess) return e;
-  dq<<<(unsigned)((int64_t)cp.NT * D.B * D.Hq), BWD_THREADS, bwd_smem<HD>(), st>>>(p);
-  count_launches(1);
-  return cudaGetLastError();
+  return launch_ahead(dq, dim3((unsigned)((int64_t)cp.NT * D.B * D.Hq)), BWD_THREADS, bwd_smem<HD>(), st, p);
 }
 
 template <typename T, int HD>
@@ -823,10 +826,8 @@ cudaError_t pre_t(const WinDims& D, const WinBwdArgs& a, cudaStream_t st) {
 
 template <typename T, int HD, int BTJ>
 cudaError_t join_t(const WinDims& D, const WinBwdArgs& a, const ChunkPlan& p, const float* part, cudaStream_t st) {
-  win_kvjoin_kernel<T, HD, BTJ><<<dim3(p.cut, D.B * D.Hkv, 8), 256, 0, st>>>(
-      part, a.dk, a.dv, D.Hkv, D.g, D.N, p.L, p.partials, D.window, D.sinks, D.scale);
-  count_launches(1);
-  return cudaGetLastError();
+  return launch_ahead(win_kvjoin_kernel<T, HD, BTJ>, dim3(p.cut, D.B * D.Hkv, 8), 256, 0, st, part, a.dk, a.dv, D.Hkv, D.g,
+                      D.N, p.L, p.partials, D.window, D.sinks, D.scale);
 }
 
 template <int HD>

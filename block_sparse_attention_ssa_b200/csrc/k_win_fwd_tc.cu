@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (PAGED) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be brought up
+  if (PAGED) allow_ahead();  // the join
   const uint32_t tmem = M.tmem_base;
   uint8_t* sQ = smem;
   uint8_t* sK = smem + C::OFF_K;

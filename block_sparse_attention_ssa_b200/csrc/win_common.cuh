@@ -42,6 +42,29 @@ struct PagedArgs {
   void* ws;
 };
 
+// ---------------------------------------------------------------- kernels launched ahead
+// A kernel launched by launch_ahead() may be brought up while the kernel before it in the stream still runs; every
+// one of its threads calls ahead_wait() before it touches what that kernel wrote (and before it ends: what follows
+// in the stream waits for the last kernel alone).  allow_ahead() in the kernel before says when.
+__device__ __forceinline__ void ahead_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void allow_ahead() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+inline cudaError_t launch_ahead(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, A&&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  count_launches(1);
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 // ---------------------------------------------------------------- key tiles of a run of queries
 // The tiles of KT keys that queries at positions pmin..pmax see: the sink tiles
 // 0..ns-1, then tiles lo..hi of the window (sink tiles that the window reaches
