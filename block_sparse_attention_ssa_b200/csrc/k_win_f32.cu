@@ -556,7 +556,6 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dq_f32_kernel(F32Bwd p
   };
   copy_rows<HD, PA>(sQ, p.q.p, threadIdx.x, BWD_THREADS, query(p.q));
   copy_rows<HD, PA>(sG, p.q.p, threadIdx.x, BWD_THREADS, query(p.g));
-  allow_ahead();
   ahead_wait();
   float nl[2], nd[2], acc[HD / 8][4];  // -lse2, -D
 #pragma unroll

@@ -45,7 +45,7 @@ ssa_status_t check_paged(const ssa_paged_dims_t* in, PagedDims* out, bool* empty
   if (D.d != 64 && D.d != 128) return SSA_ERR_UNSUPPORTED;
   if (D.page != 16 && D.page != 32 && D.page != 64 && D.page != 128 && D.page != 256) return SSA_ERR_UNSUPPORTED;
   D.g = D.Hq / D.Hkv;
-  if (D.g > 64 || D.T > kMaxPositions || D.seqs > kMaxPositions || (int64_t)D.max_pages * D.page > kMaxPositions)
+  if (D.g > 64 || D.Hq > 65535 || D.T > kMaxPositions || D.seqs > kMaxPositions || (int64_t)D.max_pages * D.page > kMaxPositions)
     return SSA_ERR_UNSUPPORTED;
   *empty = D.seqs == 0 || D.T == 0 || D.Hq == 0;
   // positions stay below 2^30, so nothing lies behind a longer window or past more sinks

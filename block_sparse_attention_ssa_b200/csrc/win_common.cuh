@@ -248,7 +248,8 @@ inline ChunkPlan chunk_plan(const WinDims& D, int ctas, int min_steps) {
   for (int kt = 0; kt < p.NT; ++kt) steps += (long long)query_tiles_of<BT>(kt, D.N, D.window, D.sinks) * D.g;
   const long long all = steps * D.B * D.Hkv;
   const long long even = (all + ctas - 1) / ctas;
-  p.L = (int)(even < min_steps ? min_steps : even);
+  // the longest shapes that the size function answers for have more steps than an int holds
+  p.L = (int)(even < min_steps ? min_steps : (even < (1 << 30) ? even : 1 << 30));
   for (int kt = 0; kt < p.NT; ++kt) {
     const int n = (int)(((long long)query_tiles_of<BT>(kt, D.N, D.window, D.sinks) * D.g + p.L - 1) / p.L);
     p.chunks += n;

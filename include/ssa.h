@@ -370,7 +370,7 @@ SSA_API ssa_status_t ssa_block_scores_noalloc(const ssa_dims_t* dims, const ssa_
  * of the sequence.  window >= N is causal attention over everything.  Nothing
  * is selected, so N needs no block: any N >= 0, odd ones too. */
 typedef struct {
-  int32_t B, Hq, Hkv, N, d; /* Hq % Hkv == 0, d in {64, 128}, 0 <= N <= 2^24 */
+  int32_t B, Hq, Hkv, N, d; /* Hq % Hkv == 0, B * Hq <= 65535, d in {64, 128}, 0 <= N <= 2^24 */
   int32_t window;           /* >= 1 */
   int32_t sinks;            /* >= 0 */
   float scale;              /* finite, > 0 */
@@ -391,7 +391,8 @@ SSA_API size_t ssa_window_workspace_bytes(const ssa_window_dims_t* dims);
  *     row of token u may also reach tokens that do not see u but share a tile
  *     with one that does (a weight of zero times it): up to 127 positions
  *     before u, or behind the end of u's window.  The same holds for the
- *     gradients and NaN or infinities in Q, K, g. */
+ *     gradients and NaN or infinities in Q, K, g.  In fp32 magnitudes from
+ *     3.4019e38 on (where rounding to TF32 overflows) count as infinities. */
 SSA_API ssa_status_t ssa_fwd_window(const ssa_window_dims_t* dims, const ssa_tensor_t* Q, const ssa_tensor_t* K,
                                     const ssa_tensor_t* V, const ssa_tensor_t* h, float* lse,
                                     ssa_stream_t stream);
@@ -435,7 +436,7 @@ SSA_API ssa_status_t ssa_bwd_window(const ssa_window_dims_t* dims, const ssa_ten
 typedef struct {
   int32_t num_seqs;  /* >= 0 */
   int32_t total_q;   /* rows of the packed tensors, 0 .. 2^30 */
-  int32_t Hq, Hkv, d; /* Hq % Hkv == 0, Hq / Hkv <= 64, d in {64, 128} */
+  int32_t Hq, Hkv, d; /* Hq % Hkv == 0, Hq <= 65535, Hq / Hkv <= 64, d in {64, 128} */
   int32_t page;      /* tokens in a page: 16, 32, 64, 128 or 256 */
   int32_t num_pages; /* pages of each cache, >= 1 */
   int32_t max_pages; /* columns of the page table, >= 1; max_pages * page <= 2^30 */

@@ -234,6 +234,36 @@ def test_captured_decoding_follows_the_lengths(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_shared_pages_and_fused_rows(dtype):
+    """Sequences that begin with the same pages, one page twice in a sequence, and q, k, v as slices of one tensor."""
+    b = Batch([40, 1, 3], [140, 97, 130], 4, 2, 64, 16, dtype)
+    b.table[1, :5] = b.table[0, :5]
+    b.table[2, 3] = b.table[2, 1]
+    qkv = torch.full((b.T, 2 * b.Hq + 4 * b.Hkv, b.d), 7.0, dtype=TYPES[dtype])
+    part = {"q": slice(0, b.Hq), "k": slice(b.Hq, b.Hq + b.Hkv), "v": slice(b.Hq + 2 * b.Hkv, b.Hq + 3 * b.Hkv)}
+    host_q = b.q
+    qkv[:, part["q"]] = host_q
+    # the new tokens' rows, as the cache has them already (none lies in a page that is used twice)
+    for name, c in zip("kv", b.caches):
+        for s in range(3):
+            for r in range(b.q_start[s], b.q_start[s + 1]):
+                u = int(b.kv_len[s] - b.q_start[s + 1]) + r
+                qkv[r, part[name]] = c[b.table[s, u // b.page], u % b.page]
+    qkv = qkv.cuda()
+    caches = [b.device_cache(c) for c in b.caches]
+    before = [c.clone() for c in caches]
+    api.ssa_paged_append(b.dims(), qkv[:, part["k"]], qkv[:, part["v"]], b.q_start.cuda(), b.kv_len.cuda(), b.table.cuda(),
+                         *caches)
+    for x, y in zip(before, caches):
+        assert torch.equal(x.nan_to_num(9.0), y.nan_to_num(9.0))
+    for window, sinks in ((None, 0), (60, 20)):
+        b.q = qkv[:, part["q"]]
+        out = b.attend(window, sinks)
+        b.q = host_q
+        b.check(out, window, sinks)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_two_calls_at_once(dtype):
     """Two batches on two streams, each with its own workspace, many times over."""
     batches = [Batch([1] * 5, [900, 20, 300, 77, 1200], 8, 2, 128, 16, dtype, seed=s) for s in (1, 2)]

@@ -167,6 +167,46 @@ def test_gradient_by_differences(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_two_calls_at_once(dtype):
+    """Training steps of two shapes on two streams, each with its own workspace, many times over; then both in one
+    graph, one after the other over one workspace."""
+    shapes = [(1, 4, 2, 900, 128, 150, 20), (2, 2, 1, 333, 64, 1 << 20, 0)]
+    state = []
+    for i, s in enumerate(shapes):
+        dims, x = api.make_window_dims(*s, dtype), {k: v.cuda() for k, v in _inputs(*s[:5], dtype, i).items()}
+        state.append((dims, x, _run(dims, x), {**api.alloc_window_forward(dims), **api.alloc_window_backward(dims)},
+                      api.alloc_window_workspace(dims)))
+
+    def step(dims, x, out, ws, stream=None):
+        api.ssa_fwd_window(dims, x["Q"], x["K"], x["V"], out["h"], out["lse"], stream=stream)
+        api.ssa_bwd_window(dims, x["Q"], x["K"], x["V"], out["h"], out["lse"], x["g"], out["dQ"], out["dK"], out["dV"], ws,
+                           stream=stream)
+
+    def compare():
+        torch.cuda.synchronize()
+        assert api.ssa_device_status() == api.SSA_OK
+        for _, _, want, out, _ in state:
+            for k in out:
+                assert torch.equal(out[k], want[k]), k
+                out[k].fill_(3.0)
+
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in state]
+    for _ in range(10):
+        for s, (dims, x, _, out, ws) in zip(streams, state):
+            step(dims, x, out, ws, s)
+    compare()
+    shared = max((st[4] for st in state), key=torch.numel)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for dims, x, _, out, _ in state:
+            step(dims, x, out, shared)
+    for _ in range(3):
+        graph.replay()
+    compare()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_same_bits_and_captured(dtype):
     """The same inputs give the same bits, eagerly, on another stream and from a captured graph with new inputs."""
     B, Hq, Hkv, N, d, window, sinks = 1, 4, 2, 1100, 128, 150, 20

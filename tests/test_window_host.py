@@ -132,11 +132,12 @@ def test_paged_bad_dims(lib, field, value):
     assert lib.ssa_paged_workspace_bytes(ctypes.byref(d)) == 0
 
 
-@pytest.mark.parametrize("field,value", [("d", 80), ("page", 8), ("page", 48), ("page", 512), ("Hq", 130),
+@pytest.mark.parametrize("field,value", [("d", 80), ("page", 8), ("page", 48), ("page", 512), ("Hq", 130), ("heads", 65536),
                                          ("max_pages", (1 << 26) + 1), ("total_q", (1 << 30) + 1)])
 def test_paged_unsupported_dims(lib, field, value):
     d = api.make_paged_dims(2, 10, 4, 2, 64, 16, 8, 4)
-    setattr(d, field, value)
+    for name in ("Hq", "Hkv") if field == "heads" else (field,):
+        setattr(d, name, value)
     assert set(_paged_calls(lib, d)) == {api.SSA_ERR_UNSUPPORTED}
 
 
@@ -185,6 +186,19 @@ def test_workspaces(lib):
         assert call(_p(), need - 1) == api.SSA_ERR_WORKSPACE
         assert call(None, need) == api.SSA_ERR_WORKSPACE
         assert call(_p(128), need) == api.SSA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,Hq,Hkv", [(1, 1, 1), (1, 37, 1), (1, 148, 1), (1, 4096, 8), (64, 64, 64)])
+def test_workspace_of_the_longest_sequences(lib, B, Hq, Hkv, dtype):
+    """2^24 tokens, everything visible: -lse and -D, and partials of tiles that are cut, each into chunks of an equal
+    share (a 296th of the steps, 2^30 at most): no more tiles than shares, and a chunk begun for each."""
+    N, d, tile = 1 << 24, 128, 128 if dtype == "bf16" else 64
+    need = api.ssa_window_workspace_bytes(api.make_window_dims(B, Hq, Hkv, N, d, dtype=dtype))
+    rows = 2 * B * Hq * N * 4
+    steps = B * Hq * (N // tile) * (N // tile + 1) // 2
+    partials = 2 * max(296, -(-steps >> 30))
+    assert rows <= need <= rows + partials * 2 * tile * d * 4 + 1024
 
 
 def test_binding_refuses_wrong_tensors():
