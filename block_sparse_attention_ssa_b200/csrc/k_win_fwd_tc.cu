@@ -479,10 +479,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     float* mref = &M.mref[s][row];
     // V rows that no query of the item sees may hold anything (NaN times a zero weight is NaN): zeros in
     // shared memory instead, before this slot's weights go to the product.  Both slots may write them.
-    auto clear_v = [&](const Item& I, int j) {
-      const int u0 = I.tile(j) * TILE, pmax = I.p0 + I.toks - 1, lo_min = I.p0 - p.window + 1;
-      if (u0 + TILE - 1 <= pmax && (u0 >= lo_min || u0 + TILE <= p.sinks)) return;
-      const uint32_t n = base + j;
+    auto clear_v = [&](const Item& I, uint32_t n, int u0) {
+      const int pmax = I.p0 + I.toks - 1, lo_min = I.p0 - p.window + 1;
       if (!mbar_wait(&M.v_full[n % C::NSV], (n / C::NSV) & 1u, abort)) return;  // noticed at the next wait
       uint8_t* sv = sV + (n % C::NSV) * C::TB;
       for (int e = threadIdx.x & 127; e < TILE * (HD / 64) * 8; e += 128) {
@@ -507,14 +505,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       float m = kNegInf, l = 0.f;  // the reference of this thread's sum, and the sum
       bool any = false;            // a tile of this share is the slot's
       for (int j = I.next(0); j < I.T; j = I.next(j + 1)) {
+        // what the step sees is found before its logits are waited for
+        const int u0 = I.tile(j) * TILE + half * UNIT;
+        const bool none = u0 > wmax || (u0 + UNIT - 1 <= wmin - p.window && u0 >= p.sinks);
+        const bool whole = u0 + UNIT - 1 <= wmin && (u0 > wmax - p.window || u0 + UNIT <= p.sinks);
+        const bool clear = PAGED && half == 0 &&
+                           (u0 + TILE - 1 >= I.p0 + I.toks || (u0 <= I.p0 - p.window && u0 + TILE > p.sinks));
         if (!(ok = wait(&M.s_full[s][half], tc))) break;
         tc_fence_after();
-        if (PAGED && half == 0) clear_v(I, j);
+        if (clear) clear_v(I, base + j, u0);
         if (live) {
-          const int u0 = I.tile(j) * TILE + half * UNIT;
           const uint32_t bad = PAGED ? (M.bad[(base + j) & 7] >> (half * 4)) & 15u : 0u;
-          const bool none = u0 > wmax || (u0 + UNIT - 1 <= wmin - p.window && u0 >= p.sinks);
-          const bool all = u0 + UNIT - 1 <= wmin && (u0 > wmax - p.window || u0 + UNIT <= p.sinks) && bad == 0;
+          const bool all = whole && bad == 0;
           // 32 logits at a time stay in registers (96 a thread): the first half of them is read for its
           // maximum and once more for its weights.
           float x[32];
