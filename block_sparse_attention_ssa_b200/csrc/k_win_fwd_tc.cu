@@ -29,6 +29,14 @@
 // (new token, head of the group) pair, so the g heads of a kv head share each K/V load
 // and a single token fills g rows; 128 / g tokens to a slot.  Paged items are cut into
 // equal shares of key tiles (win_common.cuh); cut items leave fp32 partials.
+//
+// Measured (bf16, 32 heads over 8, d = 128).  32768 tokens, window 1024, 64 sinks: 660 us, 870 TFLOP/s of visible pairs
+// (768 on a box under its power cap).  Chunks of 2048 tokens over 14000 more, 4 sequences: 1096 us, 1030 TFLOP/s (1284).
+// Bound by the chain of a step, 3500 cycles for a tile of both slots: logits waited for 1100, loaded for their maximum 350,
+// maximum passed on 570, exponentials 1200, P stored 330; of these the tensor pipe is busy 2560 (45 % over
+// the kernel) and the exponentials' pipe 2048.  Between items 5500 cycles (sums, last product, output), which bounds
+// short windows: 8192 tokens, 32 heads over 2, d = 64, window 256: 76 us, 235 TFLOP/s.  One token of 64
+// sequences over 8000 each: 240 us, 5.5 TB/s, bound by memory.
 #include "win_common.cuh"
 
 #include "sm100_ptx.cuh"
@@ -45,7 +53,6 @@ constexpr int NTHREADS = 640;
 constexpr int WARP_TMA = 16, WARP_MMA = 17, WARP_TMA_V = 19;  // and WARP_MMA + 1 for slot 1
 
 constexpr int kCtas = 148;     // one per SM
-constexpr int kMinUnits = 4;   // key tiles worth a CTA of their own
 constexpr float kRescaleThreshold = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -86,7 +93,7 @@ struct TcParams {
   int32_t* status;
   int B, Hq, g, N, window, sinks;
   int zk, zv, zq;    // broadcast dimensions of K, V, Q: bit 0 batch, bit 1 head
-  int rows_item;     // window form: tokens of an item (256, or 128 when those would leave SMs idle)
+  int rows_item;     // window form: tokens of an item (256, or 128 when those would be fewer than the SMs)
   float c;           // scale * log2(e)
   bool wide;         // h in 32-byte pieces
   // paged form
@@ -261,7 +268,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
   if (PAGED && warp == 0) {
     const long long U = p.batch.total<TILE>();
-    const long long per = share(U, (int)gridDim.x, kMinUnits);
+    const long long per = share(U, (int)gridDim.x);
     const long long u0 = per * blockIdx.x;
     const long long n = u0 < U ? (U - u0 < per ? U - u0 : per) : 0;
     Place at{p.batch.seqs, 0, 0, 0};
@@ -788,6 +795,8 @@ cudaError_t launch_win_fwd_tc(const WinDims& D, const WinFwdArgs& a, int32_t* st
   p.c = D.scale * kLog2e;
   p.wide = wide_rows(a.h);
   const int64_t planes = (int64_t)D.B * D.Hq;
+  // Both slots share key tiles at 256 rows, take them in turn at 128: 167 us against 198 for 32 heads of 8192
+  // tokens (window 1024, d = 128), 13.8 against 9.7 for 8 heads of 1021 (window 200, d = 64), where 256 leaves SMs idle.
   p.rows_item = planes * ((D.N + 255) / 256) >= kCtas ? 256 : 128;
   const int64_t items = planes * ((D.N + p.rows_item - 1) / p.rows_item);
   const int ctas = (int)(items < kCtas ? items : kCtas);
@@ -825,7 +834,7 @@ cudaError_t launch_paged_tc(const PagedDims& D, const PagedArgs& a, int32_t* sta
   p.part = static_cast<float*>(a.ws);
   cudaError_t e = D.d == 64 ? launch<64, true>(q, k, v, p, kCtas, st) : launch<128, true>(q, k, v, p, kCtas, st);
   if (e != cudaSuccess) return e;
-  return launch_paged_join<TILE, 2 * TILE>(D, a, kCtas, 2 * p.TQ, kMinUnits, st);
+  return launch_paged_join<TILE, 2 * TILE>(D, a, kCtas, 2 * p.TQ, st);
 }
 
 }  // namespace ssa

@@ -62,7 +62,9 @@
  *   correct.  No kernel traps.
  * Precision.  dtype SSA_BF16: inputs/outputs bf16, products on tensor cores
  *   with fp32 accumulation and fp32 softmax statistics.  SSA_F32: fp32 inputs
- *   and outputs, fp32 arithmetic throughout (CUDA cores).
+ *   and outputs, fp32 arithmetic throughout (CUDA cores; the window and paged
+ *   calls form each product from pairs of TF32 values on the tensor cores, to
+ *   fp32's accuracy).
  */
 #ifndef SSA_H_
 #define SSA_H_
