@@ -11,8 +11,10 @@
 // twice what the pipe can take): 178 against 142 us for a training
 // step of 8 heads, 1000 tokens, d = 128, window 128.
 // Measured, that step: forward 32 us, dK and dV 66 (288 chunks, two waves of CTAs), dQ 38; chunks of 301 tokens over
-// 3001 more, 5 sequences, 8 heads over 2, d = 64, window 1000: 88 us.  Bound by the rate of the warp-level products; twice the
-// independent accumulators, or pieces twice as wide, changed nothing or spilled (134 against 134 to 144 us).
+// 3001 more, 5 sequences, 8 heads over 2, d = 64, window 1000: 88 us.  Bound by latency: the backward's eight warps an SM
+// issue in 27 to 39 % of the cycles (waits for the instruction before, barriers between warps that see unequal
+// parts of a tile), the tensor pipe is busy 22 to 32 %, and the fullest SM of the step above forms 1.6 times the mean's products.
+// Twice the independent accumulators, or pieces twice as wide, changed nothing or spilled (134 against 134 to 144 us).
 //
 // Tiles: 64 queries by 64 keys, a warp 16 rows by all columns, so that a row's statistics
 // need no exchange between warps and the weights go from the accumulators of one product to
