@@ -73,38 +73,41 @@ __global__ void __launch_bounds__(256) paged_append_kernel(PagedArgs a, PagedDim
 // its launch and search overlapped, one token over 65536 takes 65 us in all, 55 of them in that kernel.
 template <typename T, int HD, int KT, int ROWS>
 __global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, Batch batch, int T_, int g, int ctas) {
-  // Launched while the attention kernel still runs: only the partials wait for its end.
-  __shared__ Place sh;
-  __shared__ long long sh_unit[3];
+  // Launched while the attention kernel still runs: only the partials wait for its end.  The item, by one warp:
+  struct Cut {
+    Seq s;
+    int i0, kvh, parts, first;  // parts 0: nothing to join; first: slot of the first part
+  };
+  __shared__ Cut sh;
   if (threadIdx.x < 32) {
     const long long U = batch.total<KT>();
     const long long per = share(U, ctas);
     const long long u0 = per * blockIdx.x, u1 = min(u0 + per, U);
-    Place at{batch.seqs, 0, 0, 0};
-    if (u0 < U) at = batch.locate<KT>(u1 - 1);
-    if (threadIdx.x == 0) {
-      sh = at;
-      sh_unit[0] = u0;
-      sh_unit[1] = u1;
-      sh_unit[2] = per;
+    Cut cut{};
+    if (u0 < U) {
+      const Place at = batch.locate<KT>(u1 - 1);
+      const long long begin = u1 - 1 - at.off;
+      cut.s = load_seq(batch.q_start, batch.kv_len, at.b, T_, batch.cap);
+      cut.i0 = at.run * batch.TI;
+      cut.kvh = at.kvh;
+      const int units = max(1, run_tiles<KT>(cut.s, cut.i0, batch.TI, batch.window, batch.sinks).count);
+      // else begun before, or complete
+      if (begin >= u0 && begin + units > u1) cut.parts = 1 + (int)((begin + units - u1 + per - 1) / per);
+      cut.first = 2 * blockIdx.x + (begin == u0 ? 0 : 1);
     }
+    if (threadIdx.x == 0) sh = cut;
   }
   __syncthreads();
   // Every CTA waits, those without work too: what follows in the stream waits for this kernel alone.
   ahead_wait();
-  const Place at = sh;
-  if (at.b >= batch.seqs) return;
-  const long long u0 = sh_unit[0], u1 = sh_unit[1], per = sh_unit[2];
-  const long long begin = u1 - 1 - at.off;
-  const Seq s = load_seq(batch.q_start, batch.kv_len, at.b, T_, batch.cap);
-  const int i0 = at.run * batch.TI;
-  const int units = max(1, run_tiles<KT>(s, i0, batch.TI, batch.window, batch.sinks).count);
-  if (begin < u0 || begin + units <= u1) return;  // begun before, or complete
-  const int parts = 1 + (int)((begin + units - u1 + per - 1) / per);
+  const int parts = sh.parts;
+  if (parts == 0) return;
+  const Seq s = sh.s;
+  const int i0 = sh.i0, kvh = sh.kvh, first = sh.first;
   const int nrows = min(batch.TI, s.n - i0) * g;
   const size_t psz = partial_floats(ROWS, HD);
   const float* part = static_cast<const float*>(a.ws);
-  auto slot = [&](int i) { return part + psz * (i == 0 ? 2 * blockIdx.x + (begin == u0 ? 0 : 1) : 2 * (blockIdx.x + i)); };
+  auto slot = [&](int i) { return part + psz * (i == 0 ? first : 2 * (blockIdx.x + i)); };
   const int lane = threadIdx.x & 31;
   constexpr int V = HD / 32;
   for (int r = blockIdx.y + gridDim.y * (threadIdx.x >> 5); r < nrows; r += gridDim.y * 8) {
@@ -129,7 +132,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, Batch batc
       }
     }
     const float inv = l == 0.f ? 0.f : 1.0f / l;
-    const int h = at.kvh * g + r % g, row = s.q0 + i0 + r / g;
+    const int h = kvh * g + r % g, row = s.q0 + i0 + r / g;
     T* dst = row_ptr_w<T>(a.h, 0, h, row) + lane * V;
 #pragma unroll
     for (int c = 0; c < V; ++c) dst[c] = from_f32<T>(o[c] * inv);
