@@ -30,8 +30,8 @@
 // and a single token fills g rows; 128 / g tokens to a slot.  Paged items are cut into
 // equal shares of key tiles (win_common.cuh); cut items leave fp32 partials.
 //
-// Measured (bf16, 32 heads over 8, d = 128).  32768 tokens, window 1024, 64 sinks: 660 us, 870 TFLOP/s of visible pairs
-// (768 on a box under its power cap).  Chunks of 2048 tokens over 14000 more, 4 sequences: 1096 us, 1030 TFLOP/s (1284).
+// Measured (bf16, 32 heads over 8, d = 128).  32768 tokens, window 1024, 64 sinks: 647 us, 890 TFLOP/s of visible pairs
+// (750 on a box under its power cap).  Chunks of 2048 tokens over 14000 more, 4 sequences: 1096 us, 1030 TFLOP/s (1284).
 // Bound by the chain of a step, 3500 cycles for a tile of both slots: logits waited for 1100, loaded for their maximum 350,
 // maximum passed on 570, exponentials 1200, P stored 330; of these the tensor pipe is busy 2560 (45 % over
 // the kernel) and the exponentials' pipe 2048.  Between items 5500 cycles (sums, last product, output), which bounds
@@ -58,9 +58,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t COL_S = 256;
 
-template <int HD>
+template <int HD, bool PAGED>
 struct Cfg {
-  static constexpr int NSK = HD == 128 ? 3 : 4, NSV = HD == 128 ? 2 : 4;  // K, V tiles in flight
+  // K, V tiles in flight.  At d = 128 the paged form fills shared memory: one token of 64 sequences takes 236 us with three
+  // K tiles, 244 to 254 with two; the window form does better with two (32768 tokens, window 1024: 647 us against 660).
+  static constexpr int NSK = HD == 128 ? (PAGED ? 3 : 2) : 4, NSV = HD == 128 ? 2 : 4;
   static constexpr int TB = TILE * HD * 2;
   static constexpr int HALF = TILE * 128;  // 64 columns of a tile: 128 rows of 128 bytes
   static constexpr int OFF_K = 2 * TB, OFF_V = OFF_K + NSK * TB, OFF_MISC = OFF_V + NSV * TB;
@@ -220,7 +222,7 @@ template <int HD, bool PAGED>
 __global__ void __launch_bounds__(NTHREADS, 1)
     win_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TcParams p) {
-  using C = Cfg<HD>;
+  using C = Cfg<HD, PAGED>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;  // tiles need 1024-byte alignment: checked below
   Misc& M = *reinterpret_cast<Misc*>(smem + C::OFF_MISC);
@@ -758,19 +760,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
 }
 
-template <int HD>
+template <int HD, bool PAGED>
 constexpr int smem_bytes() {
-  return Cfg<HD>::OFF_MISC + (int)sizeof(Misc);
+  return Cfg<HD, PAGED>::OFF_MISC + (int)sizeof(Misc);
 }
-static_assert(smem_bytes<128>() <= 232448, "shared memory of a CTA");
+static_assert(smem_bytes<128, true>() <= 232448, "shared memory of a CTA");
 
 template <int HD, bool PAGED>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const TcParams& p, int ctas,
                    cudaStream_t st) {
   auto kern = win_fwd_tc_kernel<HD, PAGED>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<HD>());
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<HD, PAGED>());
   if (e != cudaSuccess) return e;
-  kern<<<ctas, NTHREADS, smem_bytes<HD>(), st>>>(q, k, v, p);
+  kern<<<ctas, NTHREADS, smem_bytes<HD, PAGED>(), st>>>(q, k, v, p);
   count_launches(1);
   return cudaGetLastError();
 }
