@@ -31,7 +31,7 @@
 // equal shares of key tiles (win_common.cuh); cut items leave fp32 partials.
 //
 // Measured (bf16, 32 heads over 8, d = 128).  32768 tokens, window 1024, 64 sinks: 647 us, 890 TFLOP/s of visible pairs
-// (750 on a box under its power cap).  Chunks of 2048 tokens over 14000 more, 4 sequences: 1096 us, 1030 TFLOP/s (1284).
+// (20 passes from idle; 760 in long runs).  Chunks of 2048 tokens over 14000 more, 4 sequences: 1085 us, 1040 TFLOP/s (1289).
 // Bound by the chain of a step, 3500 cycles for a tile of both slots: logits waited for 1100, loaded for their maximum 350,
 // maximum passed on 570, exponentials 1200, P stored 330; of these the tensor pipe is busy 2560 (45 % over
 // the kernel) and the exponentials' pipe 2048.  Between items 5500 cycles (sums, last product, output), which bounds
