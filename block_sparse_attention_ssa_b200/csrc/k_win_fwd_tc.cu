@@ -37,7 +37,7 @@
 // the kernel) and the exponentials' pipe 2048.  Between items 5500 cycles (sums, last product, output), which bounds
 // short windows: 8192 tokens, 32 heads over 2, d = 64, window 256: 76 us, 235 TFLOP/s.  One token of 64
 // sequences over 8000 each: 240 us, 5.5 TB/s, bound by memory.
-#include "win_common.cuh"
+#include "win_rows.cuh"
 
 #include "sm100_ptx.cuh"
 
@@ -83,6 +83,7 @@ struct Misc {
   int abort;
   int turn;  // 1 while an issuer feeds the tensor core
   int left;
+  int again[16];  // a softmax warp stored rows that are not finite
   Place at;
   uint32_t bad[8];  // pages missing from a key tile, a bit per 16 keys (ring of 2 NSK tiles)
   float mref[2][TILE];  // running maximum of each row
@@ -90,7 +91,7 @@ struct Misc {
 };
 
 struct TcParams {
-  TensorRef h;
+  TensorRef q, k, v, h;
   float* lse;
   int32_t* status;
   int B, Hq, g, N, window, sinks;
@@ -218,10 +219,50 @@ struct Walk {
   }
 };
 
+// A softmax warp's rows once more (win_rows.cuh): those whose sum is finite and whose columns are not.  Behind the loop over
+// the items, so that nothing of it is held in registers there (within it, 270 to 530 bytes were spilled), and inline: a
+// function called there took 2 us of every launch (8192 tokens, window 256: 79.6 us, inline 77.5, without any of it 77.8).
+template <int HD, bool PAGED>
+__device__ __forceinline__ void form_again(const TcParams& p, const Misc& M, int warp) {
+  constexpr int W = HD / 2;
+  const int s = warp >> 3, half = (warp >> 2) & 1, r0 = (warp & 3) * 32, lane = threadIdx.x & 31;
+  Walk<PAGED> walk(p, M, s);
+  Item I;
+  while (walk.next(I)) {
+    if (I.T == 0 || (s && !I.two)) continue;
+    const int shift = s ? I.toks0 : 0, nrows = (s ? I.toks - I.toks0 : I.toks0) * I.g;
+    const KeyRows<bf16> keys{p.k, p.v, I.b, I.kvh, PAGED ? p.table : nullptr, p.page, p.num_pages, p.max_pages};
+    for (int r = r0; r < min(r0 + 32, nrows); ++r) {
+      const int tok = I.row0 + shift + r / I.g, head = I.head0 + r % I.g;
+      const RowView view{I.kt, I.p0 + shift + r / I.g, I.off, I.off + I.T, p.window, p.sinks, p.N};
+      const bf16* q = row_ptr<bf16>(p.q, PAGED ? 0 : I.b, head, tok);
+      float* part = nullptr;
+      bf16* out = nullptr;
+      float m, l;  // of the partial; of the output, its weights are 2^(c q . k - log2(e) lse)
+      if (PAGED && I.cut) {
+        float* pb = p.part + (size_t)(2 * blockIdx.x + (I.seg ? 1 : 0)) * partial_floats(2 * TILE, HD);
+        const int pr = shift * I.g + r;
+        part = pb + (size_t)pr * HD + W * half;
+        m = pb[2 * TILE * HD + pr];
+        l = pb[2 * TILE * HD + 2 * TILE + pr];
+      } else {
+        out = row_ptr_w<bf16>(p.h, PAGED ? 0 : I.b, head, tok) + W * half;
+        l = p.lse[PAGED ? (int64_t)head * p.batch.T + tok : ((int64_t)I.b * p.Hq + head) * p.N + tok];
+        m = l * kLog2e;
+      }
+      bool fine = true;
+      for (int c = lane; c < W; c += 32) fine &= is_finite(part != nullptr ? part[c] : to_f32(out[c]));
+      if (is_finite(l) && !__all_sync(0xffffffffu, fine))
+        weigh_row<bf16, HD, W, TILE>(keys, view, q, out, part, W * half, p.c, m, 1.f);
+    }
+  }
+}
+
 template <int HD, bool PAGED>
 __global__ void __launch_bounds__(NTHREADS, 1)
     win_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TcParams p) {
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmVs,
+                      const __grid_constant__ TcParams p) {
   using C = Cfg<HD, PAGED>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;  // tiles need 1024-byte alignment: checked below
@@ -262,6 +303,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     mbar_init(&M.join_done, 8);
     M.abort = 0;
     M.turn = 0;
+    for (int w = 0; w < 16; ++w) M.again[w] = 0;
     fence_mbar_init();
   }
   if (warp == WARP_MMA) {
@@ -368,9 +410,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
           __syncwarp();
         } else if (lane == 0) {
+          // No query of the item sees more of a sink tile's keys than the sinks: V through a map that ends there, zeros
+          // behind it, so that what those rows hold does not reach every later token.
+          const CUtensorMap* mp = !is_k && j < I.kt.ns ? &tmVs : map;
           mbar_expect_tx(&full[st], C::TB);
           for (int f = 0; f < HD / 64; ++f)
-            tma_load_4d(dst + f * C::HALF, map, &full[st], 64 * f, t * TILE, zero & 2 ? 0 : I.kvh, zero & 1 ? 0 : I.b);
+            tma_load_4d(dst + f * C::HALF, mp, &full[st], 64 * f, t * TILE, zero & 2 ? 0 : I.kvh, zero & 1 ? 0 : I.b);
         }
         issued = n + 1;
       }
@@ -703,6 +748,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
           }
           const uint32_t o_addr = lane_base + HD * s + W * half;
+          float2 z = make_float2(0.f, 0.f);
 #pragma unroll 1
           for (int c0 = 0; c0 < W; c0 += 16) {
             uint32_t r[16];
@@ -721,6 +767,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               for (int c = 0; c < 16; ++c)
                 if (f1 != 0.f) r[c] = __float_as_uint(fmaf(__uint_as_float(r1[c]), f1, __uint_as_float(r[c])));
             }
+#pragma unroll
+            for (int c = 0; c < 16; c += 2)
+              z = fma2(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), make_float2(0.f, 0.f), z);
             if (po != nullptr) {
 #pragma unroll
               for (int c = 0; c < 16; c += 4)
@@ -732,6 +781,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               store_32b(ho + c0, h8, p.wide);
             }
           }
+          if (z.x + z.y != 0.f && (po != nullptr || ho != nullptr)) M.again[warp] = 1;
         }
         if (join) {
           tc_fence_before();
@@ -758,6 +808,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  // every warp's rows and statistics are stored
+  if (warp < WARP_TMA && M.again[warp] && !M.abort) form_again<HD, PAGED>(p, M, warp);
 }
 
 template <int HD, bool PAGED>
@@ -767,12 +819,12 @@ constexpr int smem_bytes() {
 static_assert(smem_bytes<128, true>() <= 232448, "shared memory of a CTA");
 
 template <int HD, bool PAGED>
-cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const TcParams& p, int ctas,
-                   cudaStream_t st) {
+cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& vs, const TcParams& p,
+                   int ctas, cudaStream_t st) {
   auto kern = win_fwd_tc_kernel<HD, PAGED>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<HD, PAGED>());
   if (e != cudaSuccess) return e;
-  kern<<<ctas, NTHREADS, smem_bytes<HD, PAGED>(), st>>>(q, k, v, p);
+  kern<<<ctas, NTHREADS, smem_bytes<HD, PAGED>(), st>>>(q, k, v, vs, p);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -780,11 +832,15 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
 }  // namespace
 
 cudaError_t launch_win_fwd_tc(const WinDims& D, const WinFwdArgs& a, int32_t* status, cudaStream_t st) {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, vs;
   TcParams p{};
   if (!win_tma_map(&q, a.q, D.B, D.Hq, D.N, TILE, D.d, &p.zq) || !win_tma_map(&k, a.k, D.B, D.Hkv, D.N, TILE, D.d, &p.zk) ||
-      !win_tma_map(&v, a.v, D.B, D.Hkv, D.N, TILE, D.d, &p.zv))
+      !win_tma_map(&v, a.v, D.B, D.Hkv, D.N, TILE, D.d, &p.zv) ||
+      !win_tma_map(&vs, a.v, D.B, D.Hkv, D.sinks > 0 ? D.sinks : D.N, TILE, D.d, &p.zv))
     return cudaErrorInvalidValue;
+  p.q = a.q;
+  p.k = a.k;
+  p.v = a.v;
   p.h = a.h;
   p.lse = a.lse;
   p.status = status;
@@ -802,7 +858,7 @@ cudaError_t launch_win_fwd_tc(const WinDims& D, const WinFwdArgs& a, int32_t* st
   p.rows_item = planes * ((D.N + 255) / 256) >= kCtas ? 256 : 128;
   const int64_t items = planes * ((D.N + p.rows_item - 1) / p.rows_item);
   const int ctas = (int)(items < kCtas ? items : kCtas);
-  return D.d == 64 ? launch<64, false>(q, k, v, p, ctas, st) : launch<128, false>(q, k, v, p, ctas, st);
+  return D.d == 64 ? launch<64, false>(q, k, v, vs, p, ctas, st) : launch<128, false>(q, k, v, vs, p, ctas, st);
 }
 
 size_t paged_tc_ws_bytes(const PagedDims& D) {
@@ -819,6 +875,9 @@ cudaError_t launch_paged_tc(const PagedDims& D, const PagedArgs& a, int32_t* sta
       !win_tma_map(&k, a.k, D.num_pages, D.Hkv, D.page, rows, D.d, &p.zk) ||
       !win_tma_map(&v, a.v, D.num_pages, D.Hkv, D.page, rows, D.d, &p.zv))
     return cudaErrorInvalidValue;
+  p.q = a.q;
+  p.k = a.k;
+  p.v = a.v;
   p.h = a.h;
   p.lse = a.lse;
   p.status = status;
@@ -834,7 +893,7 @@ cudaError_t launch_paged_tc(const PagedDims& D, const PagedArgs& a, int32_t* sta
   p.max_pages = D.max_pages;
   p.batch = Batch{a.q_start, a.kv_len, D.seqs, D.T, D.max_pages * D.page, 2 * p.TQ, D.window, D.sinks, D.Hkv};
   p.part = static_cast<float*>(a.ws);
-  cudaError_t e = D.d == 64 ? launch<64, true>(q, k, v, p, kCtas, st) : launch<128, true>(q, k, v, p, kCtas, st);
+  cudaError_t e = D.d == 64 ? launch<64, true>(q, k, v, v, p, kCtas, st) : launch<128, true>(q, k, v, v, p, kCtas, st);
   if (e != cudaSuccess) return e;
   return launch_paged_join<TILE, 2 * TILE>(D, a, kCtas, 2 * p.TQ, st);
 }
