@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (lane == 0) mbar_arrive(&M.m_ready[s][half][quarter]);
           ++mc;
           if (mn != m) {
-            l = m == kNegInf ? 0.f : l * ex2(m - mn);
+            l *= ex2(m - mn);  // from -infinity by zero, which keeps a NaN
             m = mn;
           }
           const float nm = m == kNegInf ? 0.f : -m;
@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (!(ok = wait(&M.m_ready[s][1][quarter], mc - 1))) break;
           const float mn = *mref;
           if (mn != m) {
-            l = m == kNegInf ? 0.f : l * ex2(m - mn);
+            l *= ex2(m - mn);  // from -infinity by zero, which keeps a NaN
             m = mn;
           }
           M.sum[s][row] = l;

@@ -101,6 +101,8 @@ FORWARD = {
     # behind the sinks in a tile that every later token loads
     "behind_the_sinks": lambda N: [("V", (0, 100), NAN), ("V", (slice(None), 71, 5), INF)],
     "one_element": lambda N: [("V", (0, 200, 33), INF), ("V", (0, 203, 2), -INF), ("V", (0, 210, 2), INF), ("V", (0, 131, 60), NAN)],
+    # a sink that far tokens meet alone in their first tile: its NaN comes before the first finite logit
+    "first_sink": lambda N: [("K", (0, 0), NAN)],
     "a_key_and_a_query": lambda N: [("K", (0, 150), NAN), ("Q", (1, 160), NAN), ("V", (0, 0), NAN)],
 }
 
