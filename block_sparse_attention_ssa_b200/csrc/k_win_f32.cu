@@ -27,9 +27,7 @@
 // order of the reduction is free: t and t + 4 stand for elements 2t and 2t + 1 of each eight,
 // so an accumulator is the next product's A as it is, and A and B of the logits are 8-byte
 // loads.
-#include "win_common.cuh"
-
-#include <type_traits>
+#include "win_rows.cuh"
 
 #include "mma_sync.cuh"
 
@@ -200,6 +198,90 @@ struct Fwd {
   static constexpr size_t SMEM = (size_t)(1 + GROUPS) * TILEF * 4;  // Q, then each group's K or V
 };
 
+// One item of the paged form (a share of it), or the CTA's tile of the window form.
+struct F32Item {
+  int b, head0, q0row, kvh, nrows, p0, per_tok, units, take, len;
+  KeyTiles kt;
+};
+
+template <bool PAGED>
+__device__ __forceinline__ F32Item item_of(const F32Params& p, const Place& at, int left) {
+  F32Item I;
+  if (PAGED) {
+    const Seq s = load_seq(p.batch.q_start, p.batch.kv_len, at.b, p.T, p.batch.cap);
+    const int i0 = at.run * p.batch.TI;
+    I.b = at.b;
+    I.kvh = at.kvh;
+    I.head0 = at.kvh * p.g;
+    I.per_tok = p.g;
+    I.nrows = min(p.batch.TI, s.n - i0) * p.g;
+    I.q0row = s.q0 + i0;
+    I.p0 = s.len - s.n + i0;
+    I.len = s.len;
+    I.kt = run_tiles<BT>(s, i0, p.batch.TI, p.window, p.sinks);
+    I.units = max(1, I.kt.count);
+    I.take = min(left, I.units - at.off);
+  } else {
+    const int planes = (int)(gridDim.x / p.NT);
+    const int plane = (int)blockIdx.x % planes, qt = p.NT - 1 - (int)blockIdx.x / planes;
+    I.b = plane / p.Hq;
+    I.head0 = plane % p.Hq;
+    I.kvh = I.head0 / p.g;
+    I.per_tok = 1;
+    I.q0row = I.p0 = qt * BT;
+    I.nrows = min(BT, p.N - I.p0);
+    I.len = p.N;
+    I.kt = key_tiles<BT>(I.p0, I.p0 + I.nrows - 1, p.window, p.sinks);
+    I.units = I.take = I.kt.count;
+  }
+  return I;
+}
+
+// The place behind `take` units of an item: whether the share holds more.
+__device__ __forceinline__ bool next_item(const F32Params& p, Place& at, int& left, int take) {
+  left -= take;
+  if (left <= 0) return false;
+  at.off = 0;
+  if (++at.kvh == p.batch.Hkv) {
+    at.kvh = 0;
+    ++at.run;
+    while (at.b < p.batch.seqs) {
+      const Seq s = load_seq(p.batch.q_start, p.batch.kv_len, at.b, p.T, p.batch.cap);
+      if (at.run * p.batch.TI < s.n) break;
+      at.run = 0;
+      ++at.b;
+    }
+    if (at.b >= p.batch.seqs) return false;
+  }
+  return true;
+}
+
+// The CTA's rows once more (win_rows.cuh), those that are not finite; a warp takes every n-th row.
+template <int HD, bool PAGED>
+__device__ __forceinline__ void form_again(const F32Params& p, Place at, int left) {
+  for (int seg = 0;; ++seg) {
+    const F32Item I = item_of<PAGED>(p, at, left);
+    const KeyRows<float> keys{p.k, p.v, I.b, I.kvh, PAGED ? p.table : nullptr, p.page, p.num_pages, p.max_pages};
+    for (int r = threadIdx.x >> 5; r < I.nrows; r += blockDim.x >> 5) {
+      const int tok = PAGED ? r / I.per_tok : r, head = PAGED ? I.head0 + r % I.per_tok : I.head0, row = I.q0row + tok;
+      const int first = PAGED ? at.off : 0;
+      const RowView view{I.kt, I.p0 + tok, first, min(first + I.take, I.kt.count), p.window, p.sinks, p.N};
+      RowOut<float> o{};
+      if (PAGED && I.take < I.units) {
+        float* base = p.part + (size_t)(2 * blockIdx.x + (seg ? 1 : 0)) * partial_floats(BT, HD);
+        o.part = base + r * HD;
+        o.m = base + BT * HD + r;
+        o.l = o.m + BT;
+      } else {
+        o.out = row_ptr_w<float>(p.h, PAGED ? 0 : I.b, head, row);
+        o.lse = p.lse + (PAGED ? (int64_t)head * p.T + row : ((int64_t)I.b * p.Hq + I.head0) * p.N + row);
+      }
+      mend_row<float, HD, HD, BT>(keys, view, row_ptr<float>(p.q, PAGED ? 0 : I.b, head, row), o, 0, p.c);
+    }
+    if (!PAGED || !next_item(p, at, left, I.take)) return;
+  }
+}
+
 template <int HD, bool PAGED>
 __global__ void __launch_bounds__(Fwd<HD>::THREADS, 1) win_fwd_f32_kernel(F32Params p) {
   using C = Fwd<HD>;
@@ -215,6 +297,7 @@ __global__ void __launch_bounds__(Fwd<HD>::THREADS, 1) win_fwd_f32_kernel(F32Par
 
   Place at{0, 0, 0, 0};
   int left = 1;
+  bool again = false;  // rows that are not finite were stored (a store to shared memory there held up the next row: 97 us for 92)
   if (PAGED) {
     if (threadIdx.x < 32) {
       const long long U = p.batch.total<BT>();
@@ -235,37 +318,10 @@ __global__ void __launch_bounds__(Fwd<HD>::THREADS, 1) win_fwd_f32_kernel(F32Par
 
   for (int seg = 0; left > 0; ++seg) {
     // ---- the item
-    int b, head0, q0row, kvh, nrows, p0, per_tok, i0 = 0, units, take, len;
-    Seq s{};
-    KeyTiles kt;
-    if (PAGED) {
-      b = at.b;
-      s = load_seq(p.batch.q_start, p.batch.kv_len, b, p.T, p.batch.cap);
-      i0 = at.run * p.batch.TI;
-      const int toks = min(p.batch.TI, s.n - i0);
-      kvh = at.kvh;
-      head0 = kvh * p.g;
-      per_tok = p.g;
-      nrows = toks * p.g;
-      q0row = s.q0 + i0;
-      p0 = s.len - s.n + i0;
-      len = s.len;
-      kt = run_tiles<BT>(s, i0, p.batch.TI, p.window, p.sinks);
-      units = max(1, kt.count);
-      take = min(left, units - at.off);
-    } else {
-      const int planes = (int)(gridDim.x / p.NT);
-      const int plane = (int)blockIdx.x % planes, qt = p.NT - 1 - (int)blockIdx.x / planes;
-      b = plane / p.Hq;
-      head0 = plane % p.Hq;
-      kvh = head0 / p.g;
-      per_tok = 1;
-      q0row = p0 = qt * BT;
-      nrows = min(BT, p.N - p0);
-      len = p.N;
-      kt = key_tiles<BT>(p0, p0 + nrows - 1, p.window, p.sinks);
-      units = take = kt.count;
-    }
+    const F32Item I = item_of<PAGED>(p, at, left);
+    const int b = I.b, head0 = I.head0, q0row = I.q0row, kvh = I.kvh, nrows = I.nrows, p0 = I.p0, per_tok = I.per_tok;
+    const int take = I.take, units = I.units, len = I.len;
+    const KeyTiles kt = I.kt;
     const bool cut = PAGED && take < units;
     auto tok_of = [&](int r) { return PAGED ? r / per_tok : r; };
     auto head_of = [&](int r) { return PAGED ? head0 + r % per_tok : head0; };
@@ -421,29 +477,22 @@ __global__ void __launch_bounds__(Fwd<HD>::THREADS, 1) win_fwd_f32_kernel(F32Par
             p.lse[o] = l[i] == 0.f ? kNegInf : (m[i] + log2f(l[i])) * kLn2;
           }
         }
+        float z = l[i] * 0.f;
 #pragma unroll
-        for (int n = 0; n < HD / 8; ++n)
-          *reinterpret_cast<float2*>(dst + 8 * n + 2 * t) = make_float2(acc[n][2 * i] * mul, acc[n][2 * i + 1] * mul);
+        for (int n = 0; n < HD / 8; ++n) {
+          const float2 y = make_float2(acc[n][2 * i] * mul, acc[n][2 * i + 1] * mul);
+          *reinterpret_cast<float2*>(dst + 8 * n + 2 * t) = y;
+          z = fmaf(y.x, 0.f, fmaf(y.y, 0.f, z));
+        }
+        again |= z != 0.f;
       }
     }
     if (!PAGED) break;
     // ---- the next item
-    left -= take;
-    if (left <= 0) break;
-    at.off = 0;
-    if (++at.kvh == p.batch.Hkv) {
-      at.kvh = 0;
-      ++at.run;
-      while (at.b < p.batch.seqs) {
-        s = load_seq(p.batch.q_start, p.batch.kv_len, at.b, p.T, p.batch.cap);
-        if (at.run * p.batch.TI < s.n) break;
-        at.run = 0;
-        ++at.b;
-      }
-      if (at.b >= p.batch.seqs) break;
-    }
+    if (!next_item(p, at, left, take)) break;
     __syncthreads();  // shared memory is read to the end
   }
+  if (__syncthreads_or(again)) form_again<HD, PAGED>(p, PAGED ? sh_place : Place{0, 0, 0, 0}, PAGED ? sh_left : 1);
 }
 
 // ================================================================ backward

@@ -225,7 +225,7 @@ struct Walk {
 template <int HD, bool PAGED>
 __device__ __forceinline__ void form_again(const TcParams& p, const Misc& M, int warp) {
   constexpr int W = HD / 2;
-  const int s = warp >> 3, half = (warp >> 2) & 1, r0 = (warp & 3) * 32, lane = threadIdx.x & 31;
+  const int s = warp >> 3, half = (warp >> 2) & 1, r0 = (warp & 3) * 32;
   Walk<PAGED> walk(p, M, s);
   Item I;
   while (walk.next(I)) {
@@ -236,24 +236,18 @@ __device__ __forceinline__ void form_again(const TcParams& p, const Misc& M, int
       const int tok = I.row0 + shift + r / I.g, head = I.head0 + r % I.g;
       const RowView view{I.kt, I.p0 + shift + r / I.g, I.off, I.off + I.T, p.window, p.sinks, p.N};
       const bf16* q = row_ptr<bf16>(p.q, PAGED ? 0 : I.b, head, tok);
-      float* part = nullptr;
-      bf16* out = nullptr;
-      float m, l;  // of the partial; of the output, its weights are 2^(c q . k - log2(e) lse)
+      RowOut<bf16> o{};
       if (PAGED && I.cut) {
         float* pb = p.part + (size_t)(2 * blockIdx.x + (I.seg ? 1 : 0)) * partial_floats(2 * TILE, HD);
         const int pr = shift * I.g + r;
-        part = pb + (size_t)pr * HD + W * half;
-        m = pb[2 * TILE * HD + pr];
-        l = pb[2 * TILE * HD + 2 * TILE + pr];
+        o.part = pb + (size_t)pr * HD + W * half;
+        o.m = pb + 2 * TILE * HD + pr;
+        o.l = o.m + 2 * TILE;
       } else {
-        out = row_ptr_w<bf16>(p.h, PAGED ? 0 : I.b, head, tok) + W * half;
-        l = p.lse[PAGED ? (int64_t)head * p.batch.T + tok : ((int64_t)I.b * p.Hq + head) * p.N + tok];
-        m = l * kLog2e;
+        o.out = row_ptr_w<bf16>(p.h, PAGED ? 0 : I.b, head, tok) + W * half;
+        o.lse = p.lse + (PAGED ? (int64_t)head * p.batch.T + tok : ((int64_t)I.b * p.Hq + head) * p.N + tok);
       }
-      bool fine = true;
-      for (int c = lane; c < W; c += 32) fine &= is_finite(part != nullptr ? part[c] : to_f32(out[c]));
-      if (is_finite(l) && !__all_sync(0xffffffffu, fine))
-        weigh_row<bf16, HD, W, TILE>(keys, view, q, out, part, W * half, p.c, m, 1.f);
+      mend_row<bf16, HD, W, TILE>(keys, view, q, o, W * half, p.c);
     }
   }
 }

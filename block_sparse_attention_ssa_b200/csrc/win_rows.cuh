@@ -1,13 +1,16 @@
 // Rows formed anew over the pairs that the mask leaves.
 //
 // A tile's product multiplies hidden pairs too, with a weight of zero, and zero times a NaN or an infinity is
-// NaN: one such value would spoil every row that shares a tile with a row that sees it.  So the kernels look at
-// the rows that they store (one multiply-add a value), and where some are not finite, the warp that stored them forms them
-// once more, here, from their visible pairs alone, in fp32 multiply-adds.  Rows that see no NaN or infinity come
-// out finite; the others are what the formula says.  A pass over finite values calls nothing of this.
+// NaN: one such value would spoil every row that shares a tile with a row that sees it.  An fp32 operand as a pair of TF32
+// values turns an infinity into a NaN besides.  So the kernels look at the rows that they store (one multiply-add a
+// value), and where some are not finite, the warps that stored them form them once more, here, from their visible
+// pairs alone, in fp32 multiply-adds.  Rows that see no NaN or infinity come out finite; the others are what the
+// formula says.  A pass over finite values calls nothing of this.
 #pragma once
 
 #include "win_common.cuh"
+
+#include <type_traits>
 
 namespace ssa {
 
@@ -65,24 +68,50 @@ struct RowView {
   int t, first, last, window, sinks, N;  // N: keys of the window form
 };
 
-// Values that are not finite among the W columns at `out` (dtype T, or fp32 partials at `part`) of a query's row become
-//   mul * sum_u 2^(c q . k_u - m) v_u
-// over the keys u that it sees.  k, v, q begin at the row; columns at c0.  Warp-wide.  In the window form, rows that
-// owe their state to a key that they see are left as they are without going through their keys, unless a hidden one of
-// their tiles holds such values too: only tiles that the row sees in part are looked through for it.
+// f(u0, k) for each 32 keys u0 .. u0 + 31 of the view's tiles, the newest first, until it returns false; k: the lane's
+// key row, null where the query does not see it.  Warp-wide.
+template <typename T, int KT, typename F>
+__device__ __forceinline__ void for_keys(const KeyRows<T>& keys, const RowView& r, F f) {
+  for (int j = r.last - 1; j >= r.first; --j)
+    for (int i = KT - 32; i >= 0; i -= 32) {
+      const int u0 = r.kt.tile(j) * KT + i, u = u0 + (threadIdx.x & 31);
+      if (!f(u0, sees(r.t, u, r.window, r.sinks) ? keys.at(keys.k, u) : nullptr)) return;
+    }
+}
+
+// W columns of a query's row, from column c0 on, and its statistics where they lie (partials of a cut item: its maximum
+// in base 2, its sum; outputs: lse, its normaliser's natural logarithm).  `out`, `part` (one of them null) begin at c0.
+template <typename T>
+struct RowOut {
+  T* out;
+  float* part;
+  float *m, *l;  // of the partial
+  float* lse;
+};
+
+// Forms the row anew where it is not finite.  In bf16 the statistics stand (the tensor cores hold infinities as they are)
+// and only columns that are not finite are written; in fp32 all of them are.  In the bf16 window form, rows that owe their state
+// to a key that they see are left without going through their keys, unless a hidden one of their tiles holds such
+// values too: only tiles that the row sees in part are looked through for it.  Warp-wide.
 template <typename T, int HD, int W, int KT>
-__device__ void weigh_row(const KeyRows<T>& keys, const RowView& r, const T* q, T* out, float* part, int c0, float c,
-                                       float m, float mul) {
+__device__ __forceinline__ void mend_row(const KeyRows<T>& keys, const RowView& r, const T* q, const RowOut<T>& o, int c0, float c) {
+  constexpr bool ALL = std::is_same_v<T, float>;
   constexpr int NC = (W + 31) / 32;
   const int lane = threadIdx.x & 31;
-  bool done[NC];  // finite, or NaN from a visible key
+  const float l0 = o.part != nullptr ? *o.l : *o.lse;
+  const bool empty = o.part != nullptr ? l0 == 0.f : l0 == kNegInf;
+  bool fine = empty || is_finite(l0);
+  if (!fine && !ALL) return;
+  bool done[NC];  // needs nothing, or NaN from a visible key
   float acc[NC];
 #pragma unroll
   for (int n = 0; n < NC; ++n) {
     acc[n] = 0.f;
-    done[n] = lane + 32 * n >= W || is_finite(part != nullptr ? part[lane + 32 * n] : to_f32(out[lane + 32 * n]));
+    done[n] = lane + 32 * n >= W || is_finite(o.part != nullptr ? o.part[lane + 32 * n] : to_f32(o.out[lane + 32 * n]));
+    fine &= done[n];
   }
-  if (keys.table == nullptr) {
+  if (__all_sync(0xffffffffu, fine)) return;
+  if (!ALL && keys.table == nullptr) {
     bool hidden = false;
     for (int j = r.first; j < r.last; ++j) {
       const int u0 = r.kt.tile(j) * KT;
@@ -92,34 +121,65 @@ __device__ void weigh_row(const KeyRows<T>& keys, const RowView& r, const T* q, 
     }
     if (!__any_sync(0xffffffffu, hidden)) return;
   }
+  // the row's maximum and sum
+  float m, mul = 1.f;
+  if (o.part != nullptr && !ALL) {
+    m = *o.m;
+  } else {
+    auto logit = [&](const T* k) { return dot_row<T, HD>(q, k) * c; };
+    m = kNegInf;
+    for_keys<T, KT>(keys, r, [&](int, const T* k) {
+      if (k != nullptr) m = fmaxf(m, logit(k));
+      return true;
+    });
+    float l = 0.f;
+#pragma unroll
+    for (int i = 16; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+    const float ref = m == kNegInf ? 0.f : m;
+    for_keys<T, KT>(keys, r, [&](int, const T* k) {
+      if (k != nullptr) l += exp2f(logit(k) - ref);
+      return true;
+    });
+#pragma unroll
+    for (int i = 16; i; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
+    if (o.part == nullptr) mul = l == 0.f ? 0.f : 1.0f / l;
+    if (ALL && lane == 0) {
+      if (o.part != nullptr) {
+        *o.m = m;
+        *o.l = l;
+      } else {
+        *o.lse = l == 0.f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
+      }
+    }
+    m = ref;
+  }
   bool write[NC];
 #pragma unroll
-  for (int n = 0; n < NC; ++n) write[n] = !done[n];
-  // from the newest key on: where all is NaN, the first of them ends it
-  for (int j = r.last - 1; j >= r.first; --j) {
-    for (int u0 = r.kt.tile(j) * KT + KT - 32, i0 = 0; i0 < KT; i0 += 32, u0 -= 32) {
-      const int u = u0 + lane;
-      const T* kr = sees(r.t, u, r.window, r.sinks) ? keys.at(keys.k, u) : nullptr;
-      const float w = kr != nullptr ? exp2f(fmaf(dot_row<T, HD>(q, kr), c, -m)) : 0.f;
-      for (unsigned rest = __ballot_sync(0xffffffffu, kr != nullptr); rest; rest &= rest - 1) {
-        const int i = __ffs(rest) - 1;
-        const T* vr = keys.at(keys.v, u0 + i) + c0;
-        const float wi = __shfl_sync(0xffffffffu, w, i);
-#pragma unroll
-        for (int n = 0; n < NC; ++n)
-          if (!done[n]) acc[n] = fmaf(wi, to_f32(vr[lane + 32 * n]), acc[n]);
-      }
-      bool all = true;
-#pragma unroll
-      for (int n = 0; n < NC; ++n) all &= (done[n] |= acc[n] != acc[n]);
-      if (__all_sync(0xffffffffu, all)) j = r.first, i0 = KT;
-    }
+  for (int n = 0; n < NC; ++n) {
+    if (ALL) done[n] = lane + 32 * n >= W;
+    write[n] = !done[n];
   }
+  // from the newest key on: where all is NaN, the first of them ends it
+  for_keys<T, KT>(keys, r, [&](int u0, const T* k) {
+    const float w = k != nullptr ? exp2f(dot_row<T, HD>(q, k) * c - m) * mul : 0.f;
+    for (unsigned rest = __ballot_sync(0xffffffffu, k != nullptr); rest; rest &= rest - 1) {
+      const int i = __ffs(rest) - 1;
+      const T* v = keys.at(keys.v, u0 + i) + c0;
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+        if (!done[n]) acc[n] = fmaf(wi, to_f32(v[lane + 32 * n]), acc[n]);
+    }
+    bool all = true;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) all &= (done[n] |= acc[n] != acc[n]);
+    return !__all_sync(0xffffffffu, all);
+  });
 #pragma unroll
   for (int n = 0; n < NC; ++n)
     if (write[n]) {
-      if (part != nullptr) part[lane + 32 * n] = acc[n] * mul;
-      else out[lane + 32 * n] = from_f32<T>(acc[n] * mul);
+      if (o.part != nullptr) o.part[lane + 32 * n] = acc[n];
+      else o.out[lane + 32 * n] = from_f32<T>(acc[n]);
     }
 }
 

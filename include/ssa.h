@@ -389,12 +389,8 @@ SSA_API size_t ssa_window_workspace_bytes(const ssa_window_dims_t* dims);
  *     [B, Hq, N] fp32, dense.  Inputs may broadcast batches and heads (stride 0);
  *     rows, and the slices of an output, may not lie over one another
  *     (SSA_ERR_INVALID_ARG).
- *   What a hidden key holds does not matter, in bf16 NaN and infinities
- *     included (a call whose rows meet some takes longer).  In fp32 and for
- *     the gradients, a NaN or an infinity in the row of token u may also reach
- *     tokens that do not see u but share a tile with one that does (a weight
- *     of zero times it).  In fp32 magnitudes from 3.4019e38 on (where rounding
- *     to TF32 overflows) count as infinities. */
+ *   What a hidden key holds does not matter, NaN and infinities included
+ *     (a call whose rows meet some takes longer). */
 SSA_API ssa_status_t ssa_fwd_window(const ssa_window_dims_t* dims, const ssa_tensor_t* Q, const ssa_tensor_t* K,
                                     const ssa_tensor_t* V, const ssa_tensor_t* h, float* lse,
                                     ssa_stream_t stream);
@@ -407,6 +403,10 @@ SSA_API ssa_status_t ssa_fwd_window(const ssa_window_dims_t* dims, const ssa_ten
  *   Q, K, V, h, lse: as passed to / written by ssa_fwd_window.
  *   g [B, Hq, N, d] dims->dtype (in, required).
  *   dQ [B, Hq, N, d], dK, dV [B, Hkv, N, d] (out): fully overwritten.
+ *   A NaN or an infinity in a row of Q, K or g may also reach gradients of
+ *     tokens that it has no pair with but that share a tile with such a pair
+ *     (a weight of zero times it).  In fp32 magnitudes from 3.4019e38 on (where
+ *     rounding to TF32 overflows) count as infinities.
  *   ws: at least ssa_window_workspace_bytes(dims) bytes, 256-byte aligned. */
 SSA_API ssa_status_t ssa_bwd_window(const ssa_window_dims_t* dims, const ssa_tensor_t* Q, const ssa_tensor_t* K,
                                     const ssa_tensor_t* V, const ssa_tensor_t* h, const float* lse,
@@ -470,8 +470,7 @@ SSA_API ssa_status_t ssa_paged_append(const ssa_paged_dims_t* dims, const ssa_te
  *   ws: at least ssa_paged_workspace_bytes(dims) bytes, 256-byte aligned; two
  *     calls in flight at once must not share it.
  *   What a page holds behind kv_len or outside a row's view does not matter
- *     to the row, NaN or not; in fp32 a NaN or infinity in a V row that some
- *     new token sees may reach rows of the same sequence's earlier ones. */
+ *     to the row, NaN or not. */
 SSA_API ssa_status_t ssa_paged_attention(const ssa_paged_dims_t* dims, const ssa_tensor_t* q, const ssa_tensor_t* K,
                                          const ssa_tensor_t* V, const int32_t* q_start, const int32_t* kv_len,
                                          const int32_t* page_table, const ssa_tensor_t* h, float* lse, void* ws,

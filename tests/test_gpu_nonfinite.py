@@ -107,11 +107,26 @@ FORWARD = {
 }
 
 
-@pytest.mark.parametrize("dtype", ["bf16"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("what", list(FORWARD))
 @pytest.mark.parametrize("name", list(SHAPES))
 def test_window_forward(name, what, dtype):
     _window_case(name, dtype, FORWARD[what], train=False)
+
+
+# fp32 alone: infinities and the largest magnitudes where tokens see them; -infinity in a key (finite logits of its other
+# values) hides the key from queries that are positive there
+FP32 = {
+    "infinities": lambda N: [("V", (0, 20), INF), ("V", (slice(None), 190, 7), -INF), ("V", (0, 191, 7), INF)],
+    "largest": lambda N: [("V", (0, 40, slice(0, 8)), 3.4028e38), ("V", (slice(None), 201), -3.4027e38)],
+    "hiding_keys": lambda N: [("K", (slice(None), 50, 0), -INF), ("K", (0, 180, 0), -INF)],
+}
+
+
+@pytest.mark.parametrize("what", list(FP32))
+@pytest.mark.parametrize("name", list(SHAPES))
+def test_window_forward_fp32(name, what):
+    _window_case(name, "f32", FP32[what], train=False)
 
 
 # new tokens, tokens in all, Hq, Hkv, d, page; then V rows that are spoiled: (sequence, position)
@@ -123,7 +138,7 @@ PAGED = {
 
 
 @pytest.mark.parametrize("window,sinks", [(None, 0), (200, 20)])
-@pytest.mark.parametrize("dtype", ["bf16"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("name", list(PAGED))
 def test_paged(name, dtype, window, sinks):
     args, bad = PAGED[name]
