@@ -27,7 +27,7 @@
 // Measured (16384 tokens, 32 heads over 8, d = 128, window 1024, 64 sinks): dkv 530 us, tensor pipe busy 64 % of the time
 // (1400 to 1600 cycles a unit, 1280 of them products); dq 437 us, 57 % (exponentials and dx, a chain of 1800
 // cycles a tile); with the preprocess (50 us) and the join (7 us) 680 TFLOP/s of the five products that count; seven are formed.
-#include "win_common.cuh"
+#include "win_rows.cuh"
 
 #include "sm100_ptx.cuh"
 
@@ -57,7 +57,7 @@ struct Cfg {
 };
 
 struct BwdParams {
-  TensorRef dq, dk, dv;
+  TensorRef q, k, v, up, dq, dk, dv;  // up: the upstream gradient
   const float* lse2;
   const float* dsum;
   float* part;
@@ -113,6 +113,13 @@ __device__ __forceinline__ void store16(bf16* dst, const uint32_t (&r)[16], floa
   store_32b(dst, o, wide);
 }
 
+// z becomes NaN where one of 16 values is not finite.
+__device__ __forceinline__ void look16(float2& z, const uint32_t (&r)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 2)
+    z = fma2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(0.f, 0.f), z);
+}
+
 // ================================================================ dK, dV
 template <int HD>
 struct DkvCfg {
@@ -164,6 +171,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const Chunk ch = find_chunk<TILE>((int)blockIdx.x / p.Hkv, p.cut, p.L, p.g, p.N, p.window, p.sinks);
   const int u0 = ch.kt * TILE, nq = query_tiles_of<TILE>(ch.kt, p.N, p.window, p.sinks);
   const int first = ch.idx * p.L, T = 2 * min(p.L, nq * p.g - first);  // units: step (head, query tile), half
+  bool again = false;  // the lane's row is not finite
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -351,6 +359,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const bool mine = u < p.N;
       float* part = p.part + ((size_t)plane * p.partials + ch.slot + ch.idx) * (2 * TILE * HD) +
                     (quarter * 32 + lane) * HD + col0;
+      float2 z = make_float2(0.f, 0.f);
 #pragma unroll 1
       for (int c0 = 0; c0 < 2 * W; c0 += 16) {
         const int which = c0 / W, col = c0 % W;  // 0: dK, 1: dV
@@ -358,6 +367,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         tmem_ld16((which ? cV : cK) + lane_base + col0 + col, r);
         tmem_wait_ld();
         if (!mine) continue;
+        look16(z, r);
         if (ch.n == 1) {
           const TensorRef& t = which ? p.dv : p.dk;
           store16(row_ptr_w<bf16>(t, b, kvh, u) + col0 + col, r, which ? 1.0f : p.scale, p.wide_kv);
@@ -367,6 +377,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           for (int v = 0; v < 4; ++v) d4[v] = make_uint4(r[4 * v], r[4 * v + 1], r[4 * v + 2], r[4 * v + 3]);
         }
       }
+      again = z.x + z.y != 0.f;
     }
   }
   tc_fence_before();
@@ -376,6 +387,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+  // A warp's rows that are not finite once more (win_rows.cuh).
+  for (unsigned rest = __ballot_sync(0xffffffffu, again); rest; rest &= rest - 1) {
+    constexpr int W = HD / 4;
+    const int r = (warp & 3) * 32 + __ffs(rest) - 1, u = u0 + r, c0 = W * (warp >> 2);
+    const QueryView view{p.q, p.up, p.lse2, p.dsum, b, p.Hq, kvh * p.g, ch.kt, nq, first, first + T / 2, p.N, p.Npad, p.window, p.sinks};
+    float* part = p.part + ((size_t)plane * p.partials + ch.slot + ch.idx) * (2 * TILE * HD) + r * HD + c0;
+    Columns<bf16, W> dk, dv;
+    dk.look(row_ptr_w<bf16>(p.dk, b, kvh, u) + c0, ch.n == 1 ? nullptr : part);
+    dv.look(row_ptr_w<bf16>(p.dv, b, kvh, u) + c0, ch.n == 1 ? nullptr : part + TILE * HD);
+    mend_dkv_row<bf16, HD, W, TILE>(view, u, row_ptr<bf16>(p.k, b, kvh, u), row_ptr<bf16>(p.v, b, kvh, u), dk, dv, c0, p.c, p.scale);
   }
 }
 
@@ -402,7 +424,7 @@ template <int HD>
 __global__ void __launch_bounds__(NTHREADS, 1)
     win_bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
-                         const __grid_constant__ BwdParams p) {
+                         const __grid_constant__ CUtensorMap tmKs, const __grid_constant__ BwdParams p) {
   using C = DqCfg<HD>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (misaligned(smem, p.status)) return;
@@ -446,6 +468,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint8_t* sK = smem + C::OFF_K;
   uint8_t* sV = smem + C::OFF_V;
 
+  bool again = false;  // the warp stored rows that are not finite
   const int planes = p.B * p.Hq, items = planes * p.NT;
   // The longest rows first; the heads of a group side by side, so that they share K and V in L2.
   auto item = [&](int i) {
@@ -478,7 +501,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           const int u0 = I.kt.tile(j) * TILE, ik = (int)(n % C::NSK), iv = (int)(n % C::NSV);
           if (n >= C::NSK && !(ok = mbar_wait(&M.k_empty[ik], (n / C::NSK - 1) & 1u, abort))) break;
           mbar_expect_tx(&M.k_full[ik], C::TB);
-          load_tile<HD>(sK + ik * C::TB, &tmK, &M.k_full[ik], u0, I.kvh, I.b, p.zk, HALF);
+          // a sink tile's K through a map that ends at the sinks: no query of the item sees its other keys
+          load_tile<HD>(sK + ik * C::TB, j < I.kt.ns ? &tmKs : &tmK, &M.k_full[ik], u0, I.kvh, I.b, p.zk, HALF);
           kn = n + 1;
           if (n >= C::NSV && !(ok = mbar_wait(&M.v_empty[iv], (n / C::NSV - 1) & 1u, abort))) break;
           mbar_expect_tx(&M.v_full[iv], C::TB);
@@ -551,6 +575,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t aP = cP + lane_base + COLS * cg;
     uint32_t n = 0, qn = 0;
     bool ok = true;
+    float2 z = make_float2(0.f, 0.f);  // NaN behind a row that is not finite
     DqItem I = item(blockIdx.x);
     float nl, nd;  // -lse2, -D
     auto statistics = [&](const DqItem& J) {
@@ -623,13 +648,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         uint32_t r[16];
         tmem_ld16(cQ + lane_base + W * cg + c0, r);
         tmem_wait_ld();
-        if (t < p.N) store16(row_ptr_w<bf16>(p.dq, I.b, I.h, t) + W * cg + c0, r, p.scale, p.wide_q);
+        if (t < p.N) {
+          look16(z, r);
+          store16(row_ptr_w<bf16>(p.dq, I.b, I.h, t) + W * cg + c0, r, p.scale, p.wide_q);
+        }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&M.dq_free);
       I = J;
     }
+    again = __any_sync(0xffffffffu, z.x + z.y != 0.f) && ok;
   }
   tc_fence_before();
   __syncthreads();
@@ -638,6 +667,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+  // They are formed once more (win_rows.cuh).
+  for (int i = blockIdx.x; again && i < items; i += gridDim.x) {
+    constexpr int W = HD / 4;
+    const DqItem I = item(i);
+    const KeyRows<bf16> keys{p.k, p.v, I.b, I.kvh, nullptr, 0, 0, 0};
+    const int ta = I.t0 + (warp & 3) * 32, c0 = W * (warp >> 2);
+    for (int t = ta; t < min(ta + 32, p.N); ++t) {
+      const int64_t o = ((int64_t)I.b * p.Hq + I.h) * p.Npad + t;
+      const RowView view{I.kt, t, 0, I.kt.count, p.window, p.sinks, p.N};
+      mend_dq_row<bf16, HD, W, TILE>(keys, view, row_ptr<bf16>(p.q, I.b, I.h, t), row_ptr<bf16>(p.up, I.b, I.h, t),
+                                     row_ptr_w<bf16>(p.dq, I.b, I.h, t) + c0, c0, p.c, p.lse2[o], p.dsum[o], p.scale);
+    }
   }
 }
 
@@ -655,10 +697,11 @@ template <int HD>
 cudaError_t launch(const WinDims& D, const WinBwdArgs& a, int32_t* status, cudaStream_t st) {
   BwdParams p{};
   // Boxes of 128 rows, and of 64 for the units of queries.
-  CUtensorMap q, k, v, g, qu, gu;
+  CUtensorMap q, k, ks, v, g, qu, gu;
   auto map = [&](CUtensorMap* m, const TensorRef& t, int H, int rows, int* zero) {
     return win_tma_map(m, t, D.B, H, D.N, rows, HD, zero);
   };
+  if (!win_tma_map(&ks, a.k, D.B, D.Hkv, D.sinks > 0 ? D.sinks : D.N, TILE, HD, &p.zk)) return cudaErrorInvalidValue;
   if (!map(&q, a.q, D.Hq, TILE, &p.zq) || !map(&g, a.g, D.Hq, TILE, &p.zg) || !map(&k, a.k, D.Hkv, TILE, &p.zk) ||
       !map(&v, a.v, D.Hkv, TILE, &p.zv) || !map(&qu, a.q, D.Hq, UNIT, &p.zq) || !map(&gu, a.g, D.Hq, UNIT, &p.zg))
     return cudaErrorInvalidValue;
@@ -667,6 +710,10 @@ cudaError_t launch(const WinDims& D, const WinBwdArgs& a, int32_t* status, cudaS
   const WinBwdLayout L = win_bwd_layout(D);
   const ChunkPlan cp = chunk_plan<TILE>(D, kBwdChunks, kTcMinSteps);
   char* ws = static_cast<char*>(a.ws);
+  p.q = a.q;
+  p.k = a.k;
+  p.v = a.v;
+  p.up = a.g;
   p.dq = a.dq;
   p.dk = a.dk;
   p.dv = a.dv;
@@ -697,7 +744,7 @@ cudaError_t launch(const WinDims& D, const WinBwdArgs& a, int32_t* status, cudaS
   auto dq = win_bwd_dq_tc_kernel<HD>;
   if ((e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, dq_smem<HD>())) != cudaSuccess) return e;
   const int64_t items = (int64_t)D.B * D.Hq * cp.NT;
-  return launch_ahead(dq, dim3((unsigned)(items < kCtas ? items : kCtas)), NTHREADS, dq_smem<HD>(), st, q, k, v, g, p);
+  return launch_ahead(dq, dim3((unsigned)(items < kCtas ? items : kCtas)), NTHREADS, dq_smem<HD>(), st, q, k, v, g, ks, p);
 }
 
 }  // namespace

@@ -583,11 +583,17 @@ __device__ __forceinline__ void add_groups(float (&acc)[HD / 8][4], float* buf, 
     }
 }
 
+// Returns whether a stored value is not finite.
 template <int HD>
-__device__ __forceinline__ void store_rows(float* row, const float (&acc)[HD / 8][4], int i, int t, float mul) {
+__device__ __forceinline__ bool store_rows(float* row, const float (&acc)[HD / 8][4], int i, int t, float mul) {
+  float z = 0.f;
 #pragma unroll
-  for (int n = 0; n < HD / 8; ++n)
-    *reinterpret_cast<float2*>(row + 8 * n + 2 * t) = make_float2(acc[n][2 * i] * mul, acc[n][2 * i + 1] * mul);
+  for (int n = 0; n < HD / 8; ++n) {
+    const float2 y = make_float2(acc[n][2 * i] * mul, acc[n][2 * i + 1] * mul);
+    *reinterpret_cast<float2*>(row + 8 * n + 2 * t) = y;
+    z = fmaf(y.x, 0.f, fmaf(y.y, 0.f, z));
+  }
+  return z != 0.f;
 }
 
 template <int HD>
@@ -626,8 +632,12 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dq_f32_kernel(F32Bwd p
   __syncthreads();
   for (int j = grp; j < kt.count; j += 2) {
     const int u0 = kt.tile(j) * BT;
+    // keys that no query of the tile sees are not read
     auto key = [&](const TensorRef& x) {
-      return [&, x](int r) -> const float* { return u0 + r < p.N ? row_ptr<float>(x, b, kvh, u0 + r) : nullptr; };
+      return [&, x](int r) -> const float* {
+        const int u = u0 + r;
+        return u < q0 + nrows && (u > q0 - p.window || u < p.sinks) ? row_ptr<float>(x, b, kvh, u) : nullptr;
+      };
     };
     copy_rows<HD, PD>(sK, p.q.p, tid, GROUP, key(p.k));
     copy_rows<HD, PA>(sV, p.q.p, tid, GROUP, key(p.v));
@@ -655,10 +665,21 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dq_f32_kernel(F32Bwd p
     group_sync(grp);  // K and V are read
   }
   add_groups<HD>(acc, sG + BT * PA, grp, r0, t);
+  bool again = false;
   if (grp == 0)
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (r0 + 8 * i < nrows) store_rows<HD>(row_ptr_w<float>(p.dq, b, h, q0 + r0 + 8 * i), acc, i, t, p.scale);
+      if (r0 + 8 * i < nrows) again |= store_rows<HD>(row_ptr_w<float>(p.dq, b, h, q0 + r0 + 8 * i), acc, i, t, p.scale);
+  // rows that are not finite once more (win_rows.cuh)
+  if (!__syncthreads_or(again)) return;
+  const KeyRows<float> keys{p.k, p.v, b, kvh, nullptr, 0, 0, 0};
+  for (int r = threadIdx.x >> 5; r < nrows; r += BWD_THREADS / 32) {
+    const int q = q0 + r;
+    const int64_t o = ((int64_t)b * p.Hq + h) * p.Npad + q;
+    const RowView view{kt, q, 0, kt.count, p.window, p.sinks, p.N};
+    mend_dq_row<float, HD, HD, BT>(keys, view, row_ptr<float>(p.q, b, h, q), row_ptr<float>(p.g, b, h, q),
+                                   row_ptr_w<float>(p.dq, b, h, q), 0, p.c, p.lse2[o], p.dsum[o], p.scale);
+  }
 }
 
 template <int HD>
@@ -730,20 +751,34 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dkv_f32_kernel(F32Bwd 
   }
   add_groups<HD>(dk, sV + BT * PA, grp, r0, t);
   add_groups<HD>(dv, sV + BT * PA, grp, r0, t);
+  // row `r` of the key tile in the chunk's partials
+  auto partial = [&](int r) { return p.part + ((size_t)plane * p.partials + ch.slot + ch.idx) * (2 * BT * HD) + r * HD; };
+  bool again = false;
   if (grp == 0)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int u = u0 + r0 + 8 * i;
       if (u >= p.N) continue;
       if (ch.n == 1) {
-        store_rows<HD>(row_ptr_w<float>(p.dk, b, kvh, u), dk, i, t, p.scale);
-        store_rows<HD>(row_ptr_w<float>(p.dv, b, kvh, u), dv, i, t, 1.0f);
+        again |= store_rows<HD>(row_ptr_w<float>(p.dk, b, kvh, u), dk, i, t, p.scale);
+        again |= store_rows<HD>(row_ptr_w<float>(p.dv, b, kvh, u), dv, i, t, 1.0f);
       } else {
-        float* base = p.part + ((size_t)plane * p.partials + ch.slot + ch.idx) * (2 * BT * HD) + (r0 + 8 * i) * HD;
-        store_rows<HD>(base, dk, i, t, 1.0f);
-        store_rows<HD>(base + BT * HD, dv, i, t, 1.0f);
+        float* base = partial(r0 + 8 * i);
+        again |= store_rows<HD>(base, dk, i, t, 1.0f);
+        again |= store_rows<HD>(base + BT * HD, dv, i, t, 1.0f);
       }
     }
+  // rows that are not finite once more (win_rows.cuh)
+  if (!__syncthreads_or(again)) return;
+  const QueryView view{p.q, p.g, p.lse2, p.dsum, b, p.Hq, kvh * p.grp, ch.kt, nq, first, last, p.N, p.Npad, p.window, p.sinks};
+  for (int r = threadIdx.x >> 5; r < BT && u0 + r < p.N; r += BWD_THREADS / 32) {
+    const int u = u0 + r;
+    Columns<float, HD> ck, cv;
+    const bool fk = ck.look(row_ptr_w<float>(p.dk, b, kvh, u), ch.n == 1 ? nullptr : partial(r));
+    const bool fv = cv.look(row_ptr_w<float>(p.dv, b, kvh, u), ch.n == 1 ? nullptr : partial(r) + BT * HD);
+    if (!__all_sync(0xffffffffu, fk && fv))
+      mend_dkv_row<float, HD, HD, BT>(view, u, row_ptr<float>(p.k, b, kvh, u), row_ptr<float>(p.v, b, kvh, u), ck, cv, 0, p.c, p.scale);
+  }
 }
 
 // Joins the chunks of one key tile in order: grid (key tiles that may be cut, planes, parts of a tile's rows).  Bound by

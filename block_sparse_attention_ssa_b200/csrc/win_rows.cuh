@@ -183,4 +183,138 @@ __device__ __forceinline__ void mend_row(const KeyRows<T>& keys, const RowView& 
     }
 }
 
+// ---------------------------------------------------------------- gradients
+// W columns of a gradient's row: which are not finite, and their sums over the visible pairs.
+template <typename T, int W>
+struct Columns {
+  static constexpr int NC = (W + 31) / 32;
+  float acc[NC];
+  bool write[NC], done[NC];  // done: needs nothing, or NaN from a visible pair
+  T* out;
+  float* part;  // fp32 partials; one of the two is null
+  // Both begin at the first column.  Returns whether the lane's columns are all finite.
+  __device__ __forceinline__ bool look(T* out_, float* part_) {
+    out = out_;
+    part = part_;
+    bool fine = true;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      const int c = (threadIdx.x & 31) + 32 * n;
+      acc[n] = 0.f;
+      done[n] = c >= W || is_finite(part != nullptr ? part[c] : to_f32(out[c]));
+      write[n] = !done[n];
+      fine &= done[n];
+    }
+    return fine;
+  }
+  __device__ __forceinline__ void add(float w, const T* x) {
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+      if (!done[n]) acc[n] = fmaf(w, to_f32(x[(threadIdx.x & 31) + 32 * n]), acc[n]);
+  }
+  // Whether nothing is left to add in this lane.
+  __device__ __forceinline__ bool settled() {
+    bool all = true;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) all &= (done[n] |= acc[n] != acc[n]);
+    return all;
+  }
+  __device__ __forceinline__ void store(float mul) {
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+      if (write[n]) {
+        const int c = (threadIdx.x & 31) + 32 * n;
+        if (part != nullptr) part[c] = acc[n];
+        else out[c] = from_f32<T>(acc[n] * mul);
+      }
+  }
+};
+
+// Columns c0 .. c0 + W - 1 of a query's dQ, where they are not finite:
+//   scale sum_u p (g . v_u + nd) k_u, p = 2^(c q . k_u + nl),
+// over the keys u that it sees (nl: -lse in base 2, nd: -D).  q, g begin at the row, out at c0.  As above, the bf16 form
+// goes through the row's keys only where a hidden one holds such values.  Warp-wide.
+template <typename T, int HD, int W, int KT>
+__device__ __forceinline__ void mend_dq_row(const KeyRows<T>& keys, const RowView& r, const T* q, const T* g, T* out, int c0, float c,
+                                            float nl, float nd, float scale) {
+  const int lane = threadIdx.x & 31;
+  Columns<T, W> dq;
+  // with a NaN in either statistic all of the row's weights are NaN
+  if (__all_sync(0xffffffffu, dq.look(out, nullptr)) || nl != nl || nd != nd) return;
+  if (!std::is_same_v<T, float>) {
+    bool hidden = false;
+    for (int j = r.first; j < r.last; ++j) {
+      const int u0 = r.kt.tile(j) * KT;
+      if (u0 + KT - 1 <= r.t && (r.t - u0 < r.window || u0 + KT <= r.sinks)) continue;
+      for (int u = u0 + lane; u < u0 + KT && u < r.N; u += 32)
+        if (!sees(r.t, u, r.window, r.sinks)) hidden |= spoiled<T, W>(keys.at(keys.k, u) + c0);
+    }
+    if (!__any_sync(0xffffffffu, hidden)) return;
+  }
+  for_keys<T, KT>(keys, r, [&](int u0, const T* k) {
+    const float w = k != nullptr ? exp2f(fmaf(dot_row<T, HD>(q, k), c, nl)) * (dot_row<T, HD>(g, keys.at(keys.v, u0 + lane)) + nd) : 0.f;
+    for (unsigned rest = __ballot_sync(0xffffffffu, k != nullptr); rest; rest &= rest - 1) {
+      const int i = __ffs(rest) - 1;
+      dq.add(__shfl_sync(0xffffffffu, w, i), keys.at(keys.k, u0 + i) + c0);
+    }
+    return !__all_sync(0xffffffffu, dq.settled());
+  });
+  dq.store(scale);
+}
+
+// Steps first .. last - 1 of key tile kt's queries (head h0 + s / nq, the nq query tiles of QT tokens from tile kt on).
+struct QueryView {
+  TensorRef q, g;
+  const float *nl, *nd;  // -lse in base 2, -D: rows of Npad
+  int b, Hq, h0, kt, nq, first, last, N, Npad, window, sinks;
+};
+
+// Columns c0 .. c0 + W - 1 of key u's dK and dV over those steps, where they are not finite:
+//   scale sum_t p (g_t . v + nd_t) q_t and sum_t p g_t over the queries t that see u.
+// k, v begin at the row; dk and dv look at their columns already.
+template <typename T, int HD, int W, int QT>
+__device__ __forceinline__ void mend_dkv_row(const QueryView& r, int u, const T* k, const T* v, Columns<T, W>& dk, Columns<T, W>& dv,
+                                             int c0, float c, float scale) {
+  const int lane = threadIdx.x & 31;
+  // f(h, t0) for each 32 queries until it returns false
+  auto for_queries = [&](auto f) {
+    for (int s = r.first; s < r.last; ++s)
+      for (int i = 0; i < QT; i += 32) {
+        const int t0 = (r.kt + s % r.nq) * QT + i;
+        if (t0 >= r.N) break;
+        if (!f(r.h0 + s / r.nq, t0)) return;
+      }
+  };
+  auto at = [&](const TensorRef& x, int h, int t) { return row_ptr<T>(x, r.b, h, t); };
+  if (!std::is_same_v<T, float>) {
+    bool hidden = false;
+    for_queries([&](int h, int t0) {
+      const int t = t0 + lane;
+      if (t < r.N && !sees(t, u, r.window, r.sinks))
+        hidden |= spoiled<T, W>(at(r.q, h, t) + c0) || spoiled<T, W>(at(r.g, h, t) + c0);
+      return !__any_sync(0xffffffffu, hidden);
+    });
+    if (!__any_sync(0xffffffffu, hidden)) return;
+  }
+  for_queries([&](int h, int t0) {
+    const int t = t0 + lane;
+    const bool see = t < r.N && sees(t, u, r.window, r.sinks);
+    float p = 0.f, dx = 0.f;
+    if (see) {
+      const int64_t o = ((int64_t)r.b * r.Hq + h) * r.Npad + t;
+      p = exp2f(fmaf(dot_row<T, HD>(at(r.q, h, t), k), c, r.nl[o]));
+      dx = p * (dot_row<T, HD>(at(r.g, h, t), v) + r.nd[o]);
+    }
+    for (unsigned rest = __ballot_sync(0xffffffffu, see); rest; rest &= rest - 1) {
+      const int i = __ffs(rest) - 1;
+      dk.add(__shfl_sync(0xffffffffu, dx, i), at(r.q, h, t0 + i) + c0);
+      dv.add(__shfl_sync(0xffffffffu, p, i), at(r.g, h, t0 + i) + c0);
+    }
+    const bool a = dk.settled(), b = dv.settled();
+    return !__all_sync(0xffffffffu, a && b);
+  });
+  dk.store(scale);
+  dv.store(1.f);
+}
+
 }  // namespace ssa

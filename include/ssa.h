@@ -403,10 +403,8 @@ SSA_API ssa_status_t ssa_fwd_window(const ssa_window_dims_t* dims, const ssa_ten
  *   Q, K, V, h, lse: as passed to / written by ssa_fwd_window.
  *   g [B, Hq, N, d] dims->dtype (in, required).
  *   dQ [B, Hq, N, d], dK, dV [B, Hkv, N, d] (out): fully overwritten.
- *   A NaN or an infinity in a row of Q, K or g may also reach gradients of
- *     tokens that it has no pair with but that share a tile with such a pair
- *     (a weight of zero times it).  In fp32 magnitudes from 3.4019e38 on (where
- *     rounding to TF32 overflows) count as infinities.
+ *   Pairs that are hidden do not count, NaN and infinities in their rows of
+ *     Q, K, V, h, lse and g included.
  *   ws: at least ssa_window_workspace_bytes(dims) bytes, 256-byte aligned. */
 SSA_API ssa_status_t ssa_bwd_window(const ssa_window_dims_t* dims, const ssa_tensor_t* Q, const ssa_tensor_t* K,
                                     const ssa_tensor_t* V, const ssa_tensor_t* h, const float* lse,

@@ -129,6 +129,26 @@ def test_window_forward_fp32(name, what):
     _window_case(name, "f32", FP32[what], train=False)
 
 
+BACKWARD = {
+    # rows that fill a padded batch, with gradients and without
+    "tail": lambda N: [("V", (slice(None), slice(N - 3, None)), NAN), ("K", (slice(None), slice(N - 2, None)), NAN),
+                       ("Q", (slice(None), slice(N - 2, None)), NAN), ("g", (slice(None), slice(N - 3, None)), NAN)],
+    "tail_of_inputs": lambda N: [("K", (slice(None), slice(N - 2, None)), NAN), ("Q", (slice(None), slice(N - 1, None)), NAN)],
+    # a key behind the sinks, a late token whose gradient the sinks get
+    "behind_the_sinks": lambda N: [("K", (0, 100), NAN), ("g", (1, N - 40), NAN)],
+    "a_late_query": lambda N: [("Q", (0, N - 70), NAN)],
+    "one_element": lambda N: [("K", (0, 131, 7), NAN), ("g", (0, 210, 3), INF), ("g", (2, 140, 9), NAN)],
+    "a_value": lambda N: [("V", (0, 150, 20), NAN)],
+}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("what", list(BACKWARD))
+@pytest.mark.parametrize("name", list(SHAPES))
+def test_window_backward(name, what, dtype):
+    _window_case(name, dtype, BACKWARD[what], train=True)
+
+
 # new tokens, tokens in all, Hq, Hkv, d, page; then V rows that are spoiled: (sequence, position)
 PAGED = {
     "chunks": (([70, 1, 129, 5], [500, 33, 129, 1111], 8, 2, 128, 16), [(0, 450), (0, 499), (2, 60), (3, 1107), (3, 300)]),
