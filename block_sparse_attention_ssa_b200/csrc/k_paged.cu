@@ -8,47 +8,59 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 
-// The sequence that holds packed row `row` (its first row at most `row`, the next
-// sequence's above it): -1 for rows behind the last one.
-__device__ __forceinline__ int seq_of_row(const int32_t* q_start, int seqs, int row) {
-  int lo = 0, hi = seqs;  // q_start[lo] <= row < q_start[hi] once both ends hold
-  if (row < q_start[0] || row >= q_start[seqs]) return -1;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (q_start[mid] <= row) lo = mid; else hi = mid;
-  }
-  return lo;
-}
-
 // Append: one pass over the new rows in 16-byte pieces.  A CTA takes ROWS packed tokens
-// (all kv heads); a thread finds a token's page row once, then the CTA copies.  Bound by
+// (all kv heads); a warp finds a token's sequence and page row, then the CTA copies.  Bound by
 // memory (or by the launch, for single tokens): 4 row lengths of traffic a token and head; 16384
 // tokens of 8 heads, d = 128, bf16 (90 MB) take 16.1 us, 5.6 TB/s.
 constexpr int AROWS = 8;
 __global__ void __launch_bounds__(256) paged_append_kernel(PagedArgs a, PagedDims D, int vecs, int es) {
   __shared__ int64_t page_of[AROWS];
   __shared__ int slot_of[AROWS];
-  const int row0 = blockIdx.x * AROWS;
-  if (threadIdx.x < AROWS) {
-    const int row = row0 + threadIdx.x;
+  const int row0 = blockIdx.x * AROWS, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  static_assert(AROWS == 8, "a row for each warp");
+  const int row = row0 + w;
+  // The first entry above the row ends its sequence, the largest one before it begins it (entries may fall: all are
+  // looked at, 256 in flight, each with the length of the sequence that it ends; -1 behind the last one).
+  constexpr int U = 8;
+  int end = row < D.T ? -1 : 0, begin = -1;  // end: the entry's number, -1 while not found
+  int last = 0, len = 0;                     // its value and length
+  for (int i0 = 0; end < 0 && i0 <= D.seqs; i0 += 32 * U) {
+    int q[U], n[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (i0 + 32 * k > D.seqs) break;
+      const int i = i0 + 32 * k + lane;
+      q[k] = i <= D.seqs ? clamp_row(a.q_start[i], D.T) : -1;
+      n[k] = i <= D.seqs && i > 0 ? a.kv_len[i - 1] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (end >= 0 || i0 + 32 * k > D.seqs) break;
+      const unsigned above = __ballot_sync(0xffffffffu, q[k] > row);
+      const int f = above ? __ffs(above) - 1 : 32;
+      if (above) {
+        end = i0 + 32 * k + f;
+        last = __shfl_sync(0xffffffffu, q[k], f);
+        len = __shfl_sync(0xffffffffu, n[k], f);
+      }
+      begin = max(begin, __reduce_max_sync(0xffffffffu, lane < f ? q[k] : -1));
+    }
+  }
+  if (lane == 0) {
     int64_t pg = -1;
     int slot = 0;
-    if (row < D.T) {
-      const int b = seq_of_row(a.q_start, D.seqs, row);
-      if (b >= 0) {
-        const Seq s = load_seq(a.q_start, a.kv_len, b, D.T, D.max_pages * D.page);
-        const int pos = s.len - s.n + (row - s.q0);
-        if (pos >= 0 && row - s.q0 < s.n) {
-          const int id = a.table[(int64_t)b * D.max_pages + pos / D.page];
-          if ((unsigned)id < (unsigned)D.num_pages) {
-            pg = id;
-            slot = pos % D.page;
-          }
+    if (end > 0) {
+      const int pos = min(max(len, 0), D.max_pages * D.page) - (last - begin) + (row - begin);
+      if (pos >= 0) {
+        const int id = a.table[(int64_t)(end - 1) * D.max_pages + pos / D.page];
+        if ((unsigned)id < (unsigned)D.num_pages) {
+          pg = id;
+          slot = pos % D.page;
         }
       }
     }
-    page_of[threadIdx.x] = pg;
-    slot_of[threadIdx.x] = slot;
+    page_of[w] = pg;
+    slot_of[w] = slot;
   }
   __syncthreads();
   const int per_row = D.Hkv * vecs;
@@ -87,7 +99,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, Batch batc
     if (u0 < U) {
       const Place at = batch.locate<KT>(u1 - 1);
       const long long begin = u1 - 1 - at.off;
-      cut.s = load_seq(batch.q_start, batch.kv_len, at.b, T_, batch.cap);
+      cut.s = load_seq(batch.q_start, batch.kv_len, at.b, at.q0, T_, batch.cap);
       cut.i0 = at.run * batch.TI;
       cut.kvh = at.kvh;
       const int units = max(1, run_tiles<KT>(cut.s, cut.i0, batch.TI, batch.window, batch.sinks).count);

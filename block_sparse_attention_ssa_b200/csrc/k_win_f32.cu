@@ -208,7 +208,7 @@ template <bool PAGED>
 __device__ __forceinline__ F32Item item_of(const F32Params& p, const Place& at, int left) {
   F32Item I;
   if (PAGED) {
-    const Seq s = load_seq(p.batch.q_start, p.batch.kv_len, at.b, p.T, p.batch.cap);
+    const Seq s = load_seq(p.batch.q_start, p.batch.kv_len, at.b, at.q0, p.T, p.batch.cap);
     const int i0 = at.run * p.batch.TI;
     I.b = at.b;
     I.kvh = at.kvh;
@@ -246,8 +246,9 @@ __device__ __forceinline__ bool next_item(const F32Params& p, Place& at, int& le
     at.kvh = 0;
     ++at.run;
     while (at.b < p.batch.seqs) {
-      const Seq s = load_seq(p.batch.q_start, p.batch.kv_len, at.b, p.T, p.batch.cap);
+      const Seq s = load_seq(p.batch.q_start, p.batch.kv_len, at.b, at.q0, p.T, p.batch.cap);
       if (at.run * p.batch.TI < s.n) break;
+      at.q0 += s.n;
       at.run = 0;
       ++at.b;
     }
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(Fwd<HD>::THREADS, 1) win_fwd_f32_kernel(F32Par
   __shared__ int sh_left;
   __shared__ float sh_m[C::GROUPS][BT], sh_l[C::GROUPS][BT];
 
-  Place at{0, 0, 0, 0};
+  Place at{0, 0, 0, 0, 0};
   int left = 1;
   bool again = false;  // rows that are not finite were stored (a store to shared memory there held up the next row: 97 us for 92)
   if (PAGED) {
@@ -492,7 +493,7 @@ __global__ void __launch_bounds__(Fwd<HD>::THREADS, 1) win_fwd_f32_kernel(F32Par
     if (!next_item(p, at, left, take)) break;
     __syncthreads();  // shared memory is read to the end
   }
-  if (__syncthreads_or(again)) form_again<HD, PAGED>(p, PAGED ? sh_place : Place{0, 0, 0, 0}, PAGED ? sh_left : 1);
+  if (__syncthreads_or(again)) form_again<HD, PAGED>(p, PAGED ? sh_place : Place{0, 0, 0, 0, 0}, PAGED ? sh_left : 1);
 }
 
 // ================================================================ backward

@@ -156,7 +156,7 @@ struct Walk {
     int toks, cap;
     if (PAGED) {
       if (left <= 0 || at.b >= p.batch.seqs) return false;
-      const Seq q = load_seq(p.batch.q_start, p.batch.kv_len, at.b, p.batch.T, p.batch.cap);
+      const Seq q = load_seq(p.batch.q_start, p.batch.kv_len, at.b, at.q0, p.batch.T, p.batch.cap);
       const int i0 = at.run * p.batch.TI;
       toks = min(p.batch.TI, q.n - i0);
       cap = p.TQ;
@@ -196,8 +196,9 @@ struct Walk {
         at.kvh = 0;
         ++at.run;
         while (at.b < p.batch.seqs) {
-          const Seq q = load_seq(p.batch.q_start, p.batch.kv_len, at.b, p.batch.T, p.batch.cap);
+          const Seq q = load_seq(p.batch.q_start, p.batch.kv_len, at.b, at.q0, p.batch.T, p.batch.cap);
           if (at.run * p.batch.TI < q.n) break;
+          at.q0 += q.n;
           at.run = 0;
           ++at.b;
         }
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const long long per = share(U, (int)gridDim.x);
     const long long u0 = per * blockIdx.x;
     const long long n = u0 < U ? (U - u0 < per ? U - u0 : per) : 0;
-    Place at{p.batch.seqs, 0, 0, 0};
+    Place at{p.batch.seqs, 0, 0, 0, 0};
     if (n > 0) at = p.batch.locate<TILE>(u0);
     if (lane == 0) {
       M.at = at;

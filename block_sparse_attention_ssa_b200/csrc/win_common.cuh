@@ -119,13 +119,14 @@ struct Seq {
   int q0, n, len;  // first packed row, new tokens, tokens in the cache
 };
 
-__device__ __forceinline__ Seq load_seq(const int32_t* q_start, const int32_t* kv_len, int b, int T, int cap) {
+// q_start counts as the running maximum of its values clamped to 0 .. T, so that no row has two sequences.
+__device__ __forceinline__ int clamp_row(int x, int T) { return min(max(x, 0), T); }
+
+// Sequence b; q0: the running maximum up to its own entry (the sequences before it end there).
+__device__ __forceinline__ Seq load_seq(const int32_t* q_start, const int32_t* kv_len, int b, int q0, int T, int cap) {
   Seq s;
-  // Two neighbours read the same clamped running maximum only through q_start
-  // itself: a decreasing pair gives an empty sequence.
-  const int a = min(max(q_start[b], 0), T), e = min(max(q_start[b + 1], 0), T);
-  s.q0 = a;
-  s.n = max(e - a, 0);
+  s.q0 = q0;
+  s.n = max(clamp_row(q_start[b + 1], T) - q0, 0);
   s.len = min(max(kv_len[b], 0), cap);
   return s;
 }
@@ -146,6 +147,7 @@ __device__ __forceinline__ long long seq_units(const Seq& s, int TI, int window,
 struct Place {
   int b, run, kvh;  // b = seqs: past the end
   int off;          // unit within the item
+  int q0;           // first row of sequence b
 };
 
 // Warp-wide: all 32 lanes call it with the same arguments.
@@ -154,18 +156,39 @@ struct Batch {
   const int32_t* kv_len;
   int seqs, T, cap, TI, window, sinks, Hkv;
 
+  // Lane i's sequence b0 + i (none behind the last one).  `top`: -1 while no entry has fallen (each one is then its own
+  // maximum), from then on the maximum before b0 + 32.
+  __device__ __forceinline__ Seq lane_seq(int b0, int& top) const {
+    const int lane = threadIdx.x & 31, b = b0 + lane;
+    int a = 0, e = 0, len = 0;
+    if (b < seqs) {
+      a = clamp_row(q_start[b], T);
+      e = clamp_row(q_start[b + 1], T);
+      len = min(max(kv_len[b], 0), cap);
+    }
+    if (top >= 0 || __any_sync(0xffffffffu, e < a)) {
+      if (top < 0) top = __shfl_sync(0xffffffffu, a, 0);
+#pragma unroll 1
+      for (int o = 1; o < 32; o <<= 1) e = max(e, __shfl_up_sync(0xffffffffu, e, o));
+      e = max(e, top);
+      a = __shfl_up_sync(0xffffffffu, e, 1);
+      if (lane == 0) a = top;
+      top = __shfl_sync(0xffffffffu, e, 31);
+      if (b >= seqs) e = a;
+    }
+    return Seq{a, e - a, len};
+  }
+
   template <int KT>
-  __device__ long long lane_units(int b) const {
-    if (b >= seqs) return 0;
-    const Seq s = load_seq(q_start, kv_len, b, T, cap);
+  __device__ __forceinline__ long long units_of(const Seq& s) const {
     return s.n > 0 ? seq_units<KT>(s, TI, window, sinks) * Hkv : 0;
   }
 
   template <int KT>
   __device__ long long total() const {
-    const int lane = threadIdx.x & 31;
     long long u = 0;
-    for (int b = lane; b < seqs; b += 32) u += lane_units<KT>(b);
+    int top = -1;
+    for (int b0 = 0; b0 < seqs; b0 += 32) u += units_of<KT>(lane_seq(b0, top));
 #pragma unroll
     for (int o = 16; o; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
     return u;
@@ -176,9 +199,11 @@ struct Batch {
   __device__ Place locate(long long at) const {
     const int lane = threadIdx.x & 31;
     long long before = 0;
-    Place p{seqs, 0, 0, 0};
+    int top = -1;
+    Place p{seqs, 0, 0, 0, 0};
     for (int b0 = 0; b0 < seqs; b0 += 32) {
-      const long long mine = lane_units<KT>(b0 + lane);
+      const Seq own = lane_seq(b0, top);
+      const long long mine = units_of<KT>(own);
       long long incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -190,7 +215,8 @@ struct Batch {
         const int src = __ffs(hit) - 1;
         long long rest = at - (before + __shfl_sync(0xffffffffu, incl - mine, src));
         p.b = b0 + src;
-        const Seq s = load_seq(q_start, kv_len, p.b, T, cap);
+        p.q0 = __shfl_sync(0xffffffffu, own.q0, src);
+        const Seq s{p.q0, __shfl_sync(0xffffffffu, own.n, src), __shfl_sync(0xffffffffu, own.len, src)};
         for (int i0 = 0; i0 < s.n; i0 += TI) {
           const int u = max(1, run_tiles<KT>(s, i0, TI, window, sinks).count);
           if (rest < (long long)u * Hkv) {

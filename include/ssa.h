@@ -428,8 +428,9 @@ SSA_API ssa_status_t ssa_bwd_window(const ssa_window_dims_t* dims, const ssa_ten
  *     page), so that both [num_pages, page, Hkv, d] and [num_pages, Hkv, page,
  *     d] memory will do.
  * Values out of range on the device read and write nothing out of range:
- * q_start is clamped to 0 .. total_q (a decreasing pair is a sequence without
- * new tokens), kv_len to 0 .. max_pages * page, and a page id outside
+ * q_start is clamped to 0 .. total_q and counts as its running maximum (an
+ * entry below an earlier one ends a sequence without new tokens, and no row
+ * belongs to two), kv_len to 0 .. max_pages * page, and a page id outside
  * 0 .. num_pages - 1 holds no keys (append skips it, attention masks its
  * positions).  Page ids that no
  * token sees (behind the window, past kv_len) are not looked at. */

@@ -306,3 +306,60 @@ def test_cache_past_32_bit_offsets():
     small = [np.nan_to_num(np.where(np.arange(3 * page).reshape(3, page, 1, 1) < L, c, 0.0)) for c in small]
     r = W.paged(q[-n:].double().numpy(), *small, [0, n], [L], np.array([[0, 1, 2]]), page, api.EVERYTHING, 0, 1 / math.sqrt(d), "bf16")
     within("h", out["h"], r["h"], r["tol_h"])
+
+
+STARTS = {
+    "as_meant": [0, 9, 11, 24, 24, 30],
+    "last_falls": [0, 10, 3, 3, 3, 3],
+    "falls_and_rises": [0, 5, 2, 17, 9, 30],
+    "first_behind_zero": [4, 4, 1, 20, 6, 10**9],
+    "negative": [-7, 12, -1, 12, 2**31 - 1, 0],
+    "all_behind": [2**31 - 1, 0, 5, 7, 20, 30],
+    "long": None,
+}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", list(STARTS))
+def test_q_start_counts_as_its_running_maximum(name, dtype):
+    """Entries that fall, pass total_q or are negative: append and attention take the same rows for each sequence, and
+    no others are written, nor cache rows beside theirs."""
+    Hq, Hkv, d, page, T, starts = 4, 2, 64, 16, 30, STARTS[name]
+    if starts is None:  # a rise and a fall among thousands of entries
+        starts = list(np.minimum(np.arange(1401) // 10, 130))
+        starts[300], starts[700] = 0, 75
+        T = 140
+    S = len(starts) - 1
+    gen = torch.Generator().manual_seed(8)
+    first = np.maximum.accumulate(np.clip(np.array(starts, dtype=np.int64), 0, T))
+    lens = [int(n) + 3 + 5 * (i % 7) for i, n in enumerate(np.diff(first))]
+    lens[2] = 2  # rows at negative positions where it has more
+    cols = -(-max(lens) // page)
+    pool = S * cols + 2
+    table = torch.randperm(pool, generator=gen)[:S * cols].view(S, cols).int()
+    mk = lambda *s: torch.randn(*s, generator=gen).to(TYPES[dtype])  # noqa: E731
+    q, k, v, caches = mk(T, Hq, d), mk(T, Hkv, d), mk(T, Hkv, d), [mk(pool, page, Hkv, d) for _ in range(2)]
+    want = [c.clone() for c in caches]
+    for b in range(S):
+        n = int(first[b + 1] - first[b])
+        for i in range(max(0, n - lens[b]), n):
+            u = lens[b] - n + i
+            for c, x in zip(want, (k, v)):
+                c[table[b, u // page], u % page] = x[first[b] + i]
+    dims = api.make_paged_dims(S, T, Hq, Hkv, d, page, pool, cols, dtype=dtype)
+    ints = [torch.tensor(np.array(x), dtype=torch.int32, device="cuda") for x in (starts, lens)] + [table.cuda()]
+    got = [c.cuda() for c in caches]
+    api.ssa_paged_append(dims, k.cuda(), v.cuda(), *ints, *got)
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert torch.equal(g.cpu(), w)
+    out = {n: torch.full_like(x, 5.0) for n, x in api.alloc_paged(dims).items()}
+    api.ssa_paged_attention(dims, q.cuda(), *got, *ints, out["h"], out["lse"], api.alloc_paged_workspace(dims).fill_(255))
+    torch.cuda.synchronize()
+    assert api.ssa_device_status() == api.SSA_OK
+    r = W.paged(q.double().numpy(), *(c.double().numpy() for c in want), first, lens, table.numpy(), page, api.EVERYTHING, 0,
+                1 / math.sqrt(d), dtype)
+    own = r["own"]
+    within("h", f64(out["h"])[own], r["h"][own], r["tol_h"][own])
+    within("lse", f64(out["lse"])[:, own], r["lse"][:, own], r["tol_lse"][:, own])
+    assert np.all(f64(out["h"])[~own] == 5.0) and np.all(f64(out["lse"])[:, ~own] == 5.0)
