@@ -244,17 +244,14 @@ __device__ __forceinline__ bool next_item(const F32Params& p, Place& at, int& le
   at.off = 0;
   if (++at.kvh == p.batch.Hkv) {
     at.kvh = 0;
-    ++at.run;
-    while (at.b < p.batch.seqs) {
-      const Seq s = load_seq(p.batch.q_start, p.batch.kv_len, at.b, at.q0, p.T, p.batch.cap);
-      if (at.run * p.batch.TI < s.n) break;
-      at.q0 += s.n;
+    const Seq s = load_seq(p.batch.q_start, p.batch.kv_len, at.b, at.q0, p.T, p.batch.cap);
+    if (++at.run * p.batch.TI >= s.n) {
       at.run = 0;
-      ++at.b;
+      at.q0 += s.n;
+      at.b = p.batch.next_seq(at.b + 1, at.q0);
     }
-    if (at.b >= p.batch.seqs) return false;
   }
-  return true;
+  return at.b < p.batch.seqs;
 }
 
 // The CTA's rows once more (win_rows.cuh), those that are not finite; a warp takes every n-th row.

@@ -153,12 +153,13 @@ struct Walk {
   __device__ Walk(const TcParams& p_, const Misc& M, int s_) : p(p_), at(M.at), left(M.left), idx(blockIdx.x), seg(0), s(s_) {}
 
   __device__ bool next(Item& I) {
-    int toks, cap;
+    int toks, cap, seq_n = 0;
     if (PAGED) {
       if (left <= 0 || at.b >= p.batch.seqs) return false;
       const Seq q = load_seq(p.batch.q_start, p.batch.kv_len, at.b, at.q0, p.batch.T, p.batch.cap);
       const int i0 = at.run * p.batch.TI;
       toks = min(p.batch.TI, q.n - i0);
+      seq_n = q.n;
       cap = p.TQ;
       I.b = at.b;
       I.kvh = at.kvh;
@@ -192,15 +193,12 @@ struct Walk {
       take = min(left, I.units - at.off);
       left -= take;
       at.off = 0;
-      if (++at.kvh == p.batch.Hkv) {
+      if (left > 0 && ++at.kvh == p.batch.Hkv) {
         at.kvh = 0;
-        ++at.run;
-        while (at.b < p.batch.seqs) {
-          const Seq q = load_seq(p.batch.q_start, p.batch.kv_len, at.b, at.q0, p.batch.T, p.batch.cap);
-          if (at.run * p.batch.TI < q.n) break;
-          at.q0 += q.n;
+        if (++at.run * p.batch.TI >= seq_n) {
           at.run = 0;
-          ++at.b;
+          at.q0 += seq_n;
+          at.b = p.batch.next_seq(at.b + 1, at.q0);
         }
       }
     }

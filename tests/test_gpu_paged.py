@@ -363,3 +363,52 @@ def test_q_start_counts_as_its_running_maximum(name, dtype):
     within("h", f64(out["h"])[own], r["h"][own], r["tol_h"][own])
     within("lse", f64(out["lse"])[:, own], r["lse"][:, own], r["tol_lse"][:, own])
     assert np.all(f64(out["h"])[~own] == 5.0) and np.all(f64(out["lse"])[:, ~own] == 5.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_idle_sequences_are_passed_over(dtype):
+    """Slots without new tokens before, between and behind the others: the same bits; and behind them they take no
+    longer than before them (walked one at a time they took twice as long)."""
+    Hq, Hkv, d, page, L, idle = 32, 8, 128, 64, 600, 4000
+    cols, gen = -(-L // page), torch.Generator().manual_seed(2)
+    pool = 4 * cols
+    Kc, Vc = (torch.randn(pool, page, Hkv, d, generator=gen).to(TYPES[dtype]).cuda() for _ in range(2))
+    q, pages = torch.randn(4, Hq, d, generator=gen).to(TYPES[dtype]).cuda(), torch.arange(pool, dtype=torch.int32).view(4, cols)
+
+    def calls(before, between, behind):
+        new = [0] * before + [1, 1] + [0] * between + [1, 1] + [0] * behind
+        S = len(new)
+        table = torch.full((S, cols), -1, dtype=torch.int32)
+        at = [i for i, n in enumerate(new) if n]
+        table[at] = pages
+        ints = [torch.tensor([0] + list(np.cumsum(new)), dtype=torch.int32).cuda(),
+                torch.full((S,), L, dtype=torch.int32).cuda(), table.cuda()]
+        dims = api.make_paged_dims(S, 4, Hq, Hkv, d, page, pool, cols, dtype=dtype)
+        out, ws = api.alloc_paged(dims), api.alloc_paged_workspace(dims)
+
+        def call():
+            api.ssa_paged_attention(dims, q, Kc, Vc, *ints, out["h"], out["lse"], ws)
+
+        call()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(5):
+                call()
+        return out, graph, (ints, ws)  # what the graph reads lives as long
+
+    plain = calls(0, 0, 0)[0]
+    runs = [calls(idle, 0, 0), calls(0, idle, 0), calls(0, 0, idle)]
+    best = [1e9] * 3
+    for _ in range(5):
+        for i, (_, graph, _) in enumerate(runs):
+            a, b = torch.cuda.Event(True), torch.cuda.Event(True)
+            a.record()
+            graph.replay()
+            b.record()
+            torch.cuda.synchronize()
+            best[i] = min(best[i], a.elapsed_time(b))
+    assert api.ssa_device_status() == api.SSA_OK
+    for out, _, _ in runs:
+        for k in plain:
+            assert torch.equal(out[k], plain[k]), k
+    assert best[2] <= 1.2 * best[0] and best[1] <= 1.7 * best[0], best
