@@ -56,17 +56,39 @@ ssa_status_t check_paged(const ssa_paged_dims_t* in, PagedDims* out, bool* empty
 }
 
 // A [B, H, N, d] tensor as in the other entry points.  Inputs may broadcast batches and
-// heads (stride 0); rows and an output's slices may not lie over one another.
-ssa_status_t check_tensor(const ssa_tensor_t* t, int dtype, int d, int64_t B, int64_t H, int64_t N, bool output, TensorRef* out) {
+// heads (stride 0), kRows inputs none; an output's rows and slices may not lie over one another.
+enum Use { kInput, kRows, kOutput };
+
+// Whether a tensor's rows are apart: by growing stride, each dimension steps over all that the ones before it span.
+// (Layouts whose slices interleave without nesting are taken for meeting.)
+bool apart(const int64_t (&st)[3], const int64_t (&n)[3], int d) {
+  int by[3] = {0, 1, 2};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (st[by[j]] > st[by[j + 1]]) {
+        const int x = by[j];
+        by[j] = by[j + 1];
+        by[j + 1] = x;
+      }
+  __int128 span = d;  // strides below 2^38, up to 2^31 slices
+  for (int i : by) {
+    if (n[i] <= 1) continue;
+    if (st[i] < span) return false;
+    span += (__int128)st[i] * (n[i] - 1);
+  }
+  return true;
+}
+
+ssa_status_t check_tensor(const ssa_tensor_t* t, int dtype, int d, int64_t B, int64_t H, int64_t N, Use use, TensorRef* out) {
   if (t == nullptr || !aligned(t->ptr, 16)) return SSA_ERR_INVALID_ARG;
   const int64_t es = dtype == SSA_BF16 ? 2 : 4;
   const int64_t st[3] = {t->stride_b, t->stride_h, t->stride_n}, n[3] = {B, H, N};
   for (int i = 0; i < 3; ++i) {
     if (st[i] < 0 || st[i] >= (1LL << 38) || (st[i] * es) % 16) return SSA_ERR_INVALID_ARG;
-    if (output && n[i] > 1 && st[i] < d) return SSA_ERR_INVALID_ARG;
     // rows that overlap in part describe no tensor; slices laid over one another (stride 0) are a broadcast
-    if (!output && n[i] > 1 && st[i] < d && (i == 2 || st[i] != 0)) return SSA_ERR_INVALID_ARG;
+    if (n[i] > 1 && st[i] < d && (use != kInput || i == 2 || st[i] != 0)) return SSA_ERR_INVALID_ARG;
   }
+  if (use == kOutput && !apart(st, n, d)) return SSA_ERR_INVALID_ARG;
   *out = TensorRef{t->ptr, t->stride_b, t->stride_h, t->stride_n};
   return SSA_OK;
 }
@@ -103,10 +125,10 @@ ssa_status_t ssa_fwd_window(const ssa_window_dims_t* dims, const ssa_tensor_t* Q
   if (s != SSA_OK) return s;
   if (empty) return SSA_OK;
   WinFwdArgs a{};
-  if ((s = check_tensor(Q, D.dtype, D.d, D.B, D.Hq, D.N, false, &a.q)) != SSA_OK) return s;
-  if ((s = check_tensor(K, D.dtype, D.d, D.B, D.Hkv, D.N, false, &a.k)) != SSA_OK) return s;
-  if ((s = check_tensor(V, D.dtype, D.d, D.B, D.Hkv, D.N, false, &a.v)) != SSA_OK) return s;
-  if ((s = check_tensor(h, D.dtype, D.d, D.B, D.Hq, D.N, true, &a.h)) != SSA_OK) return s;
+  if ((s = check_tensor(Q, D.dtype, D.d, D.B, D.Hq, D.N, kInput, &a.q)) != SSA_OK) return s;
+  if ((s = check_tensor(K, D.dtype, D.d, D.B, D.Hkv, D.N, kInput, &a.k)) != SSA_OK) return s;
+  if ((s = check_tensor(V, D.dtype, D.d, D.B, D.Hkv, D.N, kInput, &a.v)) != SSA_OK) return s;
+  if ((s = check_tensor(h, D.dtype, D.d, D.B, D.Hq, D.N, kOutput, &a.h)) != SSA_OK) return s;
   if (!aligned(lse, 4)) return SSA_ERR_INVALID_ARG;
   if ((s = require_sm100()) != SSA_OK) return s;
   a.lse = lse;
@@ -128,14 +150,14 @@ ssa_status_t ssa_bwd_window(const ssa_window_dims_t* dims, const ssa_tensor_t* Q
   if (s != SSA_OK) return s;
   if (empty) return SSA_OK;
   WinBwdArgs a{};
-  if ((s = check_tensor(Q, D.dtype, D.d, D.B, D.Hq, D.N, false, &a.q)) != SSA_OK) return s;
-  if ((s = check_tensor(K, D.dtype, D.d, D.B, D.Hkv, D.N, false, &a.k)) != SSA_OK) return s;
-  if ((s = check_tensor(V, D.dtype, D.d, D.B, D.Hkv, D.N, false, &a.v)) != SSA_OK) return s;
-  if ((s = check_tensor(h, D.dtype, D.d, D.B, D.Hq, D.N, false, &a.h)) != SSA_OK) return s;
-  if ((s = check_tensor(g, D.dtype, D.d, D.B, D.Hq, D.N, false, &a.g)) != SSA_OK) return s;
-  if ((s = check_tensor(dQ, D.dtype, D.d, D.B, D.Hq, D.N, true, &a.dq)) != SSA_OK) return s;
-  if ((s = check_tensor(dK, D.dtype, D.d, D.B, D.Hkv, D.N, true, &a.dk)) != SSA_OK) return s;
-  if ((s = check_tensor(dV, D.dtype, D.d, D.B, D.Hkv, D.N, true, &a.dv)) != SSA_OK) return s;
+  if ((s = check_tensor(Q, D.dtype, D.d, D.B, D.Hq, D.N, kInput, &a.q)) != SSA_OK) return s;
+  if ((s = check_tensor(K, D.dtype, D.d, D.B, D.Hkv, D.N, kInput, &a.k)) != SSA_OK) return s;
+  if ((s = check_tensor(V, D.dtype, D.d, D.B, D.Hkv, D.N, kInput, &a.v)) != SSA_OK) return s;
+  if ((s = check_tensor(h, D.dtype, D.d, D.B, D.Hq, D.N, kInput, &a.h)) != SSA_OK) return s;
+  if ((s = check_tensor(g, D.dtype, D.d, D.B, D.Hq, D.N, kInput, &a.g)) != SSA_OK) return s;
+  if ((s = check_tensor(dQ, D.dtype, D.d, D.B, D.Hq, D.N, kOutput, &a.dq)) != SSA_OK) return s;
+  if ((s = check_tensor(dK, D.dtype, D.d, D.B, D.Hkv, D.N, kOutput, &a.dk)) != SSA_OK) return s;
+  if ((s = check_tensor(dV, D.dtype, D.d, D.B, D.Hkv, D.N, kOutput, &a.dv)) != SSA_OK) return s;
   if (!aligned(lse, 4)) return SSA_ERR_INVALID_ARG;
   if ((s = check_ws(ws, ws_bytes, win_bwd_layout(D).bytes)) != SSA_OK) return s;
   if ((s = require_sm100()) != SSA_OK) return s;
@@ -165,10 +187,10 @@ ssa_status_t ssa_paged_append(const ssa_paged_dims_t* dims, const ssa_tensor_t* 
   if (s != SSA_OK) return s;
   if (empty) return SSA_OK;
   PagedArgs a{};
-  if ((s = check_tensor(k, D.dtype, D.d, 1, D.Hkv, D.T, false, &a.nk)) != SSA_OK) return s;
-  if ((s = check_tensor(v, D.dtype, D.d, 1, D.Hkv, D.T, false, &a.nv)) != SSA_OK) return s;
-  if ((s = check_tensor(K, D.dtype, D.d, D.num_pages, D.Hkv, D.page, true, &a.k)) != SSA_OK) return s;
-  if ((s = check_tensor(V, D.dtype, D.d, D.num_pages, D.Hkv, D.page, true, &a.v)) != SSA_OK) return s;
+  if ((s = check_tensor(k, D.dtype, D.d, 1, D.Hkv, D.T, kInput, &a.nk)) != SSA_OK) return s;
+  if ((s = check_tensor(v, D.dtype, D.d, 1, D.Hkv, D.T, kInput, &a.nv)) != SSA_OK) return s;
+  if ((s = check_tensor(K, D.dtype, D.d, D.num_pages, D.Hkv, D.page, kOutput, &a.k)) != SSA_OK) return s;
+  if ((s = check_tensor(V, D.dtype, D.d, D.num_pages, D.Hkv, D.page, kOutput, &a.v)) != SSA_OK) return s;
   if (!aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(page_table, 4)) return SSA_ERR_INVALID_ARG;
   if ((s = require_sm100()) != SSA_OK) return s;
   a.q_start = q_start;
@@ -189,10 +211,10 @@ ssa_status_t ssa_paged_attention(const ssa_paged_dims_t* dims, const ssa_tensor_
   if (empty) return SSA_OK;
   PagedArgs a{};
   // a slot's heads come in one TMA box: no broadcast of them
-  if ((s = check_tensor(q, D.dtype, D.d, 1, D.Hq, D.T, true, &a.q)) != SSA_OK) return s;
-  if ((s = check_tensor(K, D.dtype, D.d, D.num_pages, D.Hkv, D.page, false, &a.k)) != SSA_OK) return s;
-  if ((s = check_tensor(V, D.dtype, D.d, D.num_pages, D.Hkv, D.page, false, &a.v)) != SSA_OK) return s;
-  if ((s = check_tensor(h, D.dtype, D.d, 1, D.Hq, D.T, true, &a.h)) != SSA_OK) return s;
+  if ((s = check_tensor(q, D.dtype, D.d, 1, D.Hq, D.T, kRows, &a.q)) != SSA_OK) return s;
+  if ((s = check_tensor(K, D.dtype, D.d, D.num_pages, D.Hkv, D.page, kInput, &a.k)) != SSA_OK) return s;
+  if ((s = check_tensor(V, D.dtype, D.d, D.num_pages, D.Hkv, D.page, kInput, &a.v)) != SSA_OK) return s;
+  if ((s = check_tensor(h, D.dtype, D.d, 1, D.Hq, D.T, kOutput, &a.h)) != SSA_OK) return s;
   if (!aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(page_table, 4) || !aligned(lse, 4))
     return SSA_ERR_INVALID_ARG;
   if ((s = check_ws(ws, ws_bytes, paged_bytes(D))) != SSA_OK) return s;

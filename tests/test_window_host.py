@@ -215,3 +215,44 @@ def test_binding_refuses_wrong_tensors():
         api.ssa_paged_append(p, torch.zeros(3, 2, 64), torch.zeros(3, 2, 64), torch.zeros(2, dtype=torch.int32),
                              torch.zeros(1, dtype=torch.int32), torch.zeros(1, 2, dtype=torch.int32),
                              torch.zeros(5, 16, 2, 64), torch.zeros(5, 16, 2, 64))
+
+
+def _bwd_dq(lib, dq, B=2, Hq=4, N=100):
+    """The answer to a workspace that is too small, once the tensors are taken: nothing is enqueued."""
+    w, t, good = api.make_window_dims(B, Hq, Hq, N, 64, 10), _tensor(), _tensor(16, 1 << 30, 1 << 25, 64)
+    return lib.ssa_bwd_window(ctypes.byref(w), t, t, t, t, _p(), t, dq, good, good, _p(), 0, None)
+
+
+# [B, H, N, 64] with B = 2, H = 4, N = 100: strides whose slices meet
+MEETING = {
+    "heads_and_rows": (4 * 6400, 64, 64), "half_a_head": (4 * 6400, 128, 64), "batches_and_heads": (6400, 6400, 64),
+    "last_row": (4 * 6400, 6400 - 64, 64), "batch_in_the_last_head": (4 * 6400 - 8, 6400, 64), "rows_over_heads": (25600, 64, 192),
+    "rows_over_batches": (256, 64, 256), "far_rows": (64, 1 << 26, 1 << 20),
+}
+APART = {
+    "heads_first": (4 * 6400, 6400, 64), "rows_first": (4 * 6400, 64, 256), "padded": (32000, 7400, 72), "batches_inside": (64, 128, 512),
+    "other_rows": (128, 25600, 256), "far": (1 << 37, 1 << 35, 1 << 28),
+}
+
+
+def test_outputs_that_lie_over_themselves(lib):
+    for name, s in MEETING.items():
+        bad = _tensor(16, *s)
+        w, t, good = api.make_window_dims(2, 4, 4, 100, 64, 10), _tensor(), _tensor(16, 25600, 6400, 64)
+        assert lib.ssa_fwd_window(ctypes.byref(w), t, t, t, bad, _p(), None) == api.SSA_ERR_INVALID_ARG, name
+        assert _bwd_dq(lib, bad) == api.SSA_ERR_INVALID_ARG, name
+        for i in range(3):
+            grads = [good] * 3
+            grads[i] = bad
+            assert lib.ssa_bwd_window(ctypes.byref(w), t, t, t, t, _p(), t, *grads, _p(), 1 << 50, None) == api.SSA_ERR_INVALID_ARG
+        p = api.make_paged_dims(1, 100, 4, 4, 64, 128, 2, 4)
+        for cache in ((bad, good), (good, bad)):  # a page has 128 rows
+            assert lib.ssa_paged_append(ctypes.byref(p), t, t, _p(), _p(), _p(), *cache, None) == api.SSA_ERR_INVALID_ARG
+        if name not in ("batches_and_heads", "batch_in_the_last_head", "rows_over_batches"):  # no batches there
+            assert lib.ssa_paged_attention(ctypes.byref(p), t, t, t, _p(), _p(), _p(), bad, _p(), _p(), 1 << 50,
+                                           None) == api.SSA_ERR_INVALID_ARG, name
+    for name, s in APART.items():
+        assert _bwd_dq(lib, _tensor(16, *s)) == api.SSA_ERR_WORKSPACE, name
+    # a dimension of length one has no slices to meet
+    assert _bwd_dq(lib, _tensor(16, 64, 64, 64), B=1, Hq=2, N=1) == api.SSA_ERR_WORKSPACE
+    assert _bwd_dq(lib, _tensor(16, 64, 64, 64), B=1, Hq=1) == api.SSA_ERR_WORKSPACE
