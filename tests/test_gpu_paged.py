@@ -412,3 +412,31 @@ def test_idle_sequences_are_passed_over(dtype):
         for k in plain:
             assert torch.equal(out[k], plain[k]), k
     assert best[2] <= 1.2 * best[0] and best[1] <= 1.7 * best[0], best
+
+
+# new tokens, tokens in all, Hq, Hkv, d, page: chunks of two slots, few rows, one token cut among many CTAs
+LARGE = {
+    "chunks": ([300, 140], [700, 140], 8, 2, 128, 64),
+    "tokens": ([1, 5, 2], [600, 900, 77], 8, 2, 64, 16),
+    "one_token": ([1], [9000], 8, 2, 128, 64),
+    "one_long_chunk": ([70], [5000], 4, 1, 64, 32),
+}
+
+
+@pytest.mark.parametrize("wave", ["rising", "falling", "both"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", list(LARGE))
+def test_large_logits(name, dtype, wave):
+    """Logits of some hundreds whose maxima move along the keys: the running maximum is raised in most tiles, and the
+    partials of one item differ by hundreds."""
+    b = Batch(*LARGE[name], dtype)
+    b.q = b.q.abs()
+    for s, n in enumerate(b.total):
+        u = torch.arange(n, dtype=torch.float32)
+        ramp = {"rising": 0.1 + 8.0 * u / n, "falling": 8.1 - 8.0 * u / n, "both": 5.0 + 4.0 * torch.sin(u / 40.0)}[wave]
+        for i in range(-(-n // b.page)):
+            part = ramp[i * b.page:(i + 1) * b.page]
+            rows = b.caches[0][b.table[s, i], :len(part)]
+            rows.copy_((rows.float().abs() * part[:, None, None]).to(TYPES[dtype]))
+    for window, sinks in ((None, 0), (400, 20)):
+        b.check(b.attend(window, sinks), window, sinks)

@@ -284,3 +284,55 @@ def test_long_rows_against_a_sample():
         for name, want in (("dK", dk), ("dV", dv)):
             got = out[name][0, k, keys].double()
             assert float(((got - want).norm(dim=1) / want.norm(dim=1)).max()) < 1e-2, name
+
+
+# Logits of some hundreds whose maxima rise and fall along the keys (every raise is far above the 2^8 that the forward
+# allows without one), values far from zero, and their gradients: rows alone and two 128-row tiles at a time.
+LARGE = {
+    "rows_alone": (1, 2, 1, 400, 64, 300, 3),
+    "rows_alone_d128": (1, 2, 2, 390, 128, api.EVERYTHING, 0),
+    "two_tiles": (1, 80, 8, 400, 64, 300, 3),
+    "two_tiles_d128": (1, 75, 15, 385, 128, 200, 70),
+}
+
+
+@pytest.mark.parametrize("wave", ["rising", "rising_and_falling"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", list(LARGE))
+def test_large_logits_and_their_gradients(name, dtype, wave):
+    B, Hq, Hkv, N, d, window, sinks = LARGE[name]
+    host = _inputs(B, Hq, Hkv, N, d, dtype, 31)
+    u = torch.arange(N)[None, None, :, None]
+    ramp = 0.1 + 12.0 * u / N if wave == "rising" else 6.0 + 6.0 * torch.sin(u / 13.0)
+    host["Q"] = host["Q"].abs()
+    host["K"] = (host["K"].float().abs() * ramp).to(TYPES[dtype])
+    host["V"] = (host["V"].float() + 20.0).to(TYPES[dtype])
+    dims = api.make_window_dims(B, Hq, Hkv, N, d, window, sinks, dtype)
+    out = _run(dims, {k: v.cuda() for k, v in host.items()})
+    x = {k: v.double().numpy() for k, v in host.items()}
+    f = W.forward(x["Q"], x["K"], x["V"], window, sinks, 1 / math.sqrt(d), dtype)
+    within("h", out["h"], f["h"], f["tol_h"])
+    within("lse", out["lse"], f["lse"], f["tol_lse"])
+    r, tol = W.backward(x["Q"], x["K"], x["V"], x["g"], f, window, sinks, 1 / math.sqrt(d), dtype)
+    for k in r:
+        within(k, out[k], r[k], tol[k])
+
+
+@pytest.mark.parametrize("shape", [(1, 8, 8, 1000, 128, 128, 16), (2, 6, 2, 517, 64, 101, 7), (1, 4, 2, 700, 64, EVERYTHING, 0)])
+def test_fp32_to_its_accuracy(shape):
+    """The norms of the fp32 errors.  Unit-normal inputs: logits of about 1, lse of 5 to 7.  Roundings of an exponent,
+    uniform, of half a step of a value up to 8 (2^-21 / 2): rms 2^-21 / sqrt(12) = 1.4e-7 each; two of them and the
+    exponential (2 ulp at most: rms below 1.4e-7) give a weight 2.4e-7.  dP and D, each a sum of d terms in chunks of
+    16, add two errors of d / 16 additions (rms 2^-24 / sqrt(3) sqrt(d / 16), 1e-7 at d = 128).  A gradient's sum over
+    hundreds of terms adds the same once more, its terms' errors being independent: 2.4e-7, 1.4e-7 and 1e-7 in squares
+    are 3e-7, and twice that is left for the correlated part (lse is one value for a row, D too).  Sums that ran in
+    the tensor core, which cuts off, were 2e-6 off."""
+    B, Hq, Hkv, N, d, window, sinks = shape
+    host = _inputs(B, Hq, Hkv, N, d, "f32", 13)
+    dims = api.make_window_dims(B, Hq, Hkv, N, d, window, sinks, "f32")
+    out = _run(dims, {k: v.cuda() for k, v in host.items()})
+    x = {k: v.double().numpy() for k, v in host.items()}
+    f = W.forward(x["Q"], x["K"], x["V"], window, sinks, 1 / math.sqrt(d), "f32")
+    r, _ = W.backward(x["Q"], x["K"], x["V"], x["g"], f, window, sinks, 1 / math.sqrt(d), "f32")
+    for k, want in (("h", f["h"]), *r.items()):
+        assert rel_l2(f64(out[k]), want) < 9e-7, (k, rel_l2(f64(out[k]), want))
