@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const Chunk ch = find_chunk<TILE>((int)blockIdx.x / p.Hkv, p.cut, p.L, p.g, p.N, p.window, p.sinks);
   const int u0 = ch.kt * TILE, nq = query_tiles_of<TILE>(ch.kt, p.N, p.window, p.sinks);
   const int first = ch.idx * p.L, T = 2 * min(p.L, nq * p.g - first);  // units: step (head, query tile), half
-  bool again = false;  // the lane's row is not finite
+  bool again = false;  // the thread's row is not finite
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -381,23 +381,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
   }
   tc_fence_before();
-  __syncthreads();
+  const bool spoilt = __syncthreads_or(again) && !M.abort;
   if (M.abort && threadIdx.x == 0) atomicCAS(p.status, 0, (int)SSA_ERR_TIMEOUT);
   if (warp == WARP_MMA) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  // A warp's rows that are not finite once more (win_rows.cuh).
-  for (unsigned rest = __ballot_sync(0xffffffffu, again); rest; rest &= rest - 1) {
-    constexpr int W = HD / 4;
-    const int r = (warp & 3) * 32 + __ffs(rest) - 1, u = u0 + r, c0 = W * (warp >> 2);
-    const QueryView view{p.q, p.up, p.lse2, p.dsum, b, p.Hq, kvh * p.g, ch.kt, nq, first, first + T / 2, p.N, p.Npad, p.window, p.sinks};
-    float* part = p.part + ((size_t)plane * p.partials + ch.slot + ch.idx) * (2 * TILE * HD) + r * HD + c0;
-    Columns<bf16, W> dk, dv;
-    dk.look(row_ptr_w<bf16>(p.dk, b, kvh, u) + c0, ch.n == 1 ? nullptr : part);
-    dv.look(row_ptr_w<bf16>(p.dv, b, kvh, u) + c0, ch.n == 1 ? nullptr : part + TILE * HD);
-    mend_dkv_row<bf16, HD, W, TILE>(view, u, row_ptr<bf16>(p.k, b, kvh, u), row_ptr<bf16>(p.v, b, kvh, u), dk, dv, c0, p.c, p.scale);
+  // rows that are not finite once more (win_rows.cuh)
+  if (!spoilt) return;
+  const QueryView view{p.q, p.up, p.lse2, p.dsum, b, p.Hq, kvh * p.g, ch.kt, nq, first, first + T / 2, p.N, p.Npad, p.window, p.sinks};
+  for (int r = warp; r < TILE && u0 + r < p.N; r += NTHREADS / 32) {
+    const int u = u0 + r;
+    float* part = ch.n == 1 ? nullptr : p.part + ((size_t)plane * p.partials + ch.slot + ch.idx) * (2 * TILE * HD) + r * HD;
+    mend_dkv_row<bf16, HD, TILE>(view, u, row_ptr<bf16>(p.k, b, kvh, u), row_ptr<bf16>(p.v, b, kvh, u), row_ptr_w<bf16>(p.dk, b, kvh, u),
+                                 row_ptr_w<bf16>(p.dv, b, kvh, u), part, part == nullptr ? nullptr : part + TILE * HD, p.c, p.scale);
   }
 }
 
@@ -468,7 +466,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint8_t* sK = smem + C::OFF_K;
   uint8_t* sV = smem + C::OFF_V;
 
-  bool again = false;  // the warp stored rows that are not finite
+  bool again = false;  // the thread stored rows that are not finite
   const int planes = p.B * p.Hq, items = planes * p.NT;
   // The longest rows first; the heads of a group side by side, so that they share K and V in L2.
   auto item = [&](int i) {
@@ -658,27 +656,25 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (lane == 0) mbar_arrive(&M.dq_free);
       I = J;
     }
-    again = __any_sync(0xffffffffu, z.x + z.y != 0.f) && ok;
+    again = z.x + z.y != 0.f;
   }
   tc_fence_before();
-  __syncthreads();
+  const bool spoilt = __syncthreads_or(again) && !M.abort;
   if (M.abort && threadIdx.x == 0) atomicCAS(p.status, 0, (int)SSA_ERR_TIMEOUT);
   if (warp == WARP_MMA) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  // They are formed once more (win_rows.cuh).
-  for (int i = blockIdx.x; again && i < items; i += gridDim.x) {
-    constexpr int W = HD / 4;
+  // they are formed once more (win_rows.cuh)
+  for (int i = blockIdx.x; spoilt && i < items; i += gridDim.x) {
     const DqItem I = item(i);
     const KeyRows<bf16> keys{p.k, p.v, I.b, I.kvh, nullptr, 0, 0, 0};
-    const int ta = I.t0 + (warp & 3) * 32, c0 = W * (warp >> 2);
-    for (int t = ta; t < min(ta + 32, p.N); ++t) {
+    for (int t = I.t0 + warp; t < min(I.t0 + TILE, p.N); t += NTHREADS / 32) {
       const int64_t o = ((int64_t)I.b * p.Hq + I.h) * p.Npad + t;
       const RowView view{I.kt, t, 0, I.kt.count, p.window, p.sinks, p.N};
-      mend_dq_row<bf16, HD, W, TILE>(keys, view, row_ptr<bf16>(p.q, I.b, I.h, t), row_ptr<bf16>(p.up, I.b, I.h, t),
-                                     row_ptr_w<bf16>(p.dq, I.b, I.h, t) + c0, c0, p.c, p.lse2[o], p.dsum[o], p.scale);
+      mend_dq_row<bf16, HD, TILE>(keys, view, row_ptr<bf16>(p.q, I.b, I.h, t), row_ptr<bf16>(p.up, I.b, I.h, t),
+                                  row_ptr_w<bf16>(p.dq, I.b, I.h, t), p.c, p.lse2[o], p.dsum[o], p.scale);
     }
   }
 }

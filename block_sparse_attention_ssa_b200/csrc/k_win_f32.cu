@@ -274,7 +274,7 @@ __device__ __forceinline__ void form_again(const F32Params& p, Place at, int lef
         o.out = row_ptr_w<float>(p.h, PAGED ? 0 : I.b, head, row);
         o.lse = p.lse + (PAGED ? (int64_t)head * p.T + row : ((int64_t)I.b * p.Hq + I.head0) * p.N + row);
       }
-      mend_row<float, HD, HD, BT>(keys, view, row_ptr<float>(p.q, PAGED ? 0 : I.b, head, row), o, 0, p.c);
+      mend_row<float, HD, BT>(keys, view, row_ptr<float>(p.q, PAGED ? 0 : I.b, head, row), o, p.c);
     }
     if (!PAGED || !next_item(p, at, left, I.take)) return;
   }
@@ -675,8 +675,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dq_f32_kernel(F32Bwd p
     const int q = q0 + r;
     const int64_t o = ((int64_t)b * p.Hq + h) * p.Npad + q;
     const RowView view{kt, q, 0, kt.count, p.window, p.sinks, p.N};
-    mend_dq_row<float, HD, HD, BT>(keys, view, row_ptr<float>(p.q, b, h, q), row_ptr<float>(p.g, b, h, q),
-                                   row_ptr_w<float>(p.dq, b, h, q), 0, p.c, p.lse2[o], p.dsum[o], p.scale);
+    mend_dq_row<float, HD, BT>(keys, view, row_ptr<float>(p.q, b, h, q), row_ptr<float>(p.g, b, h, q),
+                               row_ptr_w<float>(p.dq, b, h, q), p.c, p.lse2[o], p.dsum[o], p.scale);
   }
 }
 
@@ -771,11 +771,9 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) win_bwd_dkv_f32_kernel(F32Bwd 
   const QueryView view{p.q, p.g, p.lse2, p.dsum, b, p.Hq, kvh * p.grp, ch.kt, nq, first, last, p.N, p.Npad, p.window, p.sinks};
   for (int r = threadIdx.x >> 5; r < BT && u0 + r < p.N; r += BWD_THREADS / 32) {
     const int u = u0 + r;
-    Columns<float, HD> ck, cv;
-    const bool fk = ck.look(row_ptr_w<float>(p.dk, b, kvh, u), ch.n == 1 ? nullptr : partial(r));
-    const bool fv = cv.look(row_ptr_w<float>(p.dv, b, kvh, u), ch.n == 1 ? nullptr : partial(r) + BT * HD);
-    if (!__all_sync(0xffffffffu, fk && fv))
-      mend_dkv_row<float, HD, HD, BT>(view, u, row_ptr<float>(p.k, b, kvh, u), row_ptr<float>(p.v, b, kvh, u), ck, cv, 0, p.c, p.scale);
+    float* part = ch.n == 1 ? nullptr : partial(r);
+    mend_dkv_row<float, HD, BT>(view, u, row_ptr<float>(p.k, b, kvh, u), row_ptr<float>(p.v, b, kvh, u), row_ptr_w<float>(p.dk, b, kvh, u),
+                                row_ptr_w<float>(p.dv, b, kvh, u), part, part == nullptr ? nullptr : part + BT * HD, p.c, p.scale);
   }
 }
 

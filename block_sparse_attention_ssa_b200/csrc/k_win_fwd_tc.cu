@@ -83,7 +83,7 @@ struct Misc {
   int abort;
   int turn;  // 1 while an issuer feeds the tensor core
   int left;
-  int again[16];  // a softmax warp stored rows that are not finite
+  int again;  // rows that are not finite were stored
   Place at;
   uint32_t bad[8];  // pages missing from a key tile, a bit per 16 keys (ring of 2 NSK tiles)
   float mref[2][TILE];  // running maximum of each row
@@ -218,35 +218,30 @@ struct Walk {
   }
 };
 
-// A softmax warp's rows once more (win_rows.cuh): those whose sum is finite and whose columns are not.  Behind the loop over
-// the items, so that nothing of it is held in registers there (within it, 270 to 530 bytes were spilled), and inline: a
-// function called there took 2 us of every launch (8192 tokens, window 256: 79.6 us, inline 77.5, without any of it 77.8).
+// The CTA's rows that are not finite once more (win_rows.cuh), a warp a row.  Behind the loop over the items, so that nothing
+// of it is held in registers there (within it, 270 to 530 bytes were spilled), and inline: a function called there
+// took 2 us of every launch (8192 tokens, window 256: 79.6 us, inline 77.5, without any of it 77.8).
 template <int HD, bool PAGED>
-__device__ __forceinline__ void form_again(const TcParams& p, const Misc& M, int warp) {
-  constexpr int W = HD / 2;
-  const int s = warp >> 3, half = (warp >> 2) & 1, r0 = (warp & 3) * 32;
-  Walk<PAGED> walk(p, M, s);
+__device__ __forceinline__ void form_again(const TcParams& p, const Misc& M) {
+  Walk<PAGED> walk(p, M, 0);
   Item I;
   while (walk.next(I)) {
-    if (I.T == 0 || (s && !I.two)) continue;
-    const int shift = s ? I.toks0 : 0, nrows = (s ? I.toks - I.toks0 : I.toks0) * I.g;
+    if (I.T == 0) continue;
     const KeyRows<bf16> keys{p.k, p.v, I.b, I.kvh, PAGED ? p.table : nullptr, p.page, p.num_pages, p.max_pages};
-    for (int r = r0; r < min(r0 + 32, nrows); ++r) {
-      const int tok = I.row0 + shift + r / I.g, head = I.head0 + r % I.g;
-      const RowView view{I.kt, I.p0 + shift + r / I.g, I.off, I.off + I.T, p.window, p.sinks, p.N};
-      const bf16* q = row_ptr<bf16>(p.q, PAGED ? 0 : I.b, head, tok);
+    for (int r = threadIdx.x >> 5; r < I.toks * I.g; r += NTHREADS / 32) {
+      const int i = PAGED ? r / I.g : r, tok = I.row0 + i, head = I.head0 + (PAGED ? r % I.g : 0);
+      const RowView view{I.kt, I.p0 + i, I.off, I.off + I.T, p.window, p.sinks, p.N};
       RowOut<bf16> o{};
       if (PAGED && I.cut) {
         float* pb = p.part + (size_t)(2 * blockIdx.x + (I.seg ? 1 : 0)) * partial_floats(2 * TILE, HD);
-        const int pr = shift * I.g + r;
-        o.part = pb + (size_t)pr * HD + W * half;
-        o.m = pb + 2 * TILE * HD + pr;
+        o.part = pb + (size_t)r * HD;
+        o.m = pb + 2 * TILE * HD + r;
         o.l = o.m + 2 * TILE;
       } else {
-        o.out = row_ptr_w<bf16>(p.h, PAGED ? 0 : I.b, head, tok) + W * half;
+        o.out = row_ptr_w<bf16>(p.h, PAGED ? 0 : I.b, head, tok);
         o.lse = p.lse + (PAGED ? (int64_t)head * p.batch.T + tok : ((int64_t)I.b * p.Hq + head) * p.N + tok);
       }
-      mend_row<bf16, HD, W, TILE>(keys, view, q, o, W * half, p.c);
+      mend_row<bf16, HD, TILE>(keys, view, row_ptr<bf16>(p.q, PAGED ? 0 : I.b, head, tok), o, p.c);
     }
   }
 }
@@ -296,7 +291,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     mbar_init(&M.join_done, 8);
     M.abort = 0;
     M.turn = 0;
-    for (int w = 0; w < 16; ++w) M.again[w] = 0;
+    M.again = 0;
     fence_mbar_init();
   }
   if (warp == WARP_MMA) {
@@ -774,7 +769,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               store_32b(ho + c0, h8, p.wide);
             }
           }
-          if (z.x + z.y != 0.f && (po != nullptr || ho != nullptr)) M.again[warp] = 1;
+          if (z.x + z.y != 0.f && (po != nullptr || ho != nullptr)) M.again = 1;
         }
         if (join) {
           tc_fence_before();
@@ -802,7 +797,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tmem_dealloc(tmem, 512);
   }
   // every warp's rows and statistics are stored
-  if (warp < WARP_TMA && M.again[warp] && !M.abort) form_again<HD, PAGED>(p, M, warp);
+  if (M.again && !M.abort) form_again<HD, PAGED>(p, M);
 }
 
 template <int HD, bool PAGED>

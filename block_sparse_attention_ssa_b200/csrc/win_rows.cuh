@@ -3,9 +3,13 @@
 // A tile's product multiplies hidden pairs too, with a weight of zero, and zero times a NaN or an infinity is
 // NaN: one such value would spoil every row that shares a tile with a row that sees it.  An fp32 operand as a pair of TF32
 // values turns an infinity into a NaN besides.  So the kernels look at the rows that they store (one multiply-add a
-// value), and where some are not finite, the warps that stored them form them once more, here, from their visible
-// pairs alone, in fp32 multiply-adds.  Rows that see no NaN or infinity come out finite; the others are what the
-// formula says.  A pass over finite values calls nothing of this.
+// value), and where some are not finite, the CTA forms them once more, here, from their visible pairs alone, in fp32
+// multiply-adds.  Rows that see no NaN or infinity come out finite; the others are what the formula says.  A pass over
+// finite values calls nothing of this.
+//
+// A warp takes a row.  A group of HD / (16 bytes) lanes forms a dot product, so that a load covers whole rows (a lane
+// a row took eight times the passes of each load), and 32 weights at a time go to sums of which a lane
+// holds HD / 32 columns.
 #pragma once
 
 #include "win_common.cuh"
@@ -18,34 +22,143 @@ __device__ __forceinline__ bool is_finite(float x) { return fabsf(x) < __builtin
 
 __device__ __forceinline__ bool sees(int t, int u, int window, int sinks) { return u <= t && (t - u < window || u < sinks); }
 
+// A lane's 16 bytes of a row that other rows are multiplied with.
 template <typename T, int HD>
-__device__ __forceinline__ float dot_row(const T* a, const T* b) {
-  constexpr int V = Vec16<T>::kN;
-  float s = 0.f;
-#pragma unroll 2
-  for (int c = 0; c < HD; c += V) {
-    float x[V], y[V];
-    Vec16<T>::load(a + c, x);
-    Vec16<T>::load(b + c, y);
+struct RowPart {
+  static constexpr int V = Vec16<T>::kN, LPR = HD / V, RPW = 32 / LPR;  // values of a lane, lanes of a row, rows of a load
+  float x[V];
+  __device__ __forceinline__ explicit RowPart(const T* row) { Vec16<T>::load(row + (threadIdx.x & 31) % LPR * V, x); }
+  // Lane i: the dot product with row(i), zero where that is null.  Warp-wide.
+  template <typename F>
+  __device__ __forceinline__ float dots(F row) const {
+    const int lane = threadIdx.x & 31;
+    float mine = 0.f;
+#pragma unroll 4
+    for (int j = 0; j < LPR; ++j) {
+      const T* r = row(j * RPW + lane / LPR);
+      float y[V], s = 0.f;
+      if (r != nullptr) {
+        Vec16<T>::load(r + lane % LPR * V, y);
 #pragma unroll
-    for (int i = 0; i < V; ++i) s = fmaf(x[i], y[i], s);
+        for (int i = 0; i < V; ++i) s = fmaf(x[i], y[i], s);
+      }
+#pragma unroll
+      for (int o = LPR / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      s = __shfl_sync(0xffffffffu, s, lane % RPW * LPR);
+      if (lane / RPW == j) mine = s;
+    }
+    return mine;
   }
-  return s;
-}
+};
 
-// Whether a NaN or an infinity is among W values.
-template <typename T, int W>
-__device__ __forceinline__ bool spoiled(const T* a) {
-  constexpr int V = Vec16<T>::kN;
-  float z = 0.f;
-#pragma unroll 2
-  for (int c = 0; c < W; c += V) {
-    float x[V];
-    Vec16<T>::load(a + c, x);
+// A row's columns, HD / 32 to a lane: which of them are not finite, and their sums over the visible pairs.
+template <typename T, int HD>
+struct Columns {
+  static constexpr int NC = HD / 32;
+  float acc[NC];
+  bool write[NC], done[NC];  // done: needs nothing, or NaN from a visible pair
+  T* out;
+  float* part;  // fp32 partials; one of the two is null
+  __device__ __forceinline__ static int col() { return (threadIdx.x & 31) * NC; }
+  __device__ __forceinline__ static void load(const float* p, float (&x)[NC]) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) z = fmaf(x[i], 0.f, z);
+    for (int n = 0; n < NC; n += 2) {
+      const float2 y = *reinterpret_cast<const float2*>(p + n);
+      x[n] = y.x;
+      x[n + 1] = y.y;
+    }
   }
-  return z != 0.f;  // a NaN differs from everything
+  __device__ __forceinline__ static void load(const __nv_bfloat16* p, float (&x)[NC]) {
+#pragma unroll
+    for (int n = 0; n < NC; n += 2) {
+      const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p + n));
+      x[n] = y.x;
+      x[n + 1] = y.y;
+    }
+  }
+  // Both begin at the row.  Returns whether the lane's columns are finite.
+  __device__ __forceinline__ bool look(T* out_, float* part_) {
+    out = out_;
+    part = part_;
+    float x[NC];
+    if (part != nullptr) load(part + col(), x);
+    else load(out + col(), x);
+    bool fine = true;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      acc[n] = 0.f;
+      done[n] = is_finite(x[n]);
+      write[n] = !done[n];
+      fine &= done[n];
+    }
+    return fine;
+  }
+  // Whether the lane's open columns are NaN in a row that all of them see.
+  __device__ __forceinline__ bool spoiled_by(const T* row) const {
+    if (row == nullptr) return false;
+    float x[NC];
+    load(row + col(), x);
+    bool all = true;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) all &= done[n] || x[n] != x[n];
+    return all;
+  }
+  // Settles the open columns that are NaN in a row that all of them see (null: all of them).
+  __device__ __forceinline__ void meet(const T* row) {
+    float x[NC];
+    if (row != nullptr) load(row + col(), x);
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+      if (!done[n] && (row == nullptr || x[n] != x[n])) {
+        acc[n] = __int_as_float(0x7fffffff);
+        done[n] = true;
+      }
+  }
+  // acc += w_i row(i) for the set bits i; w: lane i's weight.  Returns whether nothing is left to add in any lane.
+  template <typename F>
+  __device__ __forceinline__ void add(unsigned bits, float w, F row) {
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      if (!(bits >> i & 1u)) continue;
+      float x[NC];
+      load(row(i) + col(), x);
+#pragma unroll
+      for (int n = 0; n < NC; ++n) acc[n] = fmaf(wi, x[n], acc[n]);
+    }
+  }
+  __device__ __forceinline__ bool settled() {
+    bool all = true;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) all &= (done[n] |= acc[n] != acc[n]);
+    return all;
+  }
+  __device__ __forceinline__ void store(float mul) const {
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+      if (write[n]) {
+        if (part != nullptr) part[col() + n] = acc[n];
+        else out[col() + n] = from_f32<T>(acc[n] * mul);
+      }
+  }
+};
+
+// Whether a NaN or an infinity is among the values of row(0) .. row(31) (null: none).  Warp-wide.
+template <typename T, int HD, typename F>
+__device__ __forceinline__ bool spoiled(F row) {
+  using P = RowPart<T, HD>;
+  const int lane = threadIdx.x & 31;
+  float z = 0.f;
+#pragma unroll 4
+  for (int j = 0; j < P::LPR; ++j) {
+    const T* r = row(j * P::RPW + lane / P::LPR);
+    if (r == nullptr) continue;
+    float x[P::V];
+    Vec16<T>::load(r + lane % P::LPR * P::V, x);
+#pragma unroll
+    for (int i = 0; i < P::V; ++i) z = fmaf(x[i], 0.f, z);
+  }
+  return __any_sync(0xffffffffu, z != 0.f);  // a NaN differs from everything
 }
 
 // Where the keys of an item lie: K, V of the window form, or the pages of sequence b.
@@ -68,82 +181,87 @@ struct RowView {
   int t, first, last, window, sinks, N;  // N: keys of the window form
 };
 
-// f(u0, k) for each 32 keys u0 .. u0 + 31 of the view's tiles, the newest first, until it returns false; k: the lane's
-// key row, null where the query does not see it.  Warp-wide.
-template <typename T, int KT, typename F>
-__device__ __forceinline__ void for_keys(const KeyRows<T>& keys, const RowView& r, F f) {
+// f(u0) for each 32 keys u0 .. u0 + 31 of the view's tiles that it sees some of, the newest first, until it returns false.
+template <int KT, typename F>
+__device__ __forceinline__ void for_keys(const RowView& r, F f) {
   for (int j = r.last - 1; j >= r.first; --j)
     for (int i = KT - 32; i >= 0; i -= 32) {
-      const int u0 = r.kt.tile(j) * KT + i, u = u0 + (threadIdx.x & 31);
-      if (!f(u0, sees(r.t, u, r.window, r.sinks) ? keys.at(keys.k, u) : nullptr)) return;
+      const int u0 = r.kt.tile(j) * KT + i;
+      if (u0 > r.t || (u0 + 31 <= r.t - r.window && u0 >= r.sinks)) continue;
+      if (!f(u0)) return;
     }
 }
 
-// W columns of a query's row, from column c0 on, and its statistics where they lie (partials of a cut item: its maximum
-// in base 2, its sum; outputs: lse, its normaliser's natural logarithm).  `out`, `part` (one of them null) begin at c0.
+// Whether a hidden row of `x` that the view's tiles held is not finite: only tiles seen in part hold some.  Window form.
+template <typename T, int HD, int KT>
+__device__ __forceinline__ bool hidden_spoiled(const KeyRows<T>& keys, const TensorRef& x, const RowView& r) {
+  for (int j = r.first; j < r.last; ++j) {
+    const int u0 = r.kt.tile(j) * KT;
+    if (u0 + KT - 1 <= r.t && (r.t - u0 < r.window || u0 + KT <= r.sinks)) continue;
+    for (int u = u0; u < u0 + KT && u < r.N; u += 32)
+      if (spoiled<T, HD>([&](int i) { return u + i < r.N && !sees(r.t, u + i, r.window, r.sinks) ? keys.at(x, u + i) : nullptr; }))
+        return true;
+  }
+  return false;
+}
+
+// A query's row and its statistics where they lie: of a cut item's partial its maximum (base 2) and sum, of an output
+// its lse.
 template <typename T>
 struct RowOut {
   T* out;
-  float* part;
-  float *m, *l;  // of the partial
+  float* part;  // one of the two is null
+  float *m, *l;
   float* lse;
 };
 
-// Forms the row anew where it is not finite.  In bf16 the statistics stand (the tensor cores hold infinities as they are)
-// and only columns that are not finite are written; in fp32 all of them are.  In the bf16 window form, rows that owe their state
-// to a key that they see are left without going through their keys, unless a hidden one of their tiles holds such
-// values too: only tiles that the row sees in part are looked through for it.  Warp-wide.
-template <typename T, int HD, int W, int KT>
-__device__ __forceinline__ void mend_row(const KeyRows<T>& keys, const RowView& r, const T* q, const RowOut<T>& o, int c0, float c) {
-  constexpr bool ALL = std::is_same_v<T, float>;
-  constexpr int NC = (W + 31) / 32;
+// Forms the row anew where it is not finite.  In bf16 the statistics stand (the tensor cores hold infinities as they are);
+// in fp32 they are formed anew too where they are not finite.  In the bf16 window form, rows that owe their state to a key
+// that they see are left without going through their keys, unless a hidden one of their tiles holds such values too.
+// Warp-wide.
+template <typename T, int HD, int KT>
+__device__ __forceinline__ void mend_row(const KeyRows<T>& keys, const RowView& r, const T* q, const RowOut<T>& o, float c) {
+  constexpr bool F32 = std::is_same_v<T, float>;
   const int lane = threadIdx.x & 31;
-  const float l0 = o.part != nullptr ? *o.l : *o.lse;
-  const bool empty = o.part != nullptr ? l0 == 0.f : l0 == kNegInf;
-  bool fine = empty || is_finite(l0);
-  if (!fine && !ALL) return;
-  bool done[NC];  // needs nothing, or NaN from a visible key
-  float acc[NC];
-#pragma unroll
-  for (int n = 0; n < NC; ++n) {
-    acc[n] = 0.f;
-    done[n] = lane + 32 * n >= W || is_finite(o.part != nullptr ? o.part[lane + 32 * n] : to_f32(o.out[lane + 32 * n]));
-    fine &= done[n];
-  }
-  if (__all_sync(0xffffffffu, fine)) return;
-  if (!ALL && keys.table == nullptr) {
-    bool hidden = false;
-    for (int j = r.first; j < r.last; ++j) {
-      const int u0 = r.kt.tile(j) * KT;
-      if (u0 + KT - 1 <= r.t && (r.t - u0 < r.window || u0 + KT <= r.sinks)) continue;
-      for (int u = u0 + lane; u < u0 + KT && u < r.N; u += 32)
-        if (!sees(r.t, u, r.window, r.sinks)) hidden |= spoiled<T, W>(keys.at(keys.v, u) + c0);
-    }
-    if (!__any_sync(0xffffffffu, hidden)) return;
-  }
-  // the row's maximum and sum
-  float m, mul = 1.f;
-  if (o.part != nullptr && !ALL) {
-    m = *o.m;
-  } else {
-    auto logit = [&](const T* k) { return dot_row<T, HD>(q, k) * c; };
+  float l = o.part != nullptr ? *o.l : *o.lse, m = o.part != nullptr ? *o.m : l * 1.4426950408889634f, mul = 1.f;
+  const bool known = is_finite(l) || (o.part == nullptr && l == kNegInf);
+  Columns<T, HD> h;
+  bool fine = h.look(o.out, o.part);
+  if (!known && !F32) return;
+  if (__all_sync(0xffffffffu, known && fine)) return;
+  // A NaN in the row's own value leaves nothing to form: inputs that are NaN throughout cost no pass over the keys.
+  if (known && __all_sync(0xffffffffu, h.spoiled_by(r.t >= 0 ? keys.at(keys.v, r.t) : nullptr))) return;
+  if (!F32 && keys.table == nullptr && !hidden_spoiled<T, HD, KT>(keys, keys.v, r)) return;
+  const RowPart<T, HD> part(q);
+  auto key = [&](int u) { return sees(r.t, u, r.window, r.sinks) ? keys.at(keys.k, u) : nullptr; };
+  // the logits of keys u0 .. u0 + 31 in base 2, -infinity where the row does not see them
+  auto logits = [&](int u0) {
+    const float x = part.dots([&](int i) { return key(u0 + i); }) * c;
+    return key(u0 + lane) != nullptr ? x : kNegInf;
+  };
+  if (!known) {
     m = kNegInf;
-    for_keys<T, KT>(keys, r, [&](int, const T* k) {
-      if (k != nullptr) m = fmaxf(m, logit(k));
-      return true;
+    bool nan = false;  // a visible logit is: the row's values all are, as they stand
+    for_keys<KT>(r, [&](int u0) {
+      const float x = logits(u0);
+      m = fmaxf(m, x);
+      nan = __any_sync(0xffffffffu, x != x);
+      return !nan;
     });
-    float l = 0.f;
+    if (nan) return;
 #pragma unroll
     for (int i = 16; i; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
     const float ref = m == kNegInf ? 0.f : m;
-    for_keys<T, KT>(keys, r, [&](int, const T* k) {
-      if (k != nullptr) l += exp2f(logit(k) - ref);
+    l = 0.f;
+    for_keys<KT>(r, [&](int u0) {
+      const float x = logits(u0);
+      if (key(u0 + lane) != nullptr) l += exp2f(x - ref);
       return true;
     });
 #pragma unroll
     for (int i = 16; i; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
     if (o.part == nullptr) mul = l == 0.f ? 0.f : 1.0f / l;
-    if (ALL && lane == 0) {
+    if (lane == 0) {
       if (o.part != nullptr) {
         *o.m = m;
         *o.l = l;
@@ -151,112 +269,38 @@ __device__ __forceinline__ void mend_row(const KeyRows<T>& keys, const RowView& 
         *o.lse = l == 0.f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
       }
     }
-    m = ref;
   }
-  bool write[NC];
-#pragma unroll
-  for (int n = 0; n < NC; ++n) {
-    if (ALL) done[n] = lane + 32 * n >= W;
-    write[n] = !done[n];
-  }
+  if (m == kNegInf) m = 0.f;
   // from the newest key on: where all is NaN, the first of them ends it
-  for_keys<T, KT>(keys, r, [&](int u0, const T* k) {
-    const float w = k != nullptr ? exp2f(dot_row<T, HD>(q, k) * c - m) * mul : 0.f;
-    for (unsigned rest = __ballot_sync(0xffffffffu, k != nullptr); rest; rest &= rest - 1) {
-      const int i = __ffs(rest) - 1;
-      const T* v = keys.at(keys.v, u0 + i) + c0;
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-#pragma unroll
-      for (int n = 0; n < NC; ++n)
-        if (!done[n]) acc[n] = fmaf(wi, to_f32(v[lane + 32 * n]), acc[n]);
-    }
-    bool all = true;
-#pragma unroll
-    for (int n = 0; n < NC; ++n) all &= (done[n] |= acc[n] != acc[n]);
-    return !__all_sync(0xffffffffu, all);
+  for_keys<KT>(r, [&](int u0) {
+    const float x = logits(u0);
+    const unsigned bits = __ballot_sync(0xffffffffu, key(u0 + lane) != nullptr);
+    h.add(bits, exp2f(x - m) * mul, [&](int i) { return keys.at(keys.v, u0 + i); });
+    return !__all_sync(0xffffffffu, h.settled());
   });
-#pragma unroll
-  for (int n = 0; n < NC; ++n)
-    if (write[n]) {
-      if (o.part != nullptr) o.part[lane + 32 * n] = acc[n];
-      else o.out[lane + 32 * n] = from_f32<T>(acc[n]);
-    }
+  h.store(1.f);
 }
 
 // ---------------------------------------------------------------- gradients
-// W columns of a gradient's row: which are not finite, and their sums over the visible pairs.
-template <typename T, int W>
-struct Columns {
-  static constexpr int NC = (W + 31) / 32;
-  float acc[NC];
-  bool write[NC], done[NC];  // done: needs nothing, or NaN from a visible pair
-  T* out;
-  float* part;  // fp32 partials; one of the two is null
-  // Both begin at the first column.  Returns whether the lane's columns are all finite.
-  __device__ __forceinline__ bool look(T* out_, float* part_) {
-    out = out_;
-    part = part_;
-    bool fine = true;
-#pragma unroll
-    for (int n = 0; n < NC; ++n) {
-      const int c = (threadIdx.x & 31) + 32 * n;
-      acc[n] = 0.f;
-      done[n] = c >= W || is_finite(part != nullptr ? part[c] : to_f32(out[c]));
-      write[n] = !done[n];
-      fine &= done[n];
-    }
-    return fine;
-  }
-  __device__ __forceinline__ void add(float w, const T* x) {
-#pragma unroll
-    for (int n = 0; n < NC; ++n)
-      if (!done[n]) acc[n] = fmaf(w, to_f32(x[(threadIdx.x & 31) + 32 * n]), acc[n]);
-  }
-  // Whether nothing is left to add in this lane.
-  __device__ __forceinline__ bool settled() {
-    bool all = true;
-#pragma unroll
-    for (int n = 0; n < NC; ++n) all &= (done[n] |= acc[n] != acc[n]);
-    return all;
-  }
-  __device__ __forceinline__ void store(float mul) {
-#pragma unroll
-    for (int n = 0; n < NC; ++n)
-      if (write[n]) {
-        const int c = (threadIdx.x & 31) + 32 * n;
-        if (part != nullptr) part[c] = acc[n];
-        else out[c] = from_f32<T>(acc[n] * mul);
-      }
-  }
-};
-
-// Columns c0 .. c0 + W - 1 of a query's dQ, where they are not finite:
+// A query's dQ, where it is not finite:
 //   scale sum_u p (g . v_u + nd) k_u, p = 2^(c q . k_u + nl),
-// over the keys u that it sees (nl: -lse in base 2, nd: -D).  q, g begin at the row, out at c0.  As above, the bf16 form
-// goes through the row's keys only where a hidden one holds such values.  Warp-wide.
-template <typename T, int HD, int W, int KT>
-__device__ __forceinline__ void mend_dq_row(const KeyRows<T>& keys, const RowView& r, const T* q, const T* g, T* out, int c0, float c,
+// over the keys u that it sees (nl: -lse in base 2, nd: -D).  As above, the bf16 form goes through the row's keys
+// only where a hidden one holds such values.  Warp-wide.
+template <typename T, int HD, int KT>
+__device__ __forceinline__ void mend_dq_row(const KeyRows<T>& keys, const RowView& r, const T* q, const T* g, T* out, float c,
                                             float nl, float nd, float scale) {
   const int lane = threadIdx.x & 31;
-  Columns<T, W> dq;
+  Columns<T, HD> dq;
   // with a NaN in either statistic all of the row's weights are NaN
   if (__all_sync(0xffffffffu, dq.look(out, nullptr)) || nl != nl || nd != nd) return;
-  if (!std::is_same_v<T, float>) {
-    bool hidden = false;
-    for (int j = r.first; j < r.last; ++j) {
-      const int u0 = r.kt.tile(j) * KT;
-      if (u0 + KT - 1 <= r.t && (r.t - u0 < r.window || u0 + KT <= r.sinks)) continue;
-      for (int u = u0 + lane; u < u0 + KT && u < r.N; u += 32)
-        if (!sees(r.t, u, r.window, r.sinks)) hidden |= spoiled<T, W>(keys.at(keys.k, u) + c0);
-    }
-    if (!__any_sync(0xffffffffu, hidden)) return;
-  }
-  for_keys<T, KT>(keys, r, [&](int u0, const T* k) {
-    const float w = k != nullptr ? exp2f(fmaf(dot_row<T, HD>(q, k), c, nl)) * (dot_row<T, HD>(g, keys.at(keys.v, u0 + lane)) + nd) : 0.f;
-    for (unsigned rest = __ballot_sync(0xffffffffu, k != nullptr); rest; rest &= rest - 1) {
-      const int i = __ffs(rest) - 1;
-      dq.add(__shfl_sync(0xffffffffu, w, i), keys.at(keys.k, u0 + i) + c0);
-    }
+  if (!std::is_same_v<T, float> && !hidden_spoiled<T, HD, KT>(keys, keys.k, r)) return;
+  const RowPart<T, HD> pq(q), pg(g);
+  auto of = [&](const TensorRef& x, int u) { return sees(r.t, u, r.window, r.sinks) ? keys.at(x, u) : nullptr; };
+  for_keys<KT>(r, [&](int u0) {
+    const float x = pq.dots([&](int i) { return of(keys.k, u0 + i); });
+    const float dp = pg.dots([&](int i) { return of(keys.v, u0 + i); });
+    const unsigned bits = __ballot_sync(0xffffffffu, sees(r.t, u0 + lane, r.window, r.sinks));
+    dq.add(bits, exp2f(fmaf(x, c, nl)) * (dp + nd), [&](int i) { return keys.at(keys.k, u0 + i); });
     return !__all_sync(0xffffffffu, dq.settled());
   });
   dq.store(scale);
@@ -269,13 +313,16 @@ struct QueryView {
   int b, Hq, h0, kt, nq, first, last, N, Npad, window, sinks;
 };
 
-// Columns c0 .. c0 + W - 1 of key u's dK and dV over those steps, where they are not finite:
+// Key u's dK and dV over those steps, where they are not finite:
 //   scale sum_t p (g_t . v + nd_t) q_t and sum_t p g_t over the queries t that see u.
-// k, v begin at the row; dk and dv look at their columns already.
-template <typename T, int HD, int W, int QT>
-__device__ __forceinline__ void mend_dkv_row(const QueryView& r, int u, const T* k, const T* v, Columns<T, W>& dk, Columns<T, W>& dv,
-                                             int c0, float c, float scale) {
+// Warp-wide.
+template <typename T, int HD, int QT>
+__device__ __forceinline__ void mend_dkv_row(const QueryView& r, int u, const T* k, const T* v, T* dk_out, T* dv_out, float* dk_part,
+                                             float* dv_part, float c, float scale) {
   const int lane = threadIdx.x & 31;
+  Columns<T, HD> dk, dv;
+  const bool a = dk.look(dk_out, dk_part), b = dv.look(dv_out, dv_part);
+  if (__all_sync(0xffffffffu, a && b)) return;
   // f(h, t0) for each 32 queries until it returns false
   auto for_queries = [&](auto f) {
     for (int s = r.first; s < r.last; ++s)
@@ -286,32 +333,55 @@ __device__ __forceinline__ void mend_dkv_row(const QueryView& r, int u, const T*
       }
   };
   auto at = [&](const TensorRef& x, int h, int t) { return row_ptr<T>(x, r.b, h, t); };
-  if (!std::is_same_v<T, float>) {
-    bool hidden = false;
+  auto seen = [&](int t) { return t < r.N && sees(t, u, r.window, r.sinks); };
+  // A row of Q or g that is not finite shows in its query's statistics: f(h, t0, bits, nl, nd) for those of each 32 queries.
+  auto for_bad = [&](bool visible, auto f) {
     for_queries([&](int h, int t0) {
-      const int t = t0 + lane;
-      if (t < r.N && !sees(t, u, r.window, r.sinks))
-        hidden |= spoiled<T, W>(at(r.q, h, t) + c0) || spoiled<T, W>(at(r.g, h, t) + c0);
-      return !__any_sync(0xffffffffu, hidden);
+      const int64_t o = ((int64_t)r.b * r.Hq + h) * r.Npad + t0 + lane;  // rows up to Npad, a multiple of 128
+      const float nl = r.nl[o], nd = r.nd[o];
+      const bool bad = t0 + lane < r.N && !(is_finite(nl) && is_finite(nd)) && seen(t0 + lane) == visible;
+      const unsigned bits = __ballot_sync(0xffffffffu, bad);
+      return bits == 0 || f(h, t0, bits, nl, nd);
     });
-    if (!__any_sync(0xffffffffu, hidden)) return;
-  }
+  };
+  auto open = [](Columns<T, HD>& x) {
+    const bool e = x.settled();
+    return !__all_sync(0xffffffffu, e);
+  };
+  // A visible one with a NaN settles columns without a product.
+  for_bad(true, [&](int h, int t0, unsigned bits, float nl, float nd) {
+    for (; bits; bits &= bits - 1) {
+      const int i = __ffs(bits) - 1;
+      const float l = __shfl_sync(0xffffffffu, nl, i), d = __shfl_sync(0xffffffffu, nd, i);
+      if (l != l || d != d) dk.meet(nullptr);
+      dv.meet(l != l ? nullptr : at(r.g, h, t0 + i));
+    }
+    const bool e = open(dk), f = open(dv);
+    return e || f;
+  });
+  bool need_k = open(dk), need_v = open(dv);
+  if (!need_k && !need_v) return;
+  // In bf16 the queries are gone through only where a hidden one holds such values.
+  bool hidden = std::is_same_v<T, float>;
+  if (!hidden)
+    for_bad(false, [&](int h, int t0, unsigned bits, float, float) {
+      auto of = [&](const TensorRef& x) { return [&, x, h, t0, bits](int i) { return bits >> i & 1u ? at(x, h, t0 + i) : nullptr; }; };
+      hidden = spoiled<T, HD>(of(r.q)) || spoiled<T, HD>(of(r.g));
+      return !hidden;
+    });
+  if (!hidden) return;
+  const RowPart<T, HD> pk(k), pv(v);
   for_queries([&](int h, int t0) {
-    const int t = t0 + lane;
-    const bool see = t < r.N && sees(t, u, r.window, r.sinks);
-    float p = 0.f, dx = 0.f;
-    if (see) {
-      const int64_t o = ((int64_t)r.b * r.Hq + h) * r.Npad + t;
-      p = exp2f(fmaf(dot_row<T, HD>(at(r.q, h, t), k), c, r.nl[o]));
-      dx = p * (dot_row<T, HD>(at(r.g, h, t), v) + r.nd[o]);
-    }
-    for (unsigned rest = __ballot_sync(0xffffffffu, see); rest; rest &= rest - 1) {
-      const int i = __ffs(rest) - 1;
-      dk.add(__shfl_sync(0xffffffffu, dx, i), at(r.q, h, t0 + i) + c0);
-      dv.add(__shfl_sync(0xffffffffu, p, i), at(r.g, h, t0 + i) + c0);
-    }
-    const bool a = dk.settled(), b = dv.settled();
-    return !__all_sync(0xffffffffu, a && b);
+    const unsigned bits = __ballot_sync(0xffffffffu, seen(t0 + lane));
+    if (bits == 0) return true;
+    auto of = [&](const TensorRef& x) { return [&, x, h, t0](int i) { return seen(t0 + i) ? at(x, h, t0 + i) : nullptr; }; };
+    const int64_t o = ((int64_t)r.b * r.Hq + h) * r.Npad + t0 + lane;
+    const float p = exp2f(fmaf(pk.dots(of(r.q)), c, r.nl[o]));
+    if (need_k) dk.add(bits, p * (pv.dots(of(r.g)) + r.nd[o]), [&](int i) { return at(r.q, h, t0 + i); });
+    if (need_v) dv.add(bits, p, [&](int i) { return at(r.g, h, t0 + i); });
+    need_k = open(dk);
+    need_v = open(dv);
+    return need_k || need_v;
   });
   dk.store(scale);
   dv.store(1.f);
