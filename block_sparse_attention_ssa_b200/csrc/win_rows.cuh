@@ -114,10 +114,10 @@ struct Columns {
         done[n] = true;
       }
   }
-  // acc += w_i row(i) for the set bits i; w: lane i's weight.  Returns whether nothing is left to add in any lane.
+  // acc += w_i row(i) for the set bits i; w: lane i's weight.  (Unrolled by eight, the kernels spilled.)
   template <typename F>
   __device__ __forceinline__ void add(unsigned bits, float w, F row) {
-#pragma unroll 8
+#pragma unroll 4
     for (int i = 0; i < 32; ++i) {
       const float wi = __shfl_sync(0xffffffffu, w, i);
       if (!(bits >> i & 1u)) continue;

@@ -153,6 +153,8 @@ def test_window_backward(name, what, dtype):
 PAGED = {
     "chunks": (([70, 1, 129, 5], [500, 33, 129, 1111], 8, 2, 128, 16), [(0, 450), (0, 499), (2, 60), (3, 1107), (3, 300)]),
     "cut_chunk": (([300], [2400], 4, 1, 64, 64), [(0, 2150), (0, 2399), (0, 900)]),
+    # rows at negative positions beside rows that see NaN
+    "empty_rows": (([10, 5, 70], [4, 0, 66], 4, 2, 64, 16), [(0, 2), (0, 3), (2, 0), (2, 60)]),
     "tokens": (([1, 1, 4], [700, 900, 130], 8, 2, 64, 32), [(0, 650), (2, 127), (2, 129), (1, 5)]),
 }
 
