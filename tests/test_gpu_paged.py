@@ -440,3 +440,40 @@ def test_large_logits(name, dtype, wave):
             rows.copy_((rows.float().abs() * part[:, None, None]).to(TYPES[dtype]))
     for window, sinks in ((None, 0), (400, 20)):
         b.check(b.attend(window, sinks), window, sinks)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_lengths_out_of_range_are_clamped(dtype):
+    """kv_len below 0 and past the table's positions: the append writes and the attention reads what the clamped
+    lengths say, and every other cache row keeps its value."""
+    Hq, Hkv, d, page, cols, new = 4, 2, 64, 16, 3, [5, 7, 3, 2, 60]
+    S, T, gen = len(new), sum(new), torch.Generator().manual_seed(12)
+    lens = [100, 2**31 - 1, -5, -2**31, cols * page + 1]
+    q_start = np.concatenate([[0], np.cumsum(new)])
+    pool = S * cols + 2
+    table = torch.randperm(pool, generator=gen)[:S * cols].view(S, cols).int()
+    mk = lambda *s: torch.randn(*s, generator=gen).to(TYPES[dtype])  # noqa: E731
+    q, k, v, caches = mk(T, Hq, d), mk(T, Hkv, d), mk(T, Hkv, d), [mk(pool, page, Hkv, d) for _ in range(2)]
+    L = [min(max(n, 0), cols * page) for n in lens]
+    want = [c.clone() for c in caches]
+    for b in range(S):
+        for i in range(new[b]):
+            u = L[b] - new[b] + i
+            if u >= 0:
+                for c, x in zip(want, (k, v)):
+                    c[table[b, u // page], u % page] = x[q_start[b] + i]
+    dims = api.make_paged_dims(S, T, Hq, Hkv, d, page, pool, cols, dtype=dtype)
+    ints = [torch.tensor(np.array(x), dtype=torch.int32, device="cuda") for x in (q_start, lens)] + [table.cuda()]
+    got = [c.cuda() for c in caches]
+    api.ssa_paged_append(dims, k.cuda(), v.cuda(), *ints, *got)
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert torch.equal(g.cpu(), w)
+    out = {n: torch.full_like(x, 5.0) for n, x in api.alloc_paged(dims).items()}
+    api.ssa_paged_attention(dims, q.cuda(), *got, *ints, out["h"], out["lse"], api.alloc_paged_workspace(dims).fill_(255))
+    torch.cuda.synchronize()
+    assert api.ssa_device_status() == api.SSA_OK
+    r = W.paged(q.double().numpy(), *(c.double().numpy() for c in want), q_start, L, table.numpy(), page, api.EVERYTHING, 0,
+                1 / math.sqrt(d), dtype)
+    within("h", f64(out["h"]), r["h"], r["tol_h"])
+    within("lse", f64(out["lse"]), r["lse"], r["tol_lse"])
