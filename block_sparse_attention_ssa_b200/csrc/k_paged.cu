@@ -10,8 +10,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 // Append: one pass over the new rows in 16-byte pieces.  A CTA takes ROWS packed tokens
 // (all kv heads); a warp finds a token's sequence and page row, then the CTA copies.  Bound by
-// memory (or by the launch, for single tokens): 4 row lengths of traffic a token and head; 16384
-// tokens of 8 heads, d = 128, bf16 (90 MB) take 16.1 us, 5.6 TB/s.
+// memory (or by the launch, for single tokens): 4 row lengths of traffic a token and head; 11008
+// tokens of 8 sequences, 8 heads, d = 128, bf16 (90 MB) take 16.7 us, 5.4 TB/s.
 constexpr int AROWS = 8;
 __global__ void __launch_bounds__(256) paged_append_kernel(PagedArgs a, PagedDims D, int vecs, int es) {
   __shared__ int64_t page_of[AROWS];

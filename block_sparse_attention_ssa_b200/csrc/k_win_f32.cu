@@ -10,9 +10,9 @@
 // be.  On the FMA pipe the same tiles were bound by shared memory (a 4 x 4 thread tile reads
 // twice what the pipe can take): 178 against 142 us for a training
 // step of 8 heads, 1000 tokens, d = 128, window 128.
-// Measured, that step: forward 32 us, dK and dV 66 (288 chunks, two waves of CTAs), dQ 38; chunks of 301 tokens over
-// 3001 more, 5 sequences, 8 heads over 2, d = 64, window 1000: 88 us.  Bound by latency: the backward's eight warps an SM
-// issue in 27 to 39 % of the cycles (waits for the instruction before, barriers between warps that see unequal
+// Measured, that step: forward 33 us, dK and dV 66 (288 chunks, two waves of CTAs), dQ 38; chunks of 120 to 301
+// tokens (1051 in all) over 1200 to 3001 more, 5 sequences, 8 heads over 2, d = 64, window 1000: 89 us.  Bound by latency:
+// the backward's eight warps an SM issue in 27 to 39 % of the cycles (waits for the instruction before, barriers between warps that see unequal
 // parts of a tile), the tensor pipe is busy 22 to 32 %, and the fullest SM of the step above forms 1.6 times the mean's products.
 // Twice the independent accumulators, or pieces twice as wide, changed nothing or spilled (134 against 134 to 144 us).
 //
@@ -546,8 +546,8 @@ struct F32Bwd {
   float c, scale;
 };
 
-// Two groups of four warps, up to 255 registers a thread: the accumulators of a warp's sixteen rows stay in them
-// (128 in dkv at d = 128), logits and dP are formed 32 columns at a time.
+// Two groups of four warps, up to 255 registers a thread, for the accumulators of a warp's sixteen rows (128 in dkv at
+// d = 128, where 312 bytes are spilled all the same; dq there 36); logits and dP are formed 32 columns at a time.
 constexpr int BWD_THREADS = 2 * GROUP;
 
 // dq: Q, g, then each group's K, V.  dkv: K, V, then each group's Q, g.

@@ -30,13 +30,16 @@
 // and a single token fills g rows; 128 / g tokens to a slot.  Paged items are cut into
 // equal shares of key tiles (win_common.cuh); cut items leave fp32 partials.
 //
-// Measured (bf16, 32 heads over 8, d = 128).  32768 tokens, window 1024, 64 sinks: 647 us, 890 TFLOP/s of visible pairs
-// (20 passes from idle; 760 in long runs).  Chunks of 2048 tokens over 14000 more, 4 sequences: 1085 us, 1040 TFLOP/s (1289).
+// Measured (bf16, 32 heads over 8, d = 128).  32768 tokens, window 1024, 64 sinks: 635 us, 905 TFLOP/s of visible pairs
+// (20 passes from idle; 748 in long runs).  Chunks of 896 to 2048 tokens (5888 in all) over 6125 to 14000 more, 4 sequences:
+// 1080 us, 1047 TFLOP/s (1260 in long runs).
 // Bound by the chain of a step, 3500 cycles for a tile of both slots: logits waited for 1100, loaded for their maximum 350,
-// maximum passed on 570, exponentials 1200, P stored 330; of these the tensor pipe is busy 2560 (45 % over
-// the kernel) and the exponentials' pipe 2048.  Between items 5500 cycles (sums, last product, output), which bounds
-// short windows: 8192 tokens, 32 heads over 2, d = 64, window 256: 76 us, 235 TFLOP/s.  One token of 64
-// sequences over 8000 each: 240 us, 5.5 TB/s, bound by memory.
+// maximum passed on 570, exponentials 1200 (2048 of their pipe's cycles for both slots), P stored 330.  Over the kernel the
+// tensor pipe is active 45 % of the time, the exponentials' pipe 46 % (16384 tokens, window 1024).  Between items
+// 5500 cycles (sums, last product, output), which bounds short windows: 8192 tokens, 32 heads over 2, d = 64, window 256:
+// 77 us, 233 TFLOP/s.  One token of 64 sequences over 2094 to 8001 (323040 in all, 1.32 GB): 239 us, 5.5 TB/s, bound by
+// memory.  The runs of a sequence are counted one by one (win_common.cuh): 32768 new tokens, 32 heads over 2, d = 64,
+// window 256, take 1203 us, as many tokens of the window form 279.
 #include "win_rows.cuh"
 
 #include "sm100_ptx.cuh"

@@ -406,7 +406,8 @@ SSA_API ssa_status_t ssa_fwd_window(const ssa_window_dims_t* dims, const ssa_ten
  *   dQ [B, Hq, N, d], dK, dV [B, Hkv, N, d] (out): fully overwritten.
  *   Pairs that are hidden do not count, NaN and infinities in their rows of
  *     Q, K, V, h, lse and g included.
- *   ws: at least ssa_window_workspace_bytes(dims) bytes, 256-byte aligned. */
+ *   ws: at least ssa_window_workspace_bytes(dims) bytes, 256-byte aligned; two
+ *     calls in flight at once must not share it. */
 SSA_API ssa_status_t ssa_bwd_window(const ssa_window_dims_t* dims, const ssa_tensor_t* Q, const ssa_tensor_t* K,
                                     const ssa_tensor_t* V, const ssa_tensor_t* h, const float* lse,
                                     const ssa_tensor_t* g, const ssa_tensor_t* dQ, const ssa_tensor_t* dK,
@@ -433,8 +434,8 @@ SSA_API ssa_status_t ssa_bwd_window(const ssa_window_dims_t* dims, const ssa_ten
  * entry below an earlier one ends a sequence without new tokens, and no row
  * belongs to two), kv_len to 0 .. max_pages * page, and a page id outside
  * 0 .. num_pages - 1 holds no keys (append skips it, attention masks its
- * positions).  Page ids that no
- * token sees (behind the window, past kv_len) are not looked at. */
+ * positions).  Page ids that no token sees (behind the window, past kv_len)
+ * do not matter. */
 typedef struct {
   int32_t num_seqs;  /* >= 0 */
   int32_t total_q;   /* rows of the packed tensors, 0 .. 2^30 */
@@ -455,8 +456,7 @@ SSA_API size_t ssa_paged_workspace_bytes(const ssa_paged_dims_t* dims);
 /* Writes the new tokens' keys and values into their pages.
  *   k, v: packed [1, Hkv, total_q, d] strided (in).
  *   K, V: the caches (in/out); only the new tokens' rows are written.
- * New tokens at negative positions and rows behind q_start[num_seqs] are
- * skipped.  Two new tokens that write the same page row race. */
+ * New tokens at negative positions and rows of no sequence are skipped.  Two new tokens that write the same page row race. */
 SSA_API ssa_status_t ssa_paged_append(const ssa_paged_dims_t* dims, const ssa_tensor_t* k, const ssa_tensor_t* v,
                                       const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table,
                                       const ssa_tensor_t* K, const ssa_tensor_t* V, ssa_stream_t stream);
@@ -465,7 +465,7 @@ SSA_API ssa_status_t ssa_paged_append(const ssa_paged_dims_t* dims, const ssa_te
  * sequence (decoding), chunks of a prompt, or both in one batch.  The cache
  * holds the new tokens' keys and values already (ssa_paged_append).
  *   q, h: packed [1, Hq, total_q, d] strided, no broadcast heads; lse [Hq, total_q] fp32, dense.
- *   Rows behind q_start[num_seqs] are left as they were.  A row that sees no
+ *   Rows of no sequence are left as they were.  A row that sees no
  *     key (a negative position, missing pages) gets h = 0, lse = -INFINITY.
  *   ws: at least ssa_paged_workspace_bytes(dims) bytes, 256-byte aligned; two
  *     calls in flight at once must not share it.
