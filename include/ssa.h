@@ -389,7 +389,8 @@ SSA_API size_t ssa_window_workspace_bytes(const ssa_window_dims_t* dims);
  *     [B, Hq, N] fp32, dense.  Inputs may broadcast batches and heads (stride 0);
  *     rows, and the slices of an output, may not lie over one another
  *     (SSA_ERR_INVALID_ARG; an output's dimensions have to nest: by growing
- *     stride, each steps over all that the smaller ones span).
+ *     stride, each steps over all that the smaller ones span).  Here and in the
+ *     calls below, outputs share no memory with inputs or with one another.
  *   What a hidden key holds does not matter, NaN and infinities included
  *     (a call whose rows meet some takes longer). */
 SSA_API ssa_status_t ssa_fwd_window(const ssa_window_dims_t* dims, const ssa_tensor_t* Q, const ssa_tensor_t* K,
