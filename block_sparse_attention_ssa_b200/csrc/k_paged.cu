@@ -8,49 +8,71 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 
+// The end entry of the sequence that holds packed row `row`, by halving: entries that do not fall.  0 for rows of no sequence.
+__device__ __forceinline__ int end_by_halves(const int32_t* q_start, int seqs, int row) {
+  int lo = 0, hi = seqs;  // q_start[lo] <= row < q_start[hi] once both ends hold
+  if (row < q_start[0] || row >= q_start[seqs]) return 0;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (q_start[mid] <= row) lo = mid; else hi = mid;
+  }
+  return hi;
+}
+
+// The same where entries fall, a warp a row: the first entry above the row ends its sequence, the largest one before it
+// begins it.
+__device__ __forceinline__ void search_row(const int32_t* q_start, int seqs, int T, int row, int* end_of, int* begin_of) {
+  const int lane = threadIdx.x & 31;
+  int end = row < T ? -1 : 0, begin = 0;  // end: -1 while not found
+  for (int i0 = 0; end < 0 && i0 <= seqs; i0 += 32) {
+    const int q = i0 + lane <= seqs ? clamp_row(q_start[i0 + lane], T) : -1;
+    const unsigned above = __ballot_sync(0xffffffffu, q > row);
+    if (above) end = i0 + __ffs(above) - 1;
+    begin = max(begin, __reduce_max_sync(0xffffffffu, q > row || (above && i0 + lane > end) ? -1 : q));
+  }
+  if (lane == 0) {
+    *end_of = max(end, 0);
+    *begin_of = begin;
+  }
+}
+
 // Append: one pass over the new rows in 16-byte pieces.  A CTA takes ROWS packed tokens
-// (all kv heads); a warp finds a token's sequence and page row, then the CTA copies.  Bound by
+// (all kv heads); a thread finds a token's page row once, then the CTA copies.  Bound by
 // memory (or by the launch, for single tokens): 4 row lengths of traffic a token and head; 11008
 // tokens of 8 sequences, 8 heads, d = 128, bf16 (90 MB) take 16.7 us, 5.4 TB/s.
+// Sequences are found by halving q_start, while the CTA looks whether an entry falls; only then all are gone through
+// (always so, one token of each of 4096 sequences took 35 us, this way 8.4).  The kernel wants its 30 registers: 58, with the
+// placement tried before and after the search, took 33 us for 25.5 (8 sequences of 2048 new tokens).
 constexpr int AROWS = 8;
 __global__ void __launch_bounds__(256) paged_append_kernel(PagedArgs a, PagedDims D, int vecs, int es) {
   __shared__ int64_t page_of[AROWS];
-  __shared__ int slot_of[AROWS];
-  const int row0 = blockIdx.x * AROWS, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  static_assert(AROWS == 8, "a row for each warp");
-  const int row = row0 + w;
-  // The first entry above the row ends its sequence, the largest one before it begins it (entries may fall: all are
-  // looked at, 256 in flight, each with the length of the sequence that it ends; -1 behind the last one).
-  constexpr int U = 8;
-  int end = row < D.T ? -1 : 0, begin = -1;  // end: the entry's number, -1 while not found
-  int last = 0, len = 0;                     // its value and length
-  for (int i0 = 0; end < 0 && i0 <= D.seqs; i0 += 32 * U) {
-    int q[U], n[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      if (i0 + 32 * k > D.seqs) break;
-      const int i = i0 + 32 * k + lane;
-      q[k] = i <= D.seqs ? clamp_row(a.q_start[i], D.T) : -1;
-      n[k] = i <= D.seqs && i > 0 ? a.kv_len[i - 1] : 0;
-    }
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      if (end >= 0 || i0 + 32 * k > D.seqs) break;
-      const unsigned above = __ballot_sync(0xffffffffu, q[k] > row);
-      const int f = above ? __ffs(above) - 1 : 32;
-      if (above) {
-        end = i0 + 32 * k + f;
-        last = __shfl_sync(0xffffffffu, q[k], f);
-        len = __shfl_sync(0xffffffffu, n[k], f);
-      }
-      begin = max(begin, __reduce_max_sync(0xffffffffu, lane < f ? q[k] : -1));
+  __shared__ int slot_of[AROWS], end_of[AROWS], begin_of[AROWS];
+  const int row0 = blockIdx.x * AROWS;
+  auto entry = [&](int i) { return clamp_row(a.q_start[i], D.T); };
+  bool falls = false;
+  if (D.seqs > 1)
+    for (int i = 1 + threadIdx.x; i <= D.seqs; i += 256) falls |= entry(i) < entry(i - 1);
+  int end = 0, begin = 0;  // of the thread's row: the entry that ends its sequence (0: none), the sequence's first row
+  if (threadIdx.x < AROWS && row0 + threadIdx.x < D.T) {
+    end = end_by_halves(a.q_start, D.seqs, row0 + threadIdx.x);
+    if (end > 0) begin = entry(end - 1);
+  }
+  if (D.seqs > 1 && __syncthreads_or(falls)) {
+    static_assert(AROWS == 8, "a row for each warp");
+    const int w = threadIdx.x >> 5;
+    search_row(a.q_start, D.seqs, D.T, row0 + w, &end_of[w], &begin_of[w]);
+    __syncthreads();
+    if (threadIdx.x < AROWS) {
+      end = end_of[threadIdx.x];
+      begin = begin_of[threadIdx.x];
     }
   }
-  if (lane == 0) {
+  if (threadIdx.x < AROWS) {
     int64_t pg = -1;
     int slot = 0;
     if (end > 0) {
-      const int pos = min(max(len, 0), D.max_pages * D.page) - (last - begin) + (row - begin);
+      const Seq s = load_seq(a.q_start, a.kv_len, end - 1, begin, D.T, D.max_pages * D.page);
+      const int pos = s.len - s.n + (row0 + (int)threadIdx.x - s.q0);
       if (pos >= 0) {
         const int id = a.table[(int64_t)(end - 1) * D.max_pages + pos / D.page];
         if ((unsigned)id < (unsigned)D.num_pages) {
@@ -59,8 +81,8 @@ __global__ void __launch_bounds__(256) paged_append_kernel(PagedArgs a, PagedDim
         }
       }
     }
-    page_of[w] = pg;
-    slot_of[w] = slot;
+    page_of[threadIdx.x] = pg;
+    slot_of[threadIdx.x] = slot;
   }
   __syncthreads();
   const int per_row = D.Hkv * vecs;
