@@ -114,12 +114,13 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, Batch batc
   };
   __shared__ Cut sh;
   if (threadIdx.x < 32) {
-    const long long U = batch.total<KT>();
+    bool falls;
+    const long long U = batch.total<KT>(falls);
     const long long per = share(U, ctas);
     const long long u0 = per * blockIdx.x, u1 = min(u0 + per, U);
     Cut cut{};
     if (u0 < U) {
-      const Place at = batch.locate<KT>(u1 - 1);
+      const Place at = batch.locate<KT>(u1 - 1, falls);
       const long long begin = u1 - 1 - at.off;
       cut.s = load_seq(batch.q_start, batch.kv_len, at.b, at.q0, T_, batch.cap);
       cut.i0 = at.run * batch.TI;

@@ -298,11 +298,12 @@ __global__ void __launch_bounds__(Fwd<HD>::THREADS, 1) win_fwd_f32_kernel(F32Par
   bool again = false;  // rows that are not finite were stored (a store to shared memory there held up the next row: 97 us for 92)
   if (PAGED) {
     if (threadIdx.x < 32) {
-      const long long U = p.batch.total<BT>();
+      bool falls;
+      const long long U = p.batch.total<BT>(falls);
       const long long per = share(U, (int)gridDim.x);
       const long long u0 = per * blockIdx.x;
       const long long n = u0 < U ? min(per, U - u0) : 0;
-      if (n > 0) at = p.batch.locate<BT>(u0);
+      if (n > 0) at = p.batch.locate<BT>(u0, falls);
       if (threadIdx.x == 0) {
         sh_place = at;
         sh_left = (int)n;

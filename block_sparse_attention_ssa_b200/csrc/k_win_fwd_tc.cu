@@ -302,12 +302,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tmem_relinquish();
   }
   if (PAGED && warp == 0) {
-    const long long U = p.batch.total<TILE>();
+    bool falls;
+    const long long U = p.batch.total<TILE>(falls);
     const long long per = share(U, (int)gridDim.x);
     const long long u0 = per * blockIdx.x;
     const long long n = u0 < U ? (U - u0 < per ? U - u0 : per) : 0;
     Place at{p.batch.seqs, 0, 0, 0, 0};
-    if (n > 0) at = p.batch.locate<TILE>(u0);
+    if (n > 0) at = p.batch.locate<TILE>(u0, falls);
     if (lane == 0) {
       M.at = at;
       M.left = (int)n;

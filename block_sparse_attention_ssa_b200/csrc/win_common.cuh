@@ -156,9 +156,9 @@ struct Batch {
   const int32_t* kv_len;
   int seqs, T, cap, TI, window, sinks, Hkv;
 
-  // Lane i's sequence b0 + i (none behind the last one).  `top`: -1 while no entry has fallen (each one is then its own
-  // maximum), from then on the maximum before b0 + 32.
-  __device__ __forceinline__ Seq lane_seq(int b0, int& top) const {
+  // Lane i's sequence b0 + i (none behind the last one).  Where no entry falls each one is its own maximum; else `top` is the
+  // maximum before b0 (-1 at first), then before b0 + 32.
+  __device__ __forceinline__ Seq lane_seq(int b0, bool falls, int& top) const {
     const int lane = threadIdx.x & 31, b = b0 + lane;
     int a = 0, e = 0, len = 0;
     if (b < seqs) {
@@ -166,7 +166,7 @@ struct Batch {
       e = clamp_row(q_start[b + 1], T);
       len = min(max(kv_len[b], 0), cap);
     }
-    if (top >= 0 || __any_sync(0xffffffffu, e < a)) {
+    if (falls) {
       if (top < 0) top = __shfl_sync(0xffffffffu, a, 0);
 #pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) e = max(e, __shfl_up_sync(0xffffffffu, e, o));
@@ -181,9 +181,11 @@ struct Batch {
 
   // The first sequence from b on that has new tokens (seqs: none); q0: the rows before b.  Not warp-wide.  Entries are
   // read eight at a time: one at a time a thousand sequences without tokens, as idle slots of a captured batch are,
-  // took 50 us (four tokens over 600 before 1000 of them 30 us, once 94; 4000: 77, once 341; around 4000: 164, once 339).
+  // took 50 us (four tokens over 600 before 1000 of them 29 us, once 94; 4000: 71, once 341; around 4000: 153, once 339).
   __device__ __forceinline__ int next_seq(int b, int q0) const {
-    for (; b < seqs; b += 8) {
+    if (b < seqs && clamp_row(q_start[b + 1], T) > q0) return b;
+#pragma unroll 1
+    for (++b; b < seqs; b += 8) {
       int e[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) e[k] = b + k < seqs ? clamp_row(q_start[b + k + 1], T) : 0;
@@ -199,11 +201,23 @@ struct Batch {
     return s.n > 0 ? seq_units<KT>(s, TI, window, sinks) * Hkv : 0;
   }
 
+  // All units; whether an entry of q_start falls below the one before it.
   template <int KT>
-  __device__ long long total() const {
+  __device__ long long total(bool& falls) const {
     long long u = 0;
-    int top = -1;
-    for (int b0 = 0; b0 < seqs; b0 += 32) u += units_of<KT>(lane_seq(b0, top));
+    falls = false;
+    for (;;) {
+      int top = -1;
+      bool down = false;
+      u = 0;
+      for (int b0 = 0; b0 < seqs; b0 += 32) {
+        const Seq s = lane_seq(b0, falls, top);
+        down |= s.n < 0;
+        u += units_of<KT>(s);
+      }
+      if (falls || !__any_sync(0xffffffffu, down)) break;
+      falls = true;
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
     return u;
@@ -211,13 +225,13 @@ struct Batch {
 
   // The item and offset of unit `at` (0 <= at < total).
   template <int KT>
-  __device__ Place locate(long long at) const {
+  __device__ Place locate(long long at, bool falls) const {
     const int lane = threadIdx.x & 31;
     long long before = 0;
     int top = -1;
     Place p{seqs, 0, 0, 0, 0};
     for (int b0 = 0; b0 < seqs; b0 += 32) {
-      const Seq own = lane_seq(b0, top);
+      const Seq own = lane_seq(b0, falls, top);
       const long long mine = units_of<KT>(own);
       long long incl = mine;
 #pragma unroll
