@@ -248,7 +248,7 @@ __device__ __forceinline__ bool next_item(const F32Params& p, Place& at, int& le
     if (++at.run * p.batch.TI >= s.n) {
       at.run = 0;
       at.q0 += s.n;
-      at.b = p.batch.next_seq(at.b + 1, at.q0);
+      at.b = p.batch.next_seq<8>(at.b + 1, at.q0);
     }
   }
   return at.b < p.batch.seqs;

@@ -201,7 +201,7 @@ struct Walk {
         if (++at.run * p.batch.TI >= seq_n) {
           at.run = 0;
           at.q0 += seq_n;
-          at.b = p.batch.next_seq(at.b + 1, at.q0);
+          at.b = p.batch.next_seq<1>(at.b + 1, at.q0);
         }
       }
     }

@@ -179,18 +179,19 @@ struct Batch {
     return Seq{a, e - a, len};
   }
 
-  // The first sequence from b on that has new tokens (seqs: none); q0: the rows before b.  Not warp-wide.  Entries are
-  // read eight at a time: one at a time a thousand sequences without tokens, as idle slots of a captured batch are,
-  // took 50 us (four tokens over 600 before 1000 of them 29 us, once 94; 4000: 71, once 341; around 4000: 153, once 339).
+  // The first sequence from b on that has new tokens (seqs: none); q0: the rows before b.  Not warp-wide: called where a share
+  // goes on in another sequence, and only there (a CTA that walked on behind its share took 50 us for a thousand idle
+  // sequences: four tokens over 600 before 1000 of them 28 us, once 94; 4000: 71, once 341; around 4000: 153, once 339).
+  // AT entries a step: eight in fp32 (around 4000: 222 us, one at a time 323), one in bf16, where eight saved nothing there
+  // and cost registers (64 single tokens over 5048: 237 us, with eight 241).
+  template <int AT>
   __device__ __forceinline__ int next_seq(int b, int q0) const {
-    if (b < seqs && clamp_row(q_start[b + 1], T) > q0) return b;
-#pragma unroll 1
-    for (++b; b < seqs; b += 8) {
-      int e[8];
+    for (; b < seqs; b += AT) {
+      int e[AT];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) e[k] = b + k < seqs ? clamp_row(q_start[b + k + 1], T) : 0;
+      for (int k = 0; k < AT; ++k) e[k] = b + k < seqs ? clamp_row(q_start[b + k + 1], T) : 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
+      for (int k = 0; k < AT; ++k)
         if (e[k] > q0) return b + k;
     }
     return seqs;
