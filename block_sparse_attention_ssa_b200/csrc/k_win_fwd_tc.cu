@@ -31,8 +31,8 @@
 // equal shares of key tiles (win_common.cuh); cut items leave fp32 partials.
 //
 // Measured (bf16, 32 heads over 8, d = 128).  32768 tokens, window 1024, 64 sinks: 635 us, 905 TFLOP/s of visible pairs
-// (20 passes from idle; 748 in long runs).  Chunks of 896 to 2048 tokens (5888 in all) over 6125 to 14000 more, 4 sequences:
-// 1080 us, 1047 TFLOP/s (1260 in long runs).
+// (20 passes from idle; 736 in long runs).  Chunks of 896 to 2048 tokens (5888 in all) over 6125 to 14000 more, 4 sequences:
+// 1075 us, 1051 TFLOP/s (1233 in long runs).
 // Bound by the chain of a step, 3500 cycles for a tile of both slots: logits waited for 1100, loaded for their maximum 350,
 // maximum passed on 570, exponentials 1200 (2048 of their pipe's cycles for both slots), P stored 330.  Over the kernel the
 // tensor pipe is active 45 % of the time, the exponentials' pipe 46 % (16384 tokens, window 1024).  Between items
